@@ -15,3 +15,12 @@ from .api import (  # noqa: F401
     quantize_rowcol,
     quantize_4over6,
 )
+from .layer import (  # noqa: F401
+    add_rms_norm,
+    add_rms_norm_backward,
+    grouped_matmul,
+    grouped_wgrad,
+    matvec,
+    swiglu_backward,
+    swiglu_checkpoint,
+)

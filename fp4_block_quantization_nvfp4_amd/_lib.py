@@ -16,6 +16,7 @@ F32, BF16 = 0, 1
 RTN, SR = 0, 1
 MAE, MSE = 0, 1
 SCALE_NONE, SCALE_TENSOR, SCALE_ROW = 0, 1, 2
+BLOCK_1X16, BLOCK_16X16, BLOCK_16X16_T = 0, 1, 2
 
 _c = ctypes
 _vp, _i64, _u32, _i32, _f32, _sz = _c.c_void_p, _c.c_int64, _c.c_uint32, _c.c_int, _c.c_float, _c.c_size_t
@@ -33,6 +34,15 @@ SIGNATURES = {
     "nvfp4_quantize_2d": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _u32, _u32, _i32, _vp, _vp, _vp, _vp]),
     "nvfp4_quantize_rowcol": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp]),
     "nvfp4_quantize_4over6_2d": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _f32, _vp, _vp, _vp, _vp]),
+    "nvfp4_add_rms_norm": (_i32, [_vp, _vp, _i32, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_add_rms_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_add_rms_norm_backward": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_swiglu": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_swiglu_backward": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "nvfp4_matvec": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _i32, _f32, _vp, _i32, _vp]),
+    "nvfp4_grouped_matmul": (_i32, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _f32, _vp,
+                                    _i32, _vp]),
+    "nvfp4_grouped_wgrad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp]),
     "nvfp4_selftest_scan": (_i32, [_i32, _u32, _c.c_uint64, _c.c_uint64, _i32, _vp, _vp]),
     "nvfp4_selftest_launch_plan": (_i32, [_i32, _i64, _i64, _i32, _i32, _vp]),
 }

@@ -1,0 +1,227 @@
+// Root-mean-square norm of x + residual with 8-bit output, and its gradient.
+//
+//   h = x + r,  rstd = (mean_j h_j^2 + eps)^(-1/2),  y_j = h_j rstd w_j
+//   forward writes y as mx8 (codes, scales), h in x's type and rstd
+//   n = h rstd,  d = dy w,  dh = rstd (d - n mean_j(d_j n_j)) + dhidden,
+//   dw_j = sum over rows of dy_j n_j
+//
+// Both directions are bound by memory: every tensor is read once and written
+// once, the row stays in registers between its sum and its output.  A lane
+// holds 16 elements (half an mx8 group, so a group's maximum is one
+// cross-lane step) of one row, two such chunks for rows over 16384.
+#include "nvfp4_launch.hpp"
+#include "nvfp4_mx8.hpp"
+#include "nvfp4_plan.hpp"
+
+namespace nvfp4 {
+
+template <typename T, int C, bool RES>
+__global__ __launch_bounds__(1024) void k_add_rms_norm(const T* __restrict__ x, const T* __restrict__ res,
+                                                       const float* __restrict__ weight, int64_t rows, int H,
+                                                       float eps, uint8_t* __restrict__ codes,
+                                                       uint8_t* __restrict__ scales, T* __restrict__ hidden,
+                                                       float* __restrict__ rstd_out) {
+  __shared__ float lds[16];
+  const int nt = blockDim.x, ns = (H + kMxGroup - 1) / kMxGroup;
+  const float inv_h = 1.0f / (float)H;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t at = row * H;
+    float h[C][16];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * nt + threadIdx.x) * 16;
+      if (j < H) {
+        load16(x + at + j, h[c]);
+        if (RES) {
+          float r[16];
+          load16(res + at + j, r);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[c][i] += r[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[c][i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+    }
+    sum = block_sum(sum, lds);
+    const float rstd = 1.0f / __builtin_sqrtf(sum * inv_h + eps);
+    if (threadIdx.x == 0) rstd_out[row] = rstd;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * nt + threadIdx.x) * 16;
+      const bool in = j < H;
+      float w[16], y[16];
+      if (in) {
+        if (RES) store16(hidden + at + j, h[c]);
+        load16(weight + j, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = h[c][i] * rstd * w[i];
+      if (!in) {  // a missing half group counts as zeros, also where rstd is not finite
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+      }
+      nv_u4 q;
+      const uint32_t byte = mx8_encode16(y, q);
+      if (in) {
+        *reinterpret_cast<nv_u4*>(codes + at + j) = q;
+        if (j % kMxGroup == 0) scales[row * ns + j / kMxGroup] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+// A workgroup takes every gridDim-th row, keeps its share of dw in registers
+// and leaves one partial row of dw.
+template <typename T, int C, bool DH>
+__global__ __launch_bounds__(1024) void k_add_rms_norm_bwd(const T* __restrict__ dy, const T* __restrict__ hidden,
+                                                           const T* __restrict__ dhidden,
+                                                           const float* __restrict__ weight,
+                                                           const float* __restrict__ rstd_in, int64_t rows, int H,
+                                                           T* __restrict__ dx, float* __restrict__ partial) {
+  __shared__ float lds[16];
+  const int nt = blockDim.x;
+  const float inv_h = 1.0f / (float)H;
+  float dw[C][16];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dw[c][i] = 0.0f;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t at = row * H;
+    const float rstd = rstd_in[row];
+    float d[C][16], n[C][16], dh[C][16];
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * nt + threadIdx.x) * 16;
+      if (j < H) {
+        float w[16];
+        load16(dy + at + j, d[c]);
+        load16(hidden + at + j, n[c]);
+        if (DH) load16(dhidden + at + j, dh[c]);
+        load16(weight + j, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          n[c][i] *= rstd;
+          dw[c][i] = __builtin_fmaf(d[c][i], n[c][i], dw[c][i]);
+          d[c][i] *= w[i];
+          dot = __builtin_fmaf(d[c][i], n[c][i], dot);
+        }
+      }
+    }
+    const float mean = block_sum(dot, lds) * inv_h;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * nt + threadIdx.x) * 16;
+      if (j < H) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float v = rstd * (d[c][i] - n[c][i] * mean);
+          d[c][i] = DH ? v + dh[c][i] : v;
+        }
+        store16(dx + at + j, d[c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int j = (c * nt + threadIdx.x) * 16;
+    if (j < H) store16(partial + (int64_t)blockIdx.x * H + j, dw[c]);
+  }
+}
+
+// dw = sum of the partial rows in a fixed order: 16 lanes cover 64 columns,
+// the 16 lane groups of the workgroup take every 16th row.
+__global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ partial, int n, int H,
+                                                  float* __restrict__ out) {
+  __shared__ float lds[16][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 15) * 4, grp = threadIdx.x >> 4;
+  nv_f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < H)
+#pragma unroll 4
+    for (int r = grp; r < n; r += 16) {
+      const nv_f4 v = *reinterpret_cast<const nv_f4*>(partial + (int64_t)r * H + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += v[i];
+    }
+  *reinterpret_cast<nv_f4*>(&lds[grp][(threadIdx.x & 15) * 4]) = s;
+  __syncthreads();
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && c < H) {
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) t += lds[g][threadIdx.x];
+    out[c] = t;
+  }
+}
+
+template <typename T>
+static void norm_fwd(const T* x, const T* res, const float* w, int64_t rows, int H, float eps, uint8_t* codes,
+                     uint8_t* scales, T* hidden, float* rstd, hipStream_t st) {
+  const int nt = norm_threads(H);
+  const dim3 grid((uint32_t)(rows < kNormMaxGrid ? rows : kNormMaxGrid));
+#define NV_NORM(C, RES) k_add_rms_norm<T, C, RES><<<grid, nt, 0, st>>>(x, res, w, rows, H, eps, codes, scales, hidden, rstd)
+  if (H <= 16 * 1024) {
+    if (res) NV_NORM(1, true);
+    else NV_NORM(1, false);
+  } else {
+    if (res) NV_NORM(2, true);
+    else NV_NORM(2, false);
+  }
+#undef NV_NORM
+}
+
+int launch_add_rms_norm(const void* x, const void* res, int in_bf16, const float* w, int64_t rows, int64_t H,
+                        float eps, uint8_t* codes, uint8_t* scales, void* hidden, float* rstd, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  if (in_bf16)
+    norm_fwd<uint16_t>((const uint16_t*)x, (const uint16_t*)res, w, rows, (int)H, eps, codes, scales,
+                       (uint16_t*)hidden, rstd, st);
+  else
+    norm_fwd<float>((const float*)x, (const float*)res, w, rows, (int)H, eps, codes, scales, (float*)hidden, rstd, st);
+  return (int)hipGetLastError();
+}
+
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t H) { return (size_t)norm_bwd_groups(rows) * H * 4; }
+
+template <typename T>
+static void norm_bwd(const T* dy, const T* hidden, const T* dh, const float* w, const float* rstd, int64_t rows,
+                     int H, T* dx, float* partial, int grid, hipStream_t st) {
+  const int nt = norm_threads(H);
+#define NV_NORM(C, DH) k_add_rms_norm_bwd<T, C, DH><<<grid, nt, 0, st>>>(dy, hidden, dh, w, rstd, rows, H, dx, partial)
+  if (H <= 16 * 1024) {
+    if (dh) NV_NORM(1, true);
+    else NV_NORM(1, false);
+  } else {
+    if (dh) NV_NORM(2, true);
+    else NV_NORM(2, false);
+  }
+#undef NV_NORM
+}
+
+int launch_add_rms_norm_bwd(const void* dy, const void* hidden, const void* dh, int in_bf16, const float* w,
+                            const float* rstd, int64_t rows, int64_t H, void* dx, float* dw, void* ws,
+                            void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  const int grid = (int)norm_bwd_groups(rows);
+  float* partial = (float*)ws;
+  if (grid > 0) {
+    if (in_bf16)
+      norm_bwd<uint16_t>((const uint16_t*)dy, (const uint16_t*)hidden, (const uint16_t*)dh, w, rstd, rows, (int)H,
+                         (uint16_t*)dx, partial, grid, st);
+    else
+      norm_bwd<float>((const float*)dy, (const float*)hidden, (const float*)dh, w, rstd, rows, (int)H, (float*)dx,
+                      partial, grid, st);
+  }
+  k_sum_rows<<<(uint32_t)ceil_div(H, 64), 256, 0, st>>>(partial, grid, (int)H, dw);
+  return (int)hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,113 @@
+// Row ranges of experts, found on the device from the cumulative row counts
+// `ends` (int32 [E]).  Rows [ends[e - 1], ends[e]) belong to expert e; rows
+// at or past the last end belong to none and form the extra range E.  Counts
+// are clamped to [0, rows] and taken as their running maximum, so whatever
+// `ends` holds, the ranges are disjoint, cover all rows and stay inside.
+#pragma once
+
+#include "nvfp4_mx8.hpp"
+
+namespace nvfp4 {
+
+struct RowRange {
+  int e;       // expert, or E for rows of none
+  int row0;    // first row
+  int rows;    // rows in the range
+  int before;  // tiles of the ranges before it
+};
+
+// One wave walks the ranges 64 at a time.  `tile` rows make a tile; a range
+// has ceil(rows / tile) of them.
+struct RangeScan {
+  const int* ends;
+  int E, T, tile, lane;
+  int base, prev, tiles;         // ranges done, running end, tiles done
+  int begin, count, first, own;  // this lane's range of the current 64
+
+  NV_DEV RangeScan(const int* ends_, int E_, int T_, int tile_)
+      : ends(ends_), E(E_), T(T_), tile(tile_), lane(threadIdx.x & 63), base(0), prev(0), tiles(0) {}
+
+  // Loads the next 64 ranges; false when none are left.
+  NV_DEV bool next() {
+    if (base > E) return false;
+    const int e = base + lane;
+    int v = T;
+    if (e < E) {
+      v = ends[e];
+      v = v < 0 ? 0 : (v > T ? T : v);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int p = __shfl_up(v, o, 64);
+      if (lane >= o) v = p > v ? p : v;
+    }
+    v = v > prev ? v : prev;
+    const int p = __shfl_up(v, 1, 64);
+    begin = lane ? p : prev;
+    count = v - begin;
+    own = (count + tile - 1) / tile;
+    int s = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int q = __shfl_up(s, o, 64);
+      if (lane >= o) s += q;
+    }
+    first = tiles + s - own;
+    prev = __shfl(v, 63, 64);
+    tiles += __shfl(s, 63, 64);
+    base += 64;
+    return true;
+  }
+};
+
+NV_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The range that holds `unit`, where each tile stands for `per` consecutive
+// units; rows = -1 when there are no more.  total gets the number of tiles.
+NV_DEV RowRange find_range(const int* ends, int E, int T, int tile, int64_t per, int64_t unit) {
+  RowRange r = {0, 0, -1, 0};
+  RangeScan s(ends, E, T, tile);
+  while (s.next()) {
+    const bool mine = unit >= (int64_t)s.first * per && unit < (int64_t)(s.first + s.own) * per;
+    const uint64_t vote = __ballot(mine);
+    if (vote) {
+      const int l = __builtin_ctzll(vote);
+      r.e = uniform(s.base - 64 + l);
+      r.row0 = uniform(__shfl(s.begin, l, 64));
+      r.rows = uniform(__shfl(s.count, l, 64));
+      r.before = uniform(__shfl(s.first, l, 64));
+      return r;
+    }
+  }
+  return r;
+}
+
+// Tiles of all ranges.
+NV_DEV int count_tiles(const int* ends, int E, int T, int tile) {
+  RangeScan s(ends, E, T, tile);
+  while (s.next()) {
+  }
+  return uniform(s.tiles);
+}
+
+// Rows of expert e alone (e < E): the running maximum of the ends before it.
+NV_DEV RowRange expert_range(const int* ends, int T, int e) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  for (int b = lane; b < e; b += 64) {
+    const int v = ends[b];
+    lo = v > lo ? v : lo;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const int p = __shfl_xor(lo, o, 64);
+    lo = p > lo ? p : lo;
+  }
+  lo = lo > T ? T : lo;
+  int hi = ends[e];
+  hi = hi > T ? T : hi;
+  hi = hi > lo ? hi : lo;
+  return {e, uniform(lo), uniform(hi - lo), 0};
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,198 @@
+// Device helpers of the layer operators: 8-bit rows ("mx8"), 4-bit weight
+// decode, range-checked loads, wave sums.
+//
+// mx8: e4m3 codes with one e8m0 scale for each 32 consecutive elements of a
+// row (the last group of a row may be shorter).  The scale is the smallest
+// 2^s, s >= -117, with max |finite value| <= 448 * 2^s; what is not finite is
+// coded as NaN.  s >= -117 keeps every value code * 2^s (smallest 2^-9 *
+// 2^-117) a normal bf16, so mx8 rows enter the matrix cores exactly.
+#pragma once
+
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+typedef __bf16 nv_bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 nv_bf8 __attribute__((ext_vector_type(8)));
+typedef float nv_f4 __attribute__((ext_vector_type(4)));
+typedef unsigned int nv_u4 __attribute__((ext_vector_type(4)));
+typedef unsigned int nv_u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kMxGroup = 32;  // elements under one e8m0 scale
+
+// ------------------------------------------------------- storage formats
+
+// fp32 pair -> two bf16 in one word, round to nearest even (one conversion
+// instruction; a NaN stays a NaN).
+NV_DEV uint32_t pack_bf16(float a, float b) {
+  nv_f2 v;
+  v.x = a;
+  v.y = b;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, nv_bf2));
+}
+
+NV_DEV void store16(uint16_t* p, const float x[16]) {
+  nv_u4 a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    b[i] = pack_bf16(x[8 + 2 * i], x[9 + 2 * i]);
+  }
+  nv_u4* q = reinterpret_cast<nv_u4*>(p);
+  q[0] = a;
+  q[1] = b;
+}
+
+// Values that a store of x in the row's type would leave, as fp32.
+NV_DEV void round_to(const uint16_t*, float x[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = pack_bf16(x[2 * i], x[2 * i + 1]);
+    x[2 * i] = bits2f(w << 16);
+    x[2 * i + 1] = bits2f(w & 0xFFFF0000u);
+  }
+}
+NV_DEV void round_to(const float*, float*) {}
+
+// ------------------------------------------------------------------ mx8
+
+// Biased e8m0 byte of a group whose largest finite magnitude has the bits m:
+// m = 1.f * 2^(E - 127) needs 2^(E - 135) while 1.f <= 1.75, else 2^(E - 134).
+NV_DEV uint32_t mx8_scale_byte(uint32_t m) {
+  const int e = (int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)(e > 10 ? e : 10);
+}
+
+// Value of an e8m0 byte (a byte below 1 would be subnormal; the encoder gives
+// 10..247).  Byte 255 decodes to infinity.
+NV_DEV float e8m0_value(uint32_t byte) { return bits2f(byte << 23); }
+
+// Magnitude bits of 16 values, the largest finite one; what is not finite
+// counts as 0.
+NV_DEV uint32_t finite_amax_bits(const float v[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = f2bits(v[i]) & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  if (m >= 0x7F800000u) {  // rare: leave out infinities and NaN
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t b = f2bits(v[i]) & 0x7FFFFFFFu;
+      m = (b < 0x7F800000u && b > m) ? b : m;
+    }
+  }
+  return m;
+}
+
+// The value of the neighbouring lane (lane ^ 1).
+NV_DEV uint32_t lane_xor1(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+}
+
+// One half of an mx8 group held by this lane, the other half by lane ^ 1
+// (both lanes must be active; a missing half passes zeros).  Returns the
+// scale byte; codes gets 16 e4m3 codes.
+NV_DEV uint32_t mx8_encode16(const float v[16], nv_u4& codes) {
+  uint32_t m = finite_amax_bits(v);
+  const uint32_t o = lane_xor1(m);
+  m = m > o ? m : o;
+  const uint32_t byte = mx8_scale_byte(m);
+  const float inv = bits2f((254u - byte) << 23);  // 2^-s, s = byte - 127 in -117..120
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[4 * j + i] * inv;  // |x| <= 448 where finite: the conversion never saturates
+      q[i] = (f2bits(x) & 0x7FFFFFFFu) >= 0x7F800000u ? bits2f(0x7FC00000u) : x;
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)any_u32(), false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    codes[j] = (uint32_t)w;
+  }
+  return byte;
+}
+
+// Four e4m3 codes times a power of two -> four bf16, exact where the result
+// is a normal number.
+NV_DEV nv_u2 mx8_to_bf16(uint32_t w, float scale) {
+  nv_u2 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true));
+  return r;
+}
+
+// 16 codes (one 16-byte load) times a power of two -> 16 fp32 values.
+NV_DEV void mx8_values16(nv_u4 c, float scale, float v[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const nv_f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
+    const nv_f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], true);
+    v[4 * j] = a.x * scale;
+    v[4 * j + 1] = a.y * scale;
+    v[4 * j + 2] = b.x * scale;
+    v[4 * j + 3] = b.y * scale;
+  }
+}
+
+// -------------------------------------------------------- 4-bit weights
+
+// Eight e2m1 codes times their block's e4m3 scale s -> eight bf16.  A code
+// has 2 significant bits and a scale 4, so the product has at most 6 and
+// bf16 holds it exactly: the matrix cores multiply the stored weight, not a
+// rounding of it.  The second-level scale is applied to the sums.
+NV_DEV nv_bf8 fp4_to_bf16(uint32_t w, float s) {
+  const nv_f2 a = hw_fp4_values<0>(w), b = hw_fp4_values<1>(w), c = hw_fp4_values<2>(w), d = hw_fp4_values<3>(w);
+  nv_u4 r;
+  r[0] = pack_bf16(a.x * s, a.y * s);
+  r[1] = pack_bf16(b.x * s, b.y * s);
+  r[2] = pack_bf16(c.x * s, c.y * s);
+  r[3] = pack_bf16(d.x * s, d.y * s);
+  return __builtin_bit_cast(nv_bf8, r);
+}
+
+// D += A B for a 16x32 and a 32x16 bf16 tile.  Lane l holds A[l % 16] and
+// B[..][l % 16] at the eight k's of its lane group l / 16, and D[4 (l / 16) +
+// r][l % 16], r = 0..3.  Which k's a lane group holds is free as long as A
+// and B agree.
+NV_DEV nv_f4 mfma16(nv_bf8 a, nv_bf8 b, nv_f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// ---------------------------------------------------------------- loads
+
+// A buffer of `bytes` bytes: loads outside it return zeros.
+typedef __amdgpu_buffer_rsrc_t nv_buf;
+NV_DEV nv_buf make_buf(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer (all are below 2^31 bytes)
+NV_DEV nv_u4 buf16(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0); }
+NV_DEV nv_u2 buf8(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0); }
+NV_DEV uint32_t buf4(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0); }
+NV_DEV uint32_t buf1(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b8(b, (int)off, 0, 0); }
+
+// ------------------------------------------------------------ reductions
+
+NV_DEV float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// Sum over the workgroup; every lane gets it.  `lds` holds one float a wave
+// and is free again after the next barrier.
+NV_DEV float block_sum(float v, float* lds) {
+  v = wave_sum(v);
+  const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  if (nw == 1) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[wave] = v;
+  __syncthreads();
+  float r = 0.0f;
+  for (int i = 0; i < nw; ++i) r += lds[i];
+  return r;
+}
+
+}  // namespace nvfp4

@@ -113,4 +113,42 @@ inline LaunchPlan plan_amax(int64_t M, int64_t K, int per_row) {
   return {PLAN_AMAX_PARTIAL, 1, amax_partial_groups(M, K), kAmaxThreads};
 }
 
+// ---- layer operators
+
+// Norm: one workgroup a row, 16 elements a lane (32 for rows over 16384), at
+// most kNormMaxGrid workgroups (further rows in a loop).
+constexpr int64_t kNormMaxH = 32768;
+constexpr int64_t kNormMaxGrid = int64_t(1) << 20;
+inline int norm_threads(int64_t H) {
+  const int64_t per = H <= 16 * 1024 ? 16 : 32;
+  return (int)ceil_div(ceil_div(H, per), 64) * 64;
+}
+// Norm's gradient: workgroups, each with one partial row of dw.
+constexpr int64_t kNormBwdGroups = 1024;
+inline int64_t norm_bwd_groups(int64_t rows) { return rows < kNormBwdGroups ? rows : kNormBwdGroups; }
+
+// Matrix products.
+constexpr int kMatvecThreads = 512;
+constexpr int64_t kMatmulMaxK = int64_t(1) << 20;  // a tile's rows stay below 2^31 bytes
+constexpr int64_t kMatmulMaxE = 65534;             // grid y of k_matvec
+// Fragments of 16 n's per workgroup of k_matvec.
+inline int matvec_frags(int64_t N, int64_t E) {
+  const int64_t tiles = ceil_div(N, 16) * E;
+  return tiles >= 4096 ? 4 : tiles >= 1024 ? 2 : 1;
+}
+// Few rows an expert: weights dominate, k_matvec.
+inline bool use_matvec(int64_t T, int64_t E) { return T <= 16 * E; }
+// Row tile of k_grouped.
+inline int grouped_rows(int64_t T, int64_t E) {
+  const int64_t per = T / (E > 0 ? E : 1);
+  return per >= 128 ? 128 : per >= 64 ? 64 : 32;
+}
+// Upper bound of k_grouped's tiles for E experts and the rows of none (E = 0:
+// all rows in one range): each range adds less than one tile to T / bm.
+inline int64_t grouped_grid(int64_t T, int64_t E, int64_t N, int64_t bm) {
+  int64_t m = ceil_div(T, bm) + E;
+  if (m > T) m = T;
+  return xcd_grid(m * ceil_div(N, 256));
+}
+
 }  // namespace nvfp4

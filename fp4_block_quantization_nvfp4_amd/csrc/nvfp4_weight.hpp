@@ -1,0 +1,113 @@
+// Operands of the matrix products: rows of x (bf16 or mx8) and 4-bit weights.
+#pragma once
+
+#include "nvfp4_launch.hpp"
+#include "nvfp4_mx8.hpp"
+
+namespace nvfp4 {
+
+// Rows row0 .. row0 + rows - 1 of x; rows and k's outside read as zeros.
+template <bool MX8>
+struct RowsView {
+  nv_buf x, s;
+  int K, ns;
+  NV_DEV RowsView(const MatmulArgs& a, int64_t row0, int rows) : K(a.K), ns((a.K + kMxGroup - 1) / kMxGroup) {
+    const int64_t pitch = MX8 ? a.K : 2 * (int64_t)a.K;
+    x = make_buf((const char*)a.x + row0 * pitch, (uint32_t)(rows * pitch));
+    s = make_buf(MX8 ? a.xs + row0 * ns : nullptr, MX8 ? (uint32_t)(rows * ns) : 0u);
+  }
+  // k .. k + 31 of row r as four fragments of eight; k % 32 == 0.
+  NV_DEV void load32(int r, int k, nv_bf8 f[4]) const {
+    if (MX8) {
+      nv_u4 c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) c[h] = buf16(x, k + 16 * h < K ? (uint32_t)(r * K + k + 16 * h) : kOutside);
+      const float sc = e8m0_value(buf1(s, k < K ? (uint32_t)(r * ns + k / kMxGroup) : kOutside));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const nv_u2 p = mx8_to_bf16(c[h][2 * j], sc), q = mx8_to_bf16(c[h][2 * j + 1], sc);
+          f[2 * h + j] = __builtin_bit_cast(nv_bf8, (nv_u4){p.x, p.y, q.x, q.y});
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t off = k + 8 * j < K ? (uint32_t)(r * K + k + 8 * j) * 2u : kOutside;
+        f[j] = __builtin_bit_cast(nv_bf8, buf16(x, off));
+      }
+    }
+  }
+};
+
+// Rows n0 .. n0 + rows - 1 of expert e's weight [N, K]; BLK 0: a scale for
+// 1x16 elements [N, K / 16]; 1: for 16x16 tiles [N / 16, K / 16]; 2: the same
+// tiles stored as those of the transposed weight, [K / 16, N / 16].  Rows and
+// k's outside read as code 0, scale 0.
+template <int BLK>
+struct WeightView {
+  nv_buf w, s;
+  int K, kb, nb;  // kb blocks along k, nb tiles along n
+  int t0;         // BLK 2: first tile along n
+  NV_DEV WeightView(const MatmulArgs& a, int e, int n0, int most) : K(a.K), kb(a.K / 16), nb(a.N / 16), t0(n0 / 16) {
+    const int rows = a.N - n0 < most ? a.N - n0 : most;
+    const int64_t NK = (int64_t)a.N * a.K;
+    w = make_buf(a.w + e * (NK / 2) + (int64_t)n0 * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
+    if (BLK == 0) s = make_buf(a.ws + e * (NK / 16) + (int64_t)n0 * kb, (uint32_t)rows * (uint32_t)kb);
+    else if (BLK == 1)
+      s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
+    else s = make_buf(a.ws + e * (NK / 256), (uint32_t)kb * (uint32_t)nb);
+  }
+  // Codes of k .. k + 31 of row r (k % 32 == 0).
+  NV_DEV nv_u4 codes(int r, int k) const {
+    const uint32_t off = (uint32_t)r * (uint32_t)(K / 2) + (uint32_t)(k / 2);
+    const nv_u2 a = buf8(w, k < K ? off : kOutside), b = buf8(w, k + 16 < K ? off + 8 : kOutside);
+    return (nv_u4){a.x, a.y, b.x, b.y};
+  }
+  // Scale byte of the block that holds k (k % 16 == 0) of row r.
+  NV_DEV uint32_t scale(int r, int k) const {
+    const uint32_t b = (uint32_t)(k / 16);
+    const uint32_t off = BLK == 0 ? (uint32_t)r * (uint32_t)kb + b
+                         : BLK == 1 ? (uint32_t)(r / 16) * (uint32_t)kb + b
+                                    : b * (uint32_t)nb + (uint32_t)(t0 + r / 16);
+    return buf1(s, k < K ? off : kOutside);
+  }
+  NV_DEV void load32(int r, int k, nv_bf8 f[4]) const {
+    const nv_u4 c = codes(r, k);
+    const float s0 = __builtin_amdgcn_cvt_f32_fp8((int)scale(r, k), 0);
+    const float s1 = __builtin_amdgcn_cvt_f32_fp8((int)scale(r, k + 16), 0);
+    f[0] = fp4_to_bf16(c[0], s0);
+    f[1] = fp4_to_bf16(c[1], s0);
+    f[2] = fp4_to_bf16(c[2], s1);
+    f[3] = fp4_to_bf16(c[3], s1);
+  }
+};
+
+// Second-level scale of row n of expert e's weight.
+NV_DEV float second_scale(const MatmulArgs& a, int e, int n) {
+  if (a.mode == 0) return 1.0f;
+  return a.amax[a.mode == 1 ? (int64_t)e : (int64_t)e * a.N + n] / a.D;
+}
+
+NV_DEV void store_out(const MatmulArgs& a, float v, int64_t t, int n) {
+  const int64_t i = t * a.N + n;
+  if (a.out_bf16) ((uint16_t*)a.out)[i] = (uint16_t)pack_bf16(v, v);
+  else ((float*)a.out)[i] = v;
+}
+
+// Four consecutive n's (n % 4 == 0) of one row; those at or past N are left.
+NV_DEV void store_out4(const MatmulArgs& a, float v0, float v1, float v2, float v3, int64_t t, int n) {
+  const int64_t i = t * a.N + n;
+  if (n + 4 <= a.N && a.N % 4 == 0) {
+    if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.out + i) = (nv_u2){pack_bf16(v0, v1), pack_bf16(v2, v3)};
+    else *reinterpret_cast<nv_f4*>((float*)a.out + i) = (nv_f4){v0, v1, v2, v3};
+    return;
+  }
+  if (n < a.N) store_out(a, v0, t, n);
+  if (n + 1 < a.N) store_out(a, v1, t, n + 1);
+  if (n + 2 < a.N) store_out(a, v2, t, n + 2);
+  if (n + 3 < a.N) store_out(a, v3, t, n + 3);
+}
+
+}  // namespace nvfp4

@@ -267,6 +267,111 @@ nvfp4_status nvfp4_quantize_4over6_2d(const void* x, nvfp4_dtype dt, int64_t M, 
                                       uint8_t* tile_scales, void* stream);
 
 /*
+ * Operators of a layer whose weights are stored in NVFP4.
+ *
+ * 8-bit rows ("mx8"): e4m3 codes [T, K] with one e8m0 scale byte (a power of
+ * two, 2^(byte - 127)) for each 32 consecutive elements of a row, scales
+ * [T, ceil(K / 32)]; the last group of a row may be shorter (K % 16 == 0).
+ * The scale is the smallest 2^s, s >= -117, with max |finite value| <=
+ * 448 * 2^s, codes are rounded to nearest even, and what is not finite is
+ * coded as NaN.  Where mx8 rows are read, any scale byte is taken; values
+ * below 2^-126 may count as zero.
+ *
+ * Weights are those that nvfp4_quantize, nvfp4_quantize_2d and the
+ * four-over-six entry points write: packed [E, N, K/2], scales by `blocks`,
+ * second-level scale by scale_mode (NONE; TENSOR: global_amax[e] of each
+ * expert; ROW: global_amax[e * N + n]) and bound (256 or 448), as for
+ * nvfp4_dequantize.  The products multiply the stored weights exactly (code
+ * times block scale fits a bf16), sum in fp32 and apply the second-level
+ * scale to the sums, which are rounded once.  Sums have a fixed order.
+ *
+ * Further limits: H <= 32768 for the norm; N, K <= 2^20 and E <= 65534 for
+ * the products, T < 2^31, and E*N*K, T*N and T*K <= 2^33 (NVFP4_E_RANGE).
+ * Rows, codes and outputs are 16-byte aligned, packed weights 8-byte,
+ * fp32 and int32 arrays 4-byte (weight, dweight and workspace 16-byte).
+ */
+
+/* Scale blocks of a 4-bit weight [N, K]: 1x16 elements, scales [N, K/16];
+ * 16x16 tiles, scales [N/16, K/16] (N % 16 == 0); or 16x16 tiles stored as
+ * those of the transposed weight, scales [K/16, N/16], so that the columnwise
+ * codes of nvfp4_quantize_2d are used with its tile scales as they are. */
+typedef enum { NVFP4_BLOCK_1X16 = 0, NVFP4_BLOCK_16X16 = 1, NVFP4_BLOCK_16X16_T = 2 } nvfp4_block;
+
+/*
+ * nvfp4_add_rms_norm - root-mean-square norm of h = x + residual over rows
+ * of H elements: y_j = h_j * rstd * weight_j, rstd = 1 / sqrt(mean h^2 + eps),
+ * y written as mx8.  hidden receives h rounded to the rows' type, rstd [T]
+ * one fp32 a row; y is taken from the unrounded h.  residual and hidden are
+ * both given or both NULL (then h = x and nothing is written for it).
+ * weight [H] fp32; H % 16 == 0; eps >= 0.
+ */
+nvfp4_status nvfp4_add_rms_norm(const void* x, const void* residual, nvfp4_dtype dt, const float* weight,
+                                int64_t T, int64_t H, float eps, uint8_t* codes, uint8_t* scales,
+                                void* hidden, float* rstd, void* stream);
+
+/*
+ * nvfp4_add_rms_norm_backward - gradient of the above from hidden and rstd:
+ * n = hidden * rstd, d = dy * weight, dx = rstd * (d - n * mean(d * n)) +
+ * dhidden (the gradient that reaches h from elsewhere; NULL: none), which is
+ * the gradient of x and of residual alike, in the rows' type; dweight [H] =
+ * sum over rows of dy * n in fp32.  workspace: at least
+ * nvfp4_add_rms_norm_backward_workspace_bytes(T, H) bytes.  T == 0 gives
+ * dweight = 0.
+ */
+size_t nvfp4_add_rms_norm_backward_workspace_bytes(int64_t T, int64_t H);
+nvfp4_status nvfp4_add_rms_norm_backward(const void* dy, const void* hidden, const void* dhidden, nvfp4_dtype dt,
+                                         const float* weight, const float* rstd, int64_t T, int64_t H, void* dx,
+                                         float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_swiglu - gated activation y = g * sigmoid(g) * u of rows [g | u]
+ * (gate_up [T, 2F], F % 16 == 0), written as mx8 [T, F].  With kept and
+ * kept_scales (both or neither NULL) the same pass writes g and u as mx8:
+ * kept [T, 2F], kept_scales [T, 2 * ceil(F / 32)], those of g first.
+ */
+nvfp4_status nvfp4_swiglu(const void* gate_up, nvfp4_dtype dt, int64_t T, int64_t F, uint8_t* codes,
+                          uint8_t* scales, uint8_t* kept, uint8_t* kept_scales, void* stream);
+
+/*
+ * nvfp4_swiglu_backward - gradient of the above from the 8-bit checkpoint:
+ * with g, u its values, dg = dy * u * s * (1 + g * (1 - s)) and du = dy * g *
+ * s, s = sigmoid(g).  dout [T, F] and dgate_up [T, 2F] of dt.
+ */
+nvfp4_status nvfp4_swiglu_backward(const void* dout, nvfp4_dtype dt, int64_t T, int64_t F, const uint8_t* kept,
+                                   const uint8_t* kept_scales, void* dgate_up, void* stream);
+
+/*
+ * nvfp4_matvec - out [T, N] = x W^T for one 4-bit weight W [N, K] and a few
+ * rows x [T, K] (any T; up to 16 rows cost one read of the weights).  x is
+ * bf16, or e4m3 codes when x_scales (e8m0) is given.  K == 0 gives zeros.
+ */
+nvfp4_status nvfp4_matvec(const void* x, const uint8_t* x_scales, int64_t T, int64_t N, int64_t K,
+                          const uint8_t* packed, const uint8_t* scales, nvfp4_block blocks,
+                          const float* global_amax, nvfp4_scale_mode scale_mode, float bound, void* out,
+                          nvfp4_dtype out_dt, void* stream);
+
+/*
+ * nvfp4_grouped_matmul - out [T, N]: row t of expert e is x[t] W_e^T, for E
+ * 4-bit weights [N, K].  ends [E] int32 on the device: expert e owns the rows
+ * from ends[e - 1] (0 for the first) up to ends[e].  ends must not decrease;
+ * values are clamped to [0, T] and to the ones before them, whatever they
+ * are, and rows past the last end belong to no expert and give zeros.
+ */
+nvfp4_status nvfp4_grouped_matmul(const void* x, const uint8_t* x_scales, int64_t T, int64_t E, int64_t N,
+                                  int64_t K, const int32_t* ends, const uint8_t* packed, const uint8_t* scales,
+                                  nvfp4_block blocks, const float* global_amax, nvfp4_scale_mode scale_mode,
+                                  float bound, void* out, nvfp4_dtype out_dt, void* stream);
+
+/*
+ * nvfp4_grouped_wgrad - dw [E, N, K] of out_dt: dw[e] = sum over the rows t of
+ * expert e of dy[t]^T x[t], dy [T, N] bf16, x as above, summed in fp32.  An
+ * expert without rows gets zeros.  N % 16 == 0.
+ */
+nvfp4_status nvfp4_grouped_wgrad(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E,
+                                 int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
+                                 void* stream);
+
+/*
  * Test support (not part of the quantization path).
  *
  * nvfp4_selftest_scan - exhaustive scan of one of the gfx950 conversions the
