@@ -4,11 +4,13 @@
 //
 // A workgroup of four waves makes a tile of BM rows by 256 n's and walks k in
 // steps of 128.  The rows of x are staged as bf16 in shared memory (two
-// buffers, the loads of the next step in flight during the products of this
-// one); each wave decodes the weights of its own 64 n's straight from global
-// memory into fragments, so no weight is decoded twice in a workgroup and
-// the weights cost no shared memory.  The weight is the first operand of the
-// matrix product: a lane then holds four consecutive n's of one row.
+// buffers, half a step's loads in flight at a time); each wave decodes the
+// weights of its own 64 n's straight from global memory into fragments, so no
+// weight is decoded twice in a workgroup and the weights cost no shared
+// memory.  Codes are fetched into the registers that the step has just
+// consumed, and the next fragments are decoded and read while the matrix cores
+// work on the present ones.  The weight is the first operand of the matrix
+// product: a lane then holds four consecutive n's of one row.
 //
 // The row ranges are known on the device only, so the grid is an upper bound
 // and surplus workgroups leave at once.  Tiles are numbered per expert in
@@ -23,19 +25,19 @@ namespace nvfp4 {
 
 template <bool MX8, int BLK, int BM>
 __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
-  constexpr int MI = BM / 16;
+  constexpr int MI = BM / 32;
   __shared__ uint16_t lds[2][BM * 128];
-  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
+  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
   const int ntiles = (a.N + 255) / 256;
 
   // this workgroup's tile
   int e = 0, row0, rows, n_tile;
   {
+    RowRange rr = {0, 0, a.T, 0};
     const int total = a.ends ? count_tiles(a.ends, a.E, a.T, BM) : (a.T + BM - 1) / BM;
     const int64_t units = (int64_t)total * ntiles, per = (units + 7) / 8;
     const int64_t slot = blockIdx.x >> 3, unit = (blockIdx.x & 7) * per + slot;
     if (slot >= per || unit >= units) return;
-    RowRange rr = {0, 0, a.T, 0};
     if (a.ends) rr = find_range(a.ends, a.E, a.T, BM, ntiles, unit);
     if (rr.rows < 0) return;
     const int mt = (rr.rows + BM - 1) / BM;
@@ -50,26 +52,27 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   const bool none = a.ends && e >= a.E;
   const int n0 = n_tile * 256 + wave * 64;
 
-  nv_f4 acc[4][MI];
+  nv_f16 acc[2][MI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int m = 0; m < MI; ++m) acc[i][m] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m = 0; m < MI; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][m][r] = 0.0f;
 
   const int nk = none ? 0 : (a.K + 127) / 128;
   if (nk) {
-    const WeightView<BLK> w(a, e, n0 < a.N ? n0 : 0, 64);
+    const WeightStream<BLK> w(a, e, n0, l32, half);
     const RowsView<MX8> x(a, row0, rows);
-    // staging: 16-byte pieces of the step's x, piece p of a row
-    constexpr int PR = MX8 ? 8 : 16, PIECES = BM * PR / 256 > 0 ? BM * PR / 256 : 1;
-    constexpr bool ALL = BM * PR >= 256;
+    // staging of half a step's rows: 16-byte pieces, piece p of a row
+    constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
     nv_u4 st[PIECES];
     uint32_t sts[PIECES];
-    auto fetch = [&](int k0) {
+    auto fetch = [&](int k0, int h) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int id = tid + i * 256, r = id / PR, p = id % PR;
-        if (!ALL && r >= BM) continue;
+        const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
+        if (HALF < 256 && id >= HALF) continue;
         if (MX8) {
           const int k = k0 + p * 16;
           st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) : kOutside);
@@ -84,11 +87,11 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
     auto put = [&](uint16_t* buf, int r, int c, nv_u4 v) {
       *reinterpret_cast<nv_u4*>(buf + r * 128 + ((c ^ (r & 15)) * 8)) = v;
     };
-    auto stage = [&](uint16_t* buf) {
+    auto stage = [&](uint16_t* buf, int h) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int id = tid + i * 256, r = id / PR, p = id % PR;
-        if (!ALL && r >= BM) continue;
+        const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
+        if (HALF < 256 && id >= HALF) continue;
         if (MX8) {
           const float sc = e8m0_value(sts[i]);
 #pragma unroll
@@ -101,67 +104,81 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
         }
       }
     };
-    nv_u4 wc[4];
-    uint32_t ws[4][2];
-    auto fetch_w = [&](int k0) {
-      const int k = k0 + grp * 32;
+    nv_u4 wc[2][2];
+    uint32_t ws[2], wsn[2];
+    nv_bf8 wf[2][2], xf[2][MI];
+    auto fetch_codes = [&](int k0, int q) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wc[i] = w.codes(i * 16 + l16, k);
-        ws[i][0] = w.scale(i * 16 + l16, k);
-        ws[i][1] = w.scale(i * 16 + l16, k + 16);
-      }
+      for (int i = 0; i < 2; ++i) wc[i][q] = w.codes(i, k0, q);
     };
-    fetch(0);
-    fetch_w(0);
-    stage(lds[0]);
+    auto decode = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) wf[s & 1][i] = fp4_to_bf16(wc[i][s >> 2][s & 3], e4m3_byte(ws[i], s >> 1));
+    };
+    auto load_x = [&](const uint16_t* buf, int s) {
+#pragma unroll
+      for (int m = 0; m < MI; ++m)
+        xf[s & 1][m] = *reinterpret_cast<const nv_bf8*>(buf + (m * 32 + l32) * 128 + (((8 * half + s) ^ (l32 & 15)) * 8));
+    };
+    fetch(0, 0);
+    fetch_codes(0, 0);
+    fetch_codes(0, 1);
+    w.scales(0, ws);
+    stage(lds[0], 0);
+    fetch(0, 1);
+    stage(lds[0], 1);
     __syncthreads();
     for (int kt = 0; kt < nk; ++kt) {
       const uint16_t* buf = lds[kt & 1];
-      nv_u4 c[4];
-      float s[4][2];
+      uint16_t* next = lds[(kt + 1) & 1];
+      const int k1 = kt * 128 + 128;  // past the last step every load is outside and gives zeros
+      load_x(buf, 0);
+      decode(0);
+      fetch(k1, 0);
+      w.scales(k1, wsn);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = wc[i];
-        s[i][0] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i][0], 0);
-        s[i][1] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i][1], 0);
-      }
-      const bool more = kt + 1 < nk;
-      if (more) {
-        fetch(kt * 128 + 128);
-        fetch_w(kt * 128 + 128);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        nv_bf8 wf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wf[i] = fp4_to_bf16(c[i][j], s[i][j >> 1]);
-#pragma unroll
-        for (int m = 0; m < MI; ++m) {
-          const nv_bf8 xf = *reinterpret_cast<const nv_bf8*>(buf + (m * 16 + l16) * 128 + (((4 * grp + j) ^ l16) * 8));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][m] = mfma16(wf[i], xf, acc[i][m]);
+      for (int s = 0; s < 8; ++s) {
+        if (s < 7) {
+          load_x(buf, s + 1);
+          decode(s + 1);
         }
+        if (s == 3) fetch_codes(k1, 0);
+        if (s == 4) {
+          stage(next, 0);
+          fetch(k1, 1);
+        }
+        if (s == 6) fetch_codes(k1, 1);
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[i][m] = mfma32(wf[s & 1][i], xf[s & 1][m], acc[i][m]);
       }
-      if (more) stage(lds[(kt + 1) & 1]);
+      stage(next, 1);
+      ws[0] = wsn[0];
+      ws[1] = wsn[1];
       __syncthreads();
     }
   }
   if (n0 >= a.N) return;
+  // a lane holds, of each 32x32 tile, row l32 of x and n = 8 q + 4 half + 0..3
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + i * 16 + grp * 4;
-    float sc[4];
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sc[r] = none || n + r >= a.N ? 0.0f : second_scale(a, e, n + r);
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + i * 32 + q * 8 + half * 4;
+      float sc[4];
 #pragma unroll
-    for (int m = 0; m < MI; ++m) {
-      const int t = m * 16 + l16;
-      if (t >= rows) continue;
-      const nv_f4 v = none ? nv_f4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][m];
-      store_out4(a, v[0] * sc[0], v[1] * sc[1], v[2] * sc[2], v[3] * sc[3], row0 + t, n);
+      for (int r = 0; r < 4; ++r) sc[r] = none || n + r >= a.N ? 0.0f : second_scale(a, e, n + r);
+#pragma unroll
+      for (int m = 0; m < MI; ++m) {
+        const int t = m * 32 + l32;
+        if (t >= rows) continue;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = none ? 0.0f : acc[i][m][q * 4 + r] * sc[r];
+        store_out4(a, v[0], v[1], v[2], v[3], row0 + t, n);
+      }
     }
-  }
 }
 
 template <bool MX8, int BLK>

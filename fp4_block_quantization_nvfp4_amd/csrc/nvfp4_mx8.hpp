@@ -15,6 +15,7 @@ namespace nvfp4 {
 typedef __bf16 nv_bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 nv_bf8 __attribute__((ext_vector_type(8)));
 typedef float nv_f4 __attribute__((ext_vector_type(4)));
+typedef float nv_f16 __attribute__((ext_vector_type(16)));
 typedef unsigned int nv_u4 __attribute__((ext_vector_type(4)));
 typedef unsigned int nv_u2 __attribute__((ext_vector_type(2)));
 
@@ -154,11 +155,23 @@ NV_DEV nv_bf8 fp4_to_bf16(uint32_t w, float s) {
   return __builtin_bit_cast(nv_bf8, r);
 }
 
+// Value of byte b (0..3) of a word of e4m3 scales.
+NV_DEV float e4m3_byte(uint32_t w, int b) {
+  return b == 0 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 0) : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 1)
+       : b == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 2) : __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
+}
+
 // D += A B for a 16x32 and a 32x16 bf16 tile.  Lane l holds A[l % 16] and
 // B[..][l % 16] at the eight k's of its lane group l / 16, and D[4 (l / 16) +
 // r][l % 16], r = 0..3.  Which k's a lane group holds is free as long as A
 // and B agree.
 NV_DEV nv_f4 mfma16(nv_bf8 a, nv_bf8 b, nv_f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// The same for a 32x16 and a 16x32 tile: lane l holds A[l % 32] and B[..][l %
+// 32] at the eight k's of its half l / 32, and D[8 (r / 4) + 4 (l / 32) + r %
+// 4][l % 32], r = 0..15.  Twice the work an instruction: a loop that also
+// decodes weights needs the issue slots.
+NV_DEV nv_f16 mfma32(nv_bf8 a, nv_bf8 b, nv_f16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 
 // ---------------------------------------------------------------- loads
 

@@ -84,6 +84,64 @@ struct WeightView {
   }
 };
 
+// A wave's walk along k in steps of 128 over 64 rows of a weight: lane (l32,
+// half) takes, of rows l32 and 32 + l32, the 64 codes from k0 + 64 half on as
+// two 16-byte words and their four scales as one.  What lies past N or K reads
+// as code 0 or scale 0.
+template <int BLK>
+struct WeightStream {
+  nv_buf w, s;
+  int K, kb, nb, at;        // at: 64 half
+  uint32_t row[2], srow[2]; // byte offsets of the lane's rows
+  bool in[2];
+  NV_DEV WeightStream(const MatmulArgs& a, int e, int n0, int l32, int half)
+      : K(a.K), kb(a.K / 16), nb(a.N / 16), at(64 * half) {
+    const int rows = n0 < a.N ? (a.N - n0 < 64 ? a.N - n0 : 64) : 0, t0 = rows ? n0 / 16 : 0, base = rows ? n0 : 0;
+    const int64_t NK = (int64_t)a.N * a.K;
+    w = make_buf(a.w + e * (NK / 2) + (int64_t)base * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
+    if (BLK == 0) s = make_buf(a.ws + e * (NK / 16) + (int64_t)base * kb, (uint32_t)rows * (uint32_t)kb);
+    else if (BLK == 1) s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
+    else s = make_buf(a.ws + e * (NK / 256) + t0, rows ? (uint32_t)kb * (uint32_t)nb - (uint32_t)t0 : 0u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 32 + l32;
+      in[i] = r < rows;
+      row[i] = (uint32_t)r * (uint32_t)(K / 2);
+      srow[i] = BLK == 0 ? (uint32_t)r * (uint32_t)kb : BLK == 1 ? (uint32_t)(r / 16) * (uint32_t)kb : (uint32_t)(r / 16);
+    }
+  }
+  // Codes of the lane's k's 32 q .. 32 q + 31.  A row ends inside a word where
+  // K % 32 == 16: two halves then, so that none is read past the last row.
+  NV_DEV nv_u4 codes(int i, int k0, int q) const {
+    const int k = k0 + at + 32 * q;
+    const uint32_t off = row[i] + (uint32_t)(k / 2);
+    if (K % 32 == 0) return buf16(w, in[i] && k < K ? off : kOutside);
+    const nv_u2 a = buf8(w, in[i] && k < K ? off : kOutside), b = buf8(w, in[i] && k + 16 < K ? off + 8 : kOutside);
+    return (nv_u4){a.x, a.y, b.x, b.y};
+  }
+  // The lane's four scales of both rows, one in a byte.
+  NV_DEV void scales(int k0, uint32_t v[2]) const {
+    const int b = (k0 + at) / 16;
+    if (BLK == 2 || kb < 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = BLK == 2 ? (uint32_t)(b + j) * (uint32_t)nb + srow[i] : srow[i] + (uint32_t)(b + j);
+          p[j] = buf1(s, in[i] && b + j < kb ? off : kOutside);
+        }
+        v[i] = p[0] | p[1] << 8 | p[2] << 16 | p[3] << 24;
+      }
+      return;
+    }
+    // the last word of a row starts at its fourth last byte: shifted down, it has zeros past the row
+    const int c = b < kb - 4 ? b : kb - 4, d = b - c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = buf4(s, in[i] && b < kb ? srow[i] + (uint32_t)c : kOutside) >> (8 * (d & 3));
+  }
+};
+
 // Second-level scale of row n of expert e's weight.
 NV_DEV float second_scale(const MatmulArgs& a, int e, int n) {
   if (a.mode == 0) return 1.0f;
