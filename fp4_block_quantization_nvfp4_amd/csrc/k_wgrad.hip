@@ -1,13 +1,16 @@
 // Weight gradient of products grouped by expert: dw[e, n, k] = sum over the
 // rows t of expert e of dy[t, n] x[t, k], dy bf16, x bf16 or mx8.
 //
-// The sum runs over rows, the slow axis of both operands, so both tiles are
-// transposed on their way into shared memory: a lane takes a word (two bf16
-// or four e4m3) of eight consecutive rows and writes, for each column, the
-// eight rows as one 16-byte chunk.  A workgroup of four waves makes 256 n's by
-// 128 k's and walks the rows 64 at a time, the next rows' loads in flight
-// during the products.  x is the first operand: a lane then holds four
-// consecutive k's of one n.  An expert without rows gets zeros.
+// The sum runs over rows, the slow axis of both operands.  A workgroup of
+// four waves makes 256 n's by 128 k's and walks the rows 64 at a time.  Each
+// wave has 64 n's of its own and takes dy straight into registers: four n's of
+// eight rows a lane, turned into four fragments by byte permutes.  x is shared
+// and goes through shared memory (two buffers): a lane takes a word (two bf16
+// or four e4m3) of eight rows and writes, for each column, the eight rows as
+// one 16-byte chunk.  Loads of the next step fill the registers that this one
+// has just consumed.  x is the first operand: a lane then holds four
+// consecutive k's of one n.  Each XCD takes an eighth of every expert's tiles,
+// since experts differ in rows.  An expert without rows gets zeros.
 #include "nvfp4_experts.hpp"
 #include "nvfp4_launch.hpp"
 #include "nvfp4_plan.hpp"
@@ -30,14 +33,12 @@ NV_DEV void transpose2(const uint32_t v[8], nv_u4& c0, nv_u4& c1) {
 
 template <bool MX8>
 __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
-  __shared__ uint16_t ldy[kWgN * kWgT];
-  __shared__ uint16_t lx[kWgK * kWgT];
+  __shared__ uint16_t lx[2][kWgK * kWgT];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
   const int nk = (a.K + kWgK - 1) / kWgK, nn = (a.N + kWgN - 1) / kWgN;
-  const int64_t units = (int64_t)a.E * nk * nn, per = (units + 7) / 8;
-  const int64_t slot = blockIdx.x >> 3, unit = (blockIdx.x & 7) * per + slot;
-  if (slot >= per || unit >= units) return;
-  const int e = (int)(unit / ((int64_t)nk * nn)), in = (int)(unit - (int64_t)e * nk * nn);
+  const int share = (nk * nn + 7) / 8;  // tiles of one expert on one XCD
+  const int slot = blockIdx.x >> 3, e = slot / share, in = (blockIdx.x & 7) * share + slot % share;
+  if (in >= nk * nn) return;
   const int n0 = (in / nk) * kWgN, k0 = (in % nk) * kWgK;
   const RowRange rr = expert_range(a.ends, a.T, e);
   const int ns = (a.K + kMxGroup - 1) / kMxGroup;
@@ -48,34 +49,36 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) acc[i][m] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  constexpr int XI = MX8 ? 1 : 2;
-  uint32_t vy[4][8], vx[XI][8], vs[8];
-  const int64_t xp = MX8 ? a.K : 2 * (int64_t)a.K;
-  auto fetch = [&](int t0) {
-    const int rows = rr.rows - t0 < kWgT ? rr.rows - t0 : kWgT;
+  // dy: rows 32 j + 8 grp + t of the step, n's nl .. nl + 3
+  const int nl = n0 + wave * 64 + 4 * l16;
+  const uint32_t yat = nl < a.N ? (uint32_t)(8 * grp) * (uint32_t)a.N * 2u + (uint32_t)nl * 2u : kOutside;
+  nv_u2 vy[2][8];
+  auto fetch_y = [&](int t0, int j) {
+    const int left = rr.rows - t0, rows = left < 0 ? 0 : left < kWgT ? left : kWgT;
     const nv_buf by = make_buf((const char*)a.dy + (int64_t)(rr.row0 + t0) * 2 * a.N, (uint32_t)rows * 2u * (uint32_t)a.N);
-    const nv_buf bx = make_buf((const char*)a.x + (int64_t)(rr.row0 + t0) * xp, (uint32_t)(rows * xp));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int id = tid + i * 256, c = n0 + (id % 128) * 2, o = id / 128;
+    for (int t = 0; t < 8; ++t) vy[j][t] = buf8(by, yat + (uint32_t)(32 * j + t) * (uint32_t)a.N * 2u);
+  };
+  // x: words of eight consecutive rows
+  constexpr int XI = MX8 ? 1 : 2, XW = MX8 ? 32 : 64, XE = MX8 ? 4 : 2;  // words a row, elements a word
+  uint32_t vx[XI][8], vs[8];
+  const uint32_t xp = MX8 ? (uint32_t)a.K : 2u * (uint32_t)a.K;
+  auto fetch_x = [&](int t0) {
+    const int left = rr.rows - t0, rows = left < 0 ? 0 : left < kWgT ? left : kWgT;
+    const nv_buf bx = make_buf((const char*)a.x + (int64_t)(rr.row0 + t0) * xp, (uint32_t)rows * xp);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) vy[i][t] = buf4(by, c < a.N ? ((uint32_t)(8 * o + t) * (uint32_t)a.N + c) * 2u : kOutside);
+    for (int i = 0; i < XI; ++i) {
+      const int id = tid + i * 256, c = k0 + (id % XW) * XE, o = id / XW;
+      const uint32_t at = c < a.K ? (uint32_t)(8 * o) * xp + (uint32_t)(id % XW) * 4u + (uint32_t)(k0 * (MX8 ? 1 : 2)) : kOutside;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) vx[i][t] = buf4(bx, at + (uint32_t)t * xp);
     }
     if (MX8) {
       const nv_buf bs = make_buf(a.xs + (int64_t)(rr.row0 + t0) * ns, (uint32_t)(rows * ns));
       const int c = k0 + (tid % 32) * 4, o = tid / 32;
+      const uint32_t at = c < a.K ? (uint32_t)(8 * o) * (uint32_t)ns + (uint32_t)(c / kMxGroup) : kOutside;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        vx[0][t] = buf4(bx, c < a.K ? (uint32_t)(8 * o + t) * (uint32_t)a.K + c : kOutside);
-        vs[t] = buf1(bs, c < a.K ? (uint32_t)(8 * o + t) * (uint32_t)ns + c / kMxGroup : kOutside);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < XI; ++i) {
-        const int id = tid + i * 256, c = k0 + (id % 64) * 2, o = id / 64;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) vx[i][t] = buf4(bx, c < a.K ? ((uint32_t)(8 * o + t) * (uint32_t)a.K + c) * 2u : kOutside);
-      }
+      for (int t = 0; t < 8; ++t) vs[t] = buf1(bs, at + (uint32_t)(t * ns));
     }
   };
   auto put2 = [&](uint16_t* buf, int c, int o, const uint32_t v[8]) {
@@ -84,12 +87,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
     *reinterpret_cast<nv_u4*>(buf + wg_at(c, o)) = c0;
     *reinterpret_cast<nv_u4*>(buf + wg_at(c + 1, o)) = c1;
   };
-  auto stage = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int id = tid + i * 256;
-      put2(ldy, (id % 128) * 2, id / 128, vy[i]);
-    }
+  auto stage_x = [&](uint16_t* buf) {
     if (MX8) {
       uint32_t lo[8], hi[8];
 #pragma unroll
@@ -98,39 +96,57 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
         lo[t] = p.x;
         hi[t] = p.y;
       }
-      put2(lx, (tid % 32) * 4, tid / 32, lo);
-      put2(lx, (tid % 32) * 4 + 2, tid / 32, hi);
+      put2(buf, (tid % 32) * 4, tid / 32, lo);
+      put2(buf, (tid % 32) * 4 + 2, tid / 32, hi);
     } else {
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
         const int id = tid + i * 256;
-        put2(lx, (id % 64) * 2, id / 64, vx[i]);
+        put2(buf, (id % 64) * 2, id / 64, vx[i]);
       }
     }
   };
   const int steps = (rr.rows + kWgT - 1) / kWgT;
-  if (steps) fetch(0);
-  for (int s = 0; s < steps; ++s) {
-    stage();
+  if (steps) {
+    fetch_x(0);
+    fetch_y(0, 0);
+    fetch_y(0, 1);
+    stage_x(lx[0]);
     __syncthreads();
-    if (s + 1 < steps) fetch((s + 1) * kWgT);
+  }
+  for (int s = 0; s < steps; ++s) {
+    const uint16_t* buf = lx[s & 1];
+    const int t1 = (s + 1) * kWgT;  // past the last row every load is outside and gives zeros
+    fetch_x(t1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       nv_bf8 yf[4];
+      {
+        uint32_t w[2][8];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) yf[m] = *reinterpret_cast<const nv_bf8*>(ldy + wg_at(wave * 64 + m * 16 + l16, 4 * j + grp));
+        for (int t = 0; t < 8; ++t) w[0][t] = vy[j][t].x, w[1][t] = vy[j][t].y;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          nv_u4 c0, c1;
+          transpose2(w[p], c0, c1);
+          yf[2 * p] = __builtin_bit_cast(nv_bf8, c0);
+          yf[2 * p + 1] = __builtin_bit_cast(nv_bf8, c1);
+        }
+      }
+      fetch_y(t1, j);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const nv_bf8 xf = *reinterpret_cast<const nv_bf8*>(lx + wg_at(i * 16 + l16, 4 * j + grp));
+        const nv_bf8 xf = *reinterpret_cast<const nv_bf8*>(buf + wg_at(i * 16 + l16, 4 * j + grp));
 #pragma unroll
         for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(xf, yf[m], acc[i][m]);
       }
     }
+    stage_x(lx[(s + 1) & 1]);
     __syncthreads();
   }
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    const int n = n0 + wave * 64 + m * 16 + l16;
+    const int n = nl + m;
     if (n >= a.N) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -145,8 +161,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
 }
 
 int launch_wgrad(const WgradArgs& a, void* stream) {
-  const int64_t units = a.E * ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK);
-  const dim3 grid((uint32_t)xcd_grid(units));
+  const dim3 grid((uint32_t)(a.E * xcd_grid(ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK))));
   if (a.xs) k_wgrad<true><<<grid, 256, 0, (hipStream_t)stream>>>(a);
   else k_wgrad<false><<<grid, 256, 0, (hipStream_t)stream>>>(a);
   return (int)hipGetLastError();
