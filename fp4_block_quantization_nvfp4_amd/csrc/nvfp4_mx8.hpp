@@ -175,10 +175,16 @@ NV_DEV nv_f16 mfma32(nv_bf8 a, nv_bf8 b, nv_f16 c) { return __builtin_amdgcn_mfm
 
 // ---------------------------------------------------------------- loads
 
-// A buffer of `bytes` bytes: loads outside it return zeros.
+// A buffer of `bytes` bytes: loads outside it return zeros.  p and bytes are
+// the same in all lanes; saying so keeps the compiler from a loop around each
+// load where it cannot see it.
 typedef __amdgpu_buffer_rsrc_t nv_buf;
 NV_DEV nv_buf make_buf(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer (all are below 2^31 bytes)
 NV_DEV nv_u4 buf16(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0); }
