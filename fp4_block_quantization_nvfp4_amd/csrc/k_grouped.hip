@@ -23,7 +23,7 @@
 
 namespace nvfp4 {
 
-template <bool MX8, int BLK, int BM>
+template <bool MX8, int BLK, int BM, bool WORDS>
 __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   constexpr int MI = BM / 32;
   __shared__ uint16_t lds[2][BM * 128];
@@ -62,101 +62,119 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
 
   const int nk = none ? 0 : (a.K + 127) / 128;
   if (nk) {
-    const WeightStream<BLK> w(a, e, n0, l32, half);
+    const WeightStream<BLK, WORDS> w(a, e, n0, l32, half);
     const RowsView<MX8> x(a, row0, rows);
     // staging of half a step's rows: 16-byte pieces, piece p of a row
     constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
     nv_u4 st[PIECES];
     uint32_t sts[PIECES];
-    auto fetch = [&](int k0, int h) {
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
-        if (HALF < 256 && id >= HALF) continue;
-        if (MX8) {
-          const int k = k0 + p * 16;
-          st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) : kOutside);
-          sts[i] = buf1(x.s, k < a.K ? (uint32_t)(r * x.ns + k / kMxGroup) : kOutside);
-        } else {
-          const int k = k0 + p * 8;
-          st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) * 2u : kOutside);
-        }
+    auto fetch = [&](int i, int k0, int h) {
+      const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
+      if (HALF < 256 && id >= HALF) return;
+      if (MX8) {
+        const int k = k0 + p * 16;
+        st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) : kOutside);
+        sts[i] = buf1(x.s, k < a.K ? (uint32_t)(r * x.ns + k / kMxGroup) : kOutside);
+      } else {
+        const int k = k0 + p * 8;
+        st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) * 2u : kOutside);
       }
     };
     // row r of a buffer: 16 chunks of 16 bytes, chunk c at c ^ (r % 16)
     auto put = [&](uint16_t* buf, int r, int c, nv_u4 v) {
       *reinterpret_cast<nv_u4*>(buf + r * 128 + ((c ^ (r & 15)) * 8)) = v;
     };
-    auto stage = [&](uint16_t* buf, int h) {
+    auto stage = [&](int i, uint16_t* buf, int h) {
+      const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
+      if (HALF < 256 && id >= HALF) return;
+      if (MX8) {
+        const float sc = e8m0_value(sts[i]);
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
-        if (HALF < 256 && id >= HALF) continue;
-        if (MX8) {
-          const float sc = e8m0_value(sts[i]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const nv_u2 u = mx8_to_bf16(st[i][2 * j], sc), v = mx8_to_bf16(st[i][2 * j + 1], sc);
-            put(buf, r, 2 * p + j, (nv_u4){u.x, u.y, v.x, v.y});
-          }
-        } else {
-          put(buf, r, p, st[i]);
+        for (int j = 0; j < 2; ++j) {
+          const nv_u2 u = mx8_to_bf16(st[i][2 * j], sc), v = mx8_to_bf16(st[i][2 * j + 1], sc);
+          put(buf, r, 2 * p + j, (nv_u4){u.x, u.y, v.x, v.y});
         }
+      } else {
+        put(buf, r, p, st[i]);
       }
     };
     nv_u4 wc[2][2];
-    uint32_t ws[2], wsn[2];
-    nv_bf8 wf[2][2], xf[2][MI];
+    uint32_t ws[2][2];  // scales of this step and the next
+    nv_u2 wf[2][2][2];
+    nv_bf8 xf[MI];
     auto fetch_codes = [&](int k0, int q) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) wc[i][q] = w.codes(i, k0, q);
     };
-    auto decode = [&](int s) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) wf[s & 1][i] = fp4_to_bf16(wc[i][s >> 2][s & 3], e4m3_byte(ws[i], s >> 1));
+    // quarter d of the weight fragments of k's 8 s .. 8 s + 7 of each half
+    auto decode = [&](int s, const uint32_t v[2], int d) {
+      wf[s & 1][d >> 1][d & 1] = fp4_half_to_bf16(wc[d >> 1][s >> 2][s & 3], e4m3_byte(v[d >> 1], s >> 1), d & 1);
     };
-    auto load_x = [&](const uint16_t* buf, int s) {
-#pragma unroll
-      for (int m = 0; m < MI; ++m)
-        xf[s & 1][m] = *reinterpret_cast<const nv_bf8*>(buf + (m * 32 + l32) * 128 + (((8 * half + s) ^ (l32 & 15)) * 8));
+    auto load_x = [&](const uint16_t* buf, int s, int m) {
+      xf[m] = *reinterpret_cast<const nv_bf8*>(buf + (m * 32 + l32) * 128 + (((8 * half + s) ^ (l32 & 15)) * 8));
     };
-    fetch(0, 0);
+    auto fragment = [&](int s, int i) {
+      const nv_u2 u = wf[s & 1][i][0], v = wf[s & 1][i][1];
+      return __builtin_bit_cast(nv_bf8, (nv_u4){u.x, u.y, v.x, v.y});
+    };
     fetch_codes(0, 0);
     fetch_codes(0, 1);
-    w.scales(0, ws);
-    stage(lds[0], 0);
-    fetch(0, 1);
-    stage(lds[0], 1);
+    w.scales(0, ws[0]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) fetch(i, 0, h);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) stage(i, lds[0], h);
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) fetch(i, 128, 0);
+    w.scales(128, ws[1]);
     __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MI; ++m) load_x(lds[0], 0, m);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) decode(0, ws[0], d);
+    // Eight parts of 16 k's a step.  While the matrix cores work on part s,
+    // part s + 1 is read and decoded, a piece after each pair of products; the
+    // next step's rows are written in parts 2 and 6 and its codes fetched once
+    // this one's are decoded.  Past the last step every load is outside and
+    // gives zeros.
     for (int kt = 0; kt < nk; ++kt) {
       const uint16_t* buf = lds[kt & 1];
       uint16_t* next = lds[(kt + 1) & 1];
-      const int k1 = kt * 128 + 128;  // past the last step every load is outside and gives zeros
-      load_x(buf, 0);
-      decode(0);
-      fetch(k1, 0);
-      w.scales(k1, wsn);
+      const int k1 = kt * 128 + 128;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        if (s < 7) {
-          load_x(buf, s + 1);
-          decode(s + 1);
-        }
         if (s == 3) fetch_codes(k1, 0);
-        if (s == 4) {
-          stage(next, 0);
-          fetch(k1, 1);
+        if (s == 7) {
+          fetch_codes(k1, 1);
+          ws[0][0] = ws[1][0];
+          ws[0][1] = ws[1][1];
+          w.scales(k1 + 128, ws[1]);
         }
-        if (s == 6) fetch_codes(k1, 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < MI; ++m)
+        for (int m = 0; m < MI; ++m) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) acc[i][m] = mfma32(wf[s & 1][i], xf[s & 1][m], acc[i][m]);
+          for (int i = 0; i < 2; ++i) acc[i][m] = mfma32(fragment(s, i), xf[m], acc[i][m]);
+          load_x(s < 7 ? buf : next, (s + 1) & 7, m);
+#pragma unroll
+          for (int d = m * 4 / MI; d < (m + 1) * 4 / MI; ++d) decode((s + 1) & 7, ws[0], d);
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            if (i % MI != m) continue;
+            if (s == 2) {
+              stage(i, next, 0);
+              fetch(i, k1, 1);
+            }
+            if (s == 6) stage(i, next, 1);
+            if (s == 7) fetch(i, k1 + 128, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (s == 6) __syncthreads();  // the next step's rows are written, this one's are all read
       }
-      stage(next, 1);
-      ws[0] = wsn[0];
-      ws[1] = wsn[1];
-      __syncthreads();
     }
   }
   if (n0 >= a.N) return;
@@ -181,19 +199,25 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
     }
 }
 
-template <bool MX8, int BLK>
+template <bool MX8, int BLK, bool WORDS>
 static void grouped_go(const MatmulArgs& a, int bm, hipStream_t st) {
   const uint32_t grid = (uint32_t)grouped_grid(a.T, a.ends ? a.E : 0, a.N, bm);
-  if (bm == 128) k_grouped<MX8, BLK, 128><<<grid, 256, 0, st>>>(a);
-  else if (bm == 64) k_grouped<MX8, BLK, 64><<<grid, 256, 0, st>>>(a);
-  else k_grouped<MX8, BLK, 32><<<grid, 256, 0, st>>>(a);
+  if (bm == 128) k_grouped<MX8, BLK, 128, WORDS><<<grid, 256, 0, st>>>(a);
+  else if (bm == 64) k_grouped<MX8, BLK, 64, WORDS><<<grid, 256, 0, st>>>(a);
+  else k_grouped<MX8, BLK, 32, WORDS><<<grid, 256, 0, st>>>(a);
+}
+
+template <bool MX8, int BLK>
+static void grouped_words(const MatmulArgs& a, int bm, hipStream_t st) {
+  if (a.K % 32 == 0 && a.K >= 64) grouped_go<MX8, BLK, true>(a, bm, st);
+  else grouped_go<MX8, BLK, false>(a, bm, st);
 }
 
 int launch_grouped(const MatmulArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   const int bm = grouped_rows(a.T, a.ends ? a.E : 1);
 #define NV_GR(MX8) \
-  (a.blocks == 0 ? grouped_go<MX8, 0>(a, bm, st) : a.blocks == 1 ? grouped_go<MX8, 1>(a, bm, st) : grouped_go<MX8, 2>(a, bm, st))
+  (a.blocks == 0 ? grouped_words<MX8, 0>(a, bm, st) : a.blocks == 1 ? grouped_words<MX8, 1>(a, bm, st) : grouped_words<MX8, 2>(a, bm, st))
   if (a.xs) NV_GR(true);
   else NV_GR(false);
 #undef NV_GR

@@ -155,6 +155,12 @@ NV_DEV nv_bf8 fp4_to_bf16(uint32_t w, float s) {
   return __builtin_bit_cast(nv_bf8, r);
 }
 
+// The low (h = 0) or high four of eight codes alone.
+NV_DEV nv_u2 fp4_half_to_bf16(uint32_t w, float s, int h) {
+  const nv_f2 a = h ? hw_fp4_values<2>(w) : hw_fp4_values<0>(w), b = h ? hw_fp4_values<3>(w) : hw_fp4_values<1>(w);
+  return (nv_u2){pack_bf16(a.x * s, a.y * s), pack_bf16(b.x * s, b.y * s)};
+}
+
 // Value of byte b (0..3) of a word of e4m3 scales.
 NV_DEV float e4m3_byte(uint32_t w, int b) {
   return b == 0 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 0) : b == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 1)

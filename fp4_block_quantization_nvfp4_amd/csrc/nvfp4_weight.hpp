@@ -88,7 +88,8 @@ struct WeightView {
 // half) takes, of rows l32 and 32 + l32, the 64 codes from k0 + 64 half on as
 // two 16-byte words and their four scales as one.  What lies past N or K reads
 // as code 0 or scale 0.
-template <int BLK>
+// WORDS: rows are whole words of codes and of scales (K % 32 == 0, K >= 64).
+template <int BLK, bool WORDS>
 struct WeightStream {
   nv_buf w, s;
   int K, kb, nb, at;        // at: 64 half
@@ -115,14 +116,14 @@ struct WeightStream {
   NV_DEV nv_u4 codes(int i, int k0, int q) const {
     const int k = k0 + at + 32 * q;
     const uint32_t off = row[i] + (uint32_t)(k / 2);
-    if (K % 32 == 0) return buf16(w, in[i] && k < K ? off : kOutside);
+    if (WORDS) return buf16(w, in[i] && k < K ? off : kOutside);
     const nv_u2 a = buf8(w, in[i] && k < K ? off : kOutside), b = buf8(w, in[i] && k + 16 < K ? off + 8 : kOutside);
     return (nv_u4){a.x, a.y, b.x, b.y};
   }
   // The lane's four scales of both rows, one in a byte.
   NV_DEV void scales(int k0, uint32_t v[2]) const {
     const int b = (k0 + at) / 16;
-    if (BLK == 2 || kb < 4) {
+    if (BLK == 2 || (!WORDS && kb < 4)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t p[4];
