@@ -26,7 +26,7 @@ namespace nvfp4 {
 template <bool MX8, int BLK, int BM, bool WORDS>
 __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   constexpr int MI = BM / 32;
-  __shared__ uint16_t lds[2][BM * 128];
+  __shared__ uint16_t lds[2][(BM < 64 ? 64 : BM) * 128];  // at least 8 KB a wave for the way out
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
   const int ntiles = (a.N + 255) / 256;
 
@@ -34,11 +34,13 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   int e = 0, row0, rows, n_tile;
   {
     RowRange rr = {0, 0, a.T, 0};
-    const int total = a.ends ? count_tiles(a.ends, a.E, a.T, BM) : (a.T + BM - 1) / BM;
-    const int64_t units = (int64_t)total * ntiles, per = (units + 7) / 8;
-    const int64_t slot = blockIdx.x >> 3, unit = (blockIdx.x & 7) * per + slot;
-    if (slot >= per || unit >= units) return;
-    if (a.ends) rr = find_range(a.ends, a.E, a.T, BM, ntiles, unit);
+    int64_t unit;
+    if (a.ends) rr = find_unit(a.ends, a.E, a.T, BM, ntiles, blockIdx.x, unit);
+    else {
+      const int64_t units = (int64_t)((a.T + BM - 1) / BM) * ntiles, share = (units + 7) / 8, slot = blockIdx.x >> 3;
+      unit = (blockIdx.x & 7) * share + slot;
+      if (slot >= share || unit >= units) return;
+    }
     if (rr.rows < 0) return;
     const int mt = (rr.rows + BM - 1) / BM;
     const int local = (int)(unit - (int64_t)rr.before * ntiles), block = local / (8 * ntiles);
@@ -177,26 +179,31 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
       }
     }
   }
+  __syncthreads();  // the rows' buffers are free
   if (n0 >= a.N) return;
-  // a lane holds, of each 32x32 tile, row l32 of x and n = 8 q + 4 half + 0..3
+  // A lane holds, of each 32x32 tile, row l32 of x and n = 8 q + 4 half + 0..3.
+  // 32 rows at a time go through the wave's part of shared memory (16-byte
+  // chunk c of row t at c ^ (t % 16)) and leave as whole rows of 64 n's.
+  nv_f4* out = reinterpret_cast<nv_f4*>(&lds[0][0]) + wave * 512;
+  const int n = n0 + (lane & 15) * 4;
+  float sc[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int r = 0; r < 4; ++r) sc[r] = none || n + r >= a.N ? 0.0f : second_scale(a, e, n + r);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + i * 32 + q * 8 + half * 4;
-      float sc[4];
+  for (int m = 0; m < MI; ++m) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sc[r] = none || n + r >= a.N ? 0.0f : second_scale(a, e, n + r);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int m = 0; m < MI; ++m) {
-        const int t = m * 32 + l32;
-        if (t >= rows) continue;
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = none ? 0.0f : acc[i][m][q * 4 + r] * sc[r];
-        store_out4(a, v[0], v[1], v[2], v[3], row0 + t, n);
-      }
+      for (int q = 0; q < 4; ++q)
+        out[l32 * 16 + ((i * 8 + q * 2 + half) ^ (l32 & 15))] =
+            nv_f4{acc[i][m][q * 4], acc[i][m][q * 4 + 1], acc[i][m][q * 4 + 2], acc[i][m][q * 4 + 3]};
+    const int left = rows - m * 32 < 32 ? rows - m * 32 : 32;
+#pragma unroll 1
+    for (int t = lane >> 4; t < left; t += 4) {
+      const nv_f4 v = out[t * 16 + ((lane & 15) ^ (t & 15))];
+      store_out4(a, v[0] * sc[0], v[1] * sc[1], v[2] * sc[2], v[3] * sc[3], row0 + m * 32 + t, n);
     }
+  }
 }
 
 template <bool MX8, int BLK, bool WORDS>

@@ -144,16 +144,21 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
     stage_x(lx[(s + 1) & 1]);
     __syncthreads();
   }
+  // A lane holds, of each fragment pair (i, m), k = 16 i + 4 grp + 0..3 of n =
+  // 4 l16 + m.  16 n's at a time go through the wave's part of shared memory
+  // (16-byte chunk c of row l16 at c ^ l16) and leave as rows of 128 k's.
+  nv_f4* out = reinterpret_cast<nv_f4*>(&lx[0][0]) + wave * 512;
+  const int k = k0 + (lane & 31) * 4;
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    const int n = nl + m;
-    if (n >= a.N) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = k0 + i * 16 + grp * 4;
-      if (k >= a.K) continue;
+    for (int i = 0; i < 8; ++i) out[l16 * 32 + ((4 * i + grp) ^ l16)] = acc[i][m];
+#pragma unroll 1
+    for (int r = lane >> 5; r < 16; r += 2) {
+      const int n = n0 + wave * 64 + 4 * r + m;
+      const nv_f4 v = out[r * 32 + ((lane & 31) ^ r)];
+      if (n >= a.N || k >= a.K) continue;
       const int64_t at = ((int64_t)e * a.N + n) * a.K + k;
-      const nv_f4 v = acc[i][m];
       if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at) = (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
       else *reinterpret_cast<nv_f4*>((float*)a.dw + at) = v;
     }

@@ -62,32 +62,39 @@ struct RangeScan {
 
 NV_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The range that holds `unit`, where each tile stands for `per` consecutive
-// units; rows = -1 when there are no more.  total gets the number of tiles.
-NV_DEV RowRange find_range(const int* ends, int E, int T, int tile, int64_t per, int64_t unit) {
+// The range in s's current 64 that holds `unit`, where each tile stands for
+// `per` consecutive units; rows = -1 when none does.
+NV_DEV RowRange range_of(const RangeScan& s, int64_t per, int64_t unit) {
   RowRange r = {0, 0, -1, 0};
-  RangeScan s(ends, E, T, tile);
-  while (s.next()) {
-    const bool mine = unit >= (int64_t)s.first * per && unit < (int64_t)(s.first + s.own) * per;
-    const uint64_t vote = __ballot(mine);
-    if (vote) {
-      const int l = __builtin_ctzll(vote);
-      r.e = uniform(s.base - 64 + l);
-      r.row0 = uniform(__shfl(s.begin, l, 64));
-      r.rows = uniform(__shfl(s.count, l, 64));
-      r.before = uniform(__shfl(s.first, l, 64));
-      return r;
-    }
+  const uint64_t vote = __ballot(unit >= (int64_t)s.first * per && unit < (int64_t)(s.first + s.own) * per);
+  if (vote) {
+    const int l = __builtin_ctzll(vote);
+    r.e = uniform(s.base - 64 + l);
+    r.row0 = uniform(__shfl(s.begin, l, 64));
+    r.rows = uniform(__shfl(s.count, l, 64));
+    r.before = uniform(__shfl(s.first, l, 64));
   }
   return r;
 }
 
-// Tiles of all ranges.
-NV_DEV int count_tiles(const int* ends, int E, int T, int tile) {
+// A workgroup's unit of work, `per` units a tile: each XCD (workgroups go to
+// the eight in turn) takes a contiguous run of them.  Sets unit and the range
+// that holds it, rows = -1 for a surplus workgroup.  Up to 63 experts take one
+// scan, more of them two.
+NV_DEV RowRange find_unit(const int* ends, int E, int T, int tile, int64_t per, uint32_t block, int64_t& unit) {
   RangeScan s(ends, E, T, tile);
-  while (s.next()) {
+  s.next();
+  const bool one = s.base > E;
+  while (!one && s.next()) {
   }
-  return uniform(s.tiles);
+  const int64_t units = uniform(s.tiles) * per, share = (units + 7) / 8, slot = block >> 3;
+  unit = (block & 7) * share + slot;
+  RowRange r = {0, 0, -1, 0};
+  if (slot >= share || unit >= units) return r;
+  if (one) return range_of(s, per, unit);
+  RangeScan again(ends, E, T, tile);
+  while (r.rows < 0 && again.next()) r = range_of(again, per, unit);
+  return r;
 }
 
 // Rows of expert e alone (e < E): the running maximum of the ends before it.
