@@ -23,34 +23,13 @@
 
 namespace nvfp4 {
 
-template <bool MX8, int BLK, int BM, bool WORDS>
-__global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
+// The tile of expert e's rows row0 .. row0 + rows - 1 (rows <= BM) and n's from
+// 256 n_tile on; e >= E (rows of no expert) gives zeros.  lds: two buffers of
+// BM x 128, and 8 KB a wave for the way out.
+template <bool MX8, int BLK, int BM>
+NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0, int rows, int n_tile) {
   constexpr int MI = BM / 32;
-  __shared__ uint16_t lds[2][(BM < 64 ? 64 : BM) * 128];  // at least 8 KB a wave for the way out
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
-  const int ntiles = (a.N + 255) / 256;
-
-  // this workgroup's tile
-  int e = 0, row0, rows, n_tile;
-  {
-    RowRange rr = {0, 0, a.T, 0};
-    int64_t unit;
-    if (a.ends) rr = find_unit(a.ends, a.E, a.T, BM, ntiles, blockIdx.x, unit);
-    else {
-      const int64_t units = (int64_t)((a.T + BM - 1) / BM) * ntiles, share = (units + 7) / 8, slot = blockIdx.x >> 3;
-      unit = (blockIdx.x & 7) * share + slot;
-      if (slot >= share || unit >= units) return;
-    }
-    if (rr.rows < 0) return;
-    const int mt = (rr.rows + BM - 1) / BM;
-    const int local = (int)(unit - (int64_t)rr.before * ntiles), block = local / (8 * ntiles);
-    const int in = local - block * 8 * ntiles, bm = mt - block * 8 < 8 ? mt - block * 8 : 8;
-    n_tile = in / bm;
-    const int m_tile = block * 8 + in % bm;
-    e = rr.e;
-    row0 = rr.row0 + m_tile * BM;
-    rows = rr.rows - m_tile * BM < BM ? rr.rows - m_tile * BM : BM;
-  }
   const bool none = a.ends && e >= a.E;
   const int n0 = n_tile * 256 + wave * 64;
 
@@ -64,22 +43,23 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
 
   const int nk = none ? 0 : (a.K + 127) / 128;
   if (nk) {
-    const WeightStream<BLK, WORDS> w(a, e, n0, l32, half);
+    const WeightStream<BLK> w(a, e, n0, l32, half);
     const RowsView<MX8> x(a, row0, rows);
-    // staging of half a step's rows: 16-byte pieces, piece p of a row
+    // staging of half a step's rows: 16-byte pieces, PR a row
     constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
+    const int xr = tid / PR, xp = tid % PR;
+    const uint32_t pitch = MX8 ? (uint32_t)a.K : 2u * (uint32_t)a.K;
+    const uint32_t xat = (uint32_t)xr * pitch + (uint32_t)xp * 16u, sat = (uint32_t)(xr * x.ns + xp / 2);
     nv_u4 st[PIECES];
     uint32_t sts[PIECES];
-    auto fetch = [&](int i, int k0, int h) {
-      const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
-      if (HALF < 256 && id >= HALF) return;
-      if (MX8) {
-        const int k = k0 + p * 16;
-        st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) : kOutside);
-        sts[i] = buf1(x.s, k < a.K ? (uint32_t)(r * x.ns + k / kMxGroup) : kOutside);
-      } else {
-        const int k = k0 + p * 8;
-        st[i] = buf16(x.x, k < a.K ? (uint32_t)(r * a.K + k) * 2u : kOutside);
+    auto fetch = [&](int k0, int h) {
+      if (HALF < 256 && tid >= HALF) return;
+      const bool in = k0 + 128 <= a.K || k0 + xp * (MX8 ? 16 : 8) < a.K;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const uint32_t r = (uint32_t)(h * (BM / 2) + i * (256 / PR));
+        st[i] = buf16(x.x, in ? xat : kOutside, (uint32_t)k0 * (MX8 ? 1u : 2u) + r * pitch);
+        if (MX8) sts[i] = buf1(x.s, in ? sat : kOutside, (uint32_t)k0 / kMxGroup + r * (uint32_t)x.ns);
       }
     };
     // row r of a buffer: 16 chunks of 16 bytes, chunk c at c ^ (r % 16)
@@ -87,21 +67,21 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
       *reinterpret_cast<nv_u4*>(buf + r * 128 + ((c ^ (r & 15)) * 8)) = v;
     };
     auto stage = [&](int i, uint16_t* buf, int h) {
-      const int id = tid + i * 256, r = h * (BM / 2) + id / PR, p = id % PR;
-      if (HALF < 256 && id >= HALF) return;
+      if (HALF < 256 && tid >= HALF) return;
+      const int r = h * (BM / 2) + i * (256 / PR) + xr;
       if (MX8) {
         const float sc = e8m0_value(sts[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const nv_u2 u = mx8_to_bf16(st[i][2 * j], sc), v = mx8_to_bf16(st[i][2 * j + 1], sc);
-          put(buf, r, 2 * p + j, (nv_u4){u.x, u.y, v.x, v.y});
+          put(buf, r, 2 * xp + j, (nv_u4){u.x, u.y, v.x, v.y});
         }
       } else {
-        put(buf, r, p, st[i]);
+        put(buf, r, xp, st[i]);
       }
     };
     nv_u4 wc[2][2];
-    uint32_t ws[2][2];  // scales of this step and the next
+    uint32_t ws[2], wsn[4];  // scales of this step; of the next as fetched
     nv_u2 wf[2][2][2];
     nv_bf8 xf[MI];
     auto fetch_codes = [&](int k0, int q) {
@@ -109,8 +89,8 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
       for (int i = 0; i < 2; ++i) wc[i][q] = w.codes(i, k0, q);
     };
     // quarter d of the weight fragments of k's 8 s .. 8 s + 7 of each half
-    auto decode = [&](int s, const uint32_t v[2], int d) {
-      wf[s & 1][d >> 1][d & 1] = fp4_half_to_bf16(wc[d >> 1][s >> 2][s & 3], e4m3_byte(v[d >> 1], s >> 1), d & 1);
+    auto decode = [&](int s, int d) {
+      wf[s & 1][d >> 1][d & 1] = fp4_half_to_bf16(wc[d >> 1][s >> 2][s & 3], e4m3_byte(ws[d >> 1], s >> 1), d & 1);
     };
     auto load_x = [&](const uint16_t* buf, int s, int m) {
       xf[m] = *reinterpret_cast<const nv_bf8*>(buf + (m * 32 + l32) * 128 + (((8 * half + s) ^ (l32 & 15)) * 8));
@@ -121,39 +101,36 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
     };
     fetch_codes(0, 0);
     fetch_codes(0, 1);
-    w.scales(0, ws[0]);
+    w.fetch_scales(0, wsn);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      fetch(0, h);
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) fetch(i, 0, h);
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) stage(i, lds[0], h);
+      for (int i = 0; i < PIECES; ++i) stage(i, lds, h);
     }
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) fetch(i, 128, 0);
-    w.scales(128, ws[1]);
+    fetch(128, 0);
+    w.scales(wsn, ws);
+    w.fetch_scales(128, wsn);
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MI; ++m) load_x(lds[0], 0, m);
+    for (int m = 0; m < MI; ++m) load_x(lds, 0, m);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) decode(0, ws[0], d);
+    for (int d = 0; d < 4; ++d) decode(0, d);
     // Eight parts of 16 k's a step.  While the matrix cores work on part s,
     // part s + 1 is read and decoded, a piece after each pair of products; the
     // next step's rows are written in parts 2 and 6 and its codes fetched once
-    // this one's are decoded.  Past the last step every load is outside and
-    // gives zeros.
+    // this one's are decoded.
     for (int kt = 0; kt < nk; ++kt) {
-      const uint16_t* buf = lds[kt & 1];
-      uint16_t* next = lds[(kt + 1) & 1];
+      const uint16_t* buf = lds + (kt & 1) * (BM * 128);
+      uint16_t* next = lds + (~kt & 1) * (BM * 128);
       const int k1 = kt * 128 + 128;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         if (s == 3) fetch_codes(k1, 0);
         if (s == 7) {
           fetch_codes(k1, 1);
-          ws[0][0] = ws[1][0];
-          ws[0][1] = ws[1][1];
-          w.scales(k1 + 128, ws[1]);
+          w.scales(wsn, ws);
+          w.fetch_scales(k1 + 128, wsn);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -162,17 +139,15 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
           for (int i = 0; i < 2; ++i) acc[i][m] = mfma32(fragment(s, i), xf[m], acc[i][m]);
           load_x(s < 7 ? buf : next, (s + 1) & 7, m);
 #pragma unroll
-          for (int d = m * 4 / MI; d < (m + 1) * 4 / MI; ++d) decode((s + 1) & 7, ws[0], d);
+          for (int d = m * 4 / MI; d < (m + 1) * 4 / MI; ++d) decode((s + 1) & 7, d);
 #pragma unroll
           for (int i = 0; i < PIECES; ++i) {
             if (i % MI != m) continue;
-            if (s == 2) {
-              stage(i, next, 0);
-              fetch(i, k1, 1);
-            }
+            if (s == 2) stage(i, next, 0);
             if (s == 6) stage(i, next, 1);
-            if (s == 7) fetch(i, k1 + 128, 0);
           }
+          if (m == MI - 1 && s == 2) fetch(k1, 1);
+          if (m == MI - 1 && s == 7) fetch(k1 + 128, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (s == 6) __syncthreads();  // the next step's rows are written, this one's are all read
@@ -184,7 +159,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   // A lane holds, of each 32x32 tile, row l32 of x and n = 8 q + 4 half + 0..3.
   // 32 rows at a time go through the wave's part of shared memory (16-byte
   // chunk c of row t at c ^ (t % 16)) and leave as whole rows of 64 n's.
-  nv_f4* out = reinterpret_cast<nv_f4*>(&lds[0][0]) + wave * 512;
+  nv_f4* out = reinterpret_cast<nv_f4*>(lds) + wave * 512;
   const int n = n0 + (lane & 15) * 4;
   float sc[4];
 #pragma unroll
@@ -206,25 +181,48 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   }
 }
 
-template <bool MX8, int BLK, bool WORDS>
-static void grouped_go(const MatmulArgs& a, int bm, hipStream_t st) {
-  const uint32_t grid = (uint32_t)grouped_grid(a.T, a.ends ? a.E : 0, a.N, bm);
-  if (bm == 128) k_grouped<MX8, BLK, 128, WORDS><<<grid, 256, 0, st>>>(a);
-  else if (bm == 64) k_grouped<MX8, BLK, 64, WORDS><<<grid, 256, 0, st>>>(a);
-  else k_grouped<MX8, BLK, 32, WORDS><<<grid, 256, 0, st>>>(a);
+// BM: rows of a unit of work.  Units past the last whole round of the chip
+// (kGroupedSlots workgroups) are split among more workgroups, as long as
+// these fit: by four where they fill up to a quarter of a round, by two up to
+// a half.  A tile with few rows takes the path made for as many.
+template <bool MX8, int BLK, int BM>
+__global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
+  __shared__ uint16_t lds[2 * (BM < 64 ? 64 : BM) * 128];
+  const int ntiles = (a.N + 255) / 256;
+  int64_t unit;
+  int part;
+  RowRange rr = {0, 0, a.T, 0};
+  if (a.ends) rr = find_unit<BM == 128>(a.ends, a.E, a.T, BM, ntiles, blockIdx.x, unit, part);
+  else if (!unit_of_block<BM == 128>((int64_t)((a.T + BM - 1) / BM) * ntiles, blockIdx.x, unit, part)) return;
+  if (rr.rows < 0) return;
+  // units of a range are numbered in blocks of eight row tiles
+  const int mt = (rr.rows + BM - 1) / BM;
+  const int local = (int)(unit - (int64_t)rr.before * ntiles), block = local / (8 * ntiles);
+  const int in = local - block * 8 * ntiles, bm = mt - block * 8 < 8 ? mt - block * 8 : 8;
+  const int n_tile = in / bm, m_tile = block * 8 + in % bm;
+  const int split = part >> 8, of = split ? BM / split : BM;  // rows of a workgroup
+  const int first = m_tile * BM + (part & 255) * of;
+  const int rows = rr.rows - first < of ? rr.rows - first : of;
+  if (rows <= 0) return;
+  const int64_t row0 = (int64_t)rr.row0 + first;
+  if (BM == 128 && rows > 64) grouped_tile<MX8, BLK, BM>(a, lds, rr.e, row0, rows, n_tile);
+  else if (BM >= 64 && rows > 32) grouped_tile<MX8, BLK, BM < 64 ? BM : 64>(a, lds, rr.e, row0, rows, n_tile);
+  else grouped_tile<MX8, BLK, 32>(a, lds, rr.e, row0, rows, n_tile);
 }
 
 template <bool MX8, int BLK>
-static void grouped_words(const MatmulArgs& a, int bm, hipStream_t st) {
-  if (a.K % 32 == 0 && a.K >= 64) grouped_go<MX8, BLK, true>(a, bm, st);
-  else grouped_go<MX8, BLK, false>(a, bm, st);
+static void grouped_go(const MatmulArgs& a, int bm, hipStream_t st) {
+  const uint32_t grid = (uint32_t)grouped_grid(a.T, a.ends ? a.E : 0, a.N, bm);
+  if (bm == 128) k_grouped<MX8, BLK, 128><<<grid, 256, 0, st>>>(a);
+  else if (bm == 64) k_grouped<MX8, BLK, 64><<<grid, 256, 0, st>>>(a);
+  else k_grouped<MX8, BLK, 32><<<grid, 256, 0, st>>>(a);
 }
 
 int launch_grouped(const MatmulArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   const int bm = grouped_rows(a.T, a.ends ? a.E : 1);
 #define NV_GR(MX8) \
-  (a.blocks == 0 ? grouped_words<MX8, 0>(a, bm, st) : a.blocks == 1 ? grouped_words<MX8, 1>(a, bm, st) : grouped_words<MX8, 2>(a, bm, st))
+  (a.blocks == 0 ? grouped_go<MX8, 0>(a, bm, st) : a.blocks == 1 ? grouped_go<MX8, 1>(a, bm, st) : grouped_go<MX8, 2>(a, bm, st))
   if (a.xs) NV_GR(true);
   else NV_GR(false);
 #undef NV_GR

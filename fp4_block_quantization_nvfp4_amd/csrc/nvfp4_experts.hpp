@@ -6,6 +6,7 @@
 #pragma once
 
 #include "nvfp4_mx8.hpp"
+#include "nvfp4_plan.hpp"
 
 namespace nvfp4 {
 
@@ -77,20 +78,38 @@ NV_DEV RowRange range_of(const RangeScan& s, int64_t per, int64_t unit) {
   return r;
 }
 
-// A workgroup's unit of work, `per` units a tile: each XCD (workgroups go to
-// the eight in turn) takes a contiguous run of them.  Sets unit and the range
-// that holds it, rows = -1 for a surplus workgroup.  Up to 63 experts take one
+// A workgroup's unit of work among `units`; false for a surplus workgroup.
+// Each XCD (workgroups go to the eight in turn) takes a contiguous run.  With
+// SPLIT the units past the last whole round of kGroupedSlots are shared by two
+// or four workgroups each, as long as these fit into a round: part is then the
+// number of parts times 256 plus the workgroup's own, else 0.
+template <bool SPLIT>
+NV_DEV bool unit_of_block(int64_t units, uint32_t block, int64_t& unit, int& part) {
+  const int64_t over = SPLIT ? units % kGroupedSlots : 0;
+  const int split = over * 4 <= kGroupedSlots ? 4 : over * 2 <= kGroupedSlots ? 2 : 1;
+  const int64_t whole = units - (split > 1 ? over : 0), share = (whole + 7) / 8, slot = block >> 3;
+  part = 0;
+  unit = (block & 7) * share + slot;
+  if (slot < share) return unit < whole;
+  if (!SPLIT || split == 1) return false;
+  const int64_t parts = over * split, more = (parts + 7) / 8, p = (block & 7) * more + slot - share;
+  unit = whole + p / split;
+  part = split * 256 + (int)(p % split);
+  return slot - share < more && p < parts;
+}
+
+// The unit of a workgroup, `per` units a tile of a range, and the range that
+// holds it, rows = -1 for a surplus workgroup.  Up to 63 experts take one
 // scan, more of them two.
-NV_DEV RowRange find_unit(const int* ends, int E, int T, int tile, int64_t per, uint32_t block, int64_t& unit) {
+template <bool SPLIT>
+NV_DEV RowRange find_unit(const int* ends, int E, int T, int tile, int64_t per, uint32_t block, int64_t& unit, int& part) {
   RangeScan s(ends, E, T, tile);
   s.next();
   const bool one = s.base > E;
   while (!one && s.next()) {
   }
-  const int64_t units = uniform(s.tiles) * per, share = (units + 7) / 8, slot = block >> 3;
-  unit = (block & 7) * share + slot;
   RowRange r = {0, 0, -1, 0};
-  if (slot >= share || unit >= units) return r;
+  if (!unit_of_block<SPLIT>(uniform(s.tiles) * per, block, unit, part)) return r;
   if (one) return range_of(s, per, unit);
   RangeScan again(ends, E, T, tile);
   while (r.rows < 0 && again.next()) r = range_of(again, per, unit);

@@ -193,10 +193,13 @@ NV_DEV nv_buf make_buf(const void* p, uint32_t bytes) {
                                            __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer (all are below 2^31 bytes)
-NV_DEV nv_u4 buf16(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0); }
-NV_DEV nv_u2 buf8(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0); }
-NV_DEV uint32_t buf4(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0); }
-NV_DEV uint32_t buf1(nv_buf b, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b8(b, (int)off, 0, 0); }
+// off is a lane's own offset, base one that all lanes share (kept in a scalar,
+// so a walk along a row costs no vector instruction); their sum is what is
+// checked against the buffer, word by word in a wide load.
+NV_DEV nv_u4 buf16(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, (int)base, 0); }
+NV_DEV nv_u2 buf8(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, (int)base, 0); }
+NV_DEV uint32_t buf4(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)base, 0); }
+NV_DEV uint32_t buf1(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b8(b, (int)off, (int)base, 0); }
 
 // ------------------------------------------------------------ reductions
 

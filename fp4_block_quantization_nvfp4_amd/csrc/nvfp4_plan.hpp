@@ -143,12 +143,16 @@ inline int grouped_rows(int64_t T, int64_t E) {
   const int64_t per = T / (E > 0 ? E : 1);
   return per >= 128 ? 128 : per >= 64 ? 64 : 32;
 }
-// Upper bound of k_grouped's tiles for E experts and the rows of none (E = 0:
-// all rows in one range): each range adds less than one tile to T / bm.
+// Workgroups of k_grouped that run at a time: two on each of 256 CUs.
+constexpr int kGroupedSlots = 512;
+// Upper bound of k_grouped's workgroups for E experts and the rows of none (E
+// = 0: all rows in one range): each range adds less than one tile to T / bm,
+// and units that are split in four (up to a quarter of the slots) or two (up
+// to a half) add at most three quarters of the slots.
 inline int64_t grouped_grid(int64_t T, int64_t E, int64_t N, int64_t bm) {
   int64_t m = ceil_div(T, bm) + E;
   if (m > T) m = T;
-  return xcd_grid(m * ceil_div(N, 256));
+  return xcd_grid(m * ceil_div(N, 256)) + (bm == 128 ? kGroupedSlots * 3 / 4 : 0);
 }
 
 }  // namespace nvfp4

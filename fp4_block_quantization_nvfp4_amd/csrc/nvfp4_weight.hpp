@@ -86,60 +86,77 @@ struct WeightView {
 
 // A wave's walk along k in steps of 128 over 64 rows of a weight: lane (l32,
 // half) takes, of rows l32 and 32 + l32, the 64 codes from k0 + 64 half on as
-// two 16-byte words and their four scales as one.  What lies past N or K reads
-// as code 0 or scale 0.
-// WORDS: rows are whole words of codes and of scales (K % 32 == 0, K >= 64).
-template <int BLK, bool WORDS>
+// two 16-byte words and their four scales as one.  Steps that lie within K
+// take their offset along k from a scalar; the last, partial one is checked
+// lane by lane.  Past N and K the scales read as 0 (the codes there are
+// whatever the next row holds).
+template <int BLK>
 struct WeightStream {
   nv_buf w, s;
-  int K, kb, nb, at;        // at: 64 half
-  uint32_t row[2], srow[2]; // byte offsets of the lane's rows
-  bool in[2];
+  int K, kb, nb, at;         // at: 64 half
+  uint32_t row[2], srow[2];  // byte offsets of the lane's rows; BLK 2: srow[i] is the lane's byte of a word of four tiles
   NV_DEV WeightStream(const MatmulArgs& a, int e, int n0, int l32, int half)
       : K(a.K), kb(a.K / 16), nb(a.N / 16), at(64 * half) {
     const int rows = n0 < a.N ? (a.N - n0 < 64 ? a.N - n0 : 64) : 0, t0 = rows ? n0 / 16 : 0, base = rows ? n0 : 0;
+    const int c0 = t0 < nb - 4 ? t0 : nb > 4 ? nb - 4 : 0;  // BLK 2: first of the four tiles that a word holds
     const int64_t NK = (int64_t)a.N * a.K;
     w = make_buf(a.w + e * (NK / 2) + (int64_t)base * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
     if (BLK == 0) s = make_buf(a.ws + e * (NK / 16) + (int64_t)base * kb, (uint32_t)rows * (uint32_t)kb);
     else if (BLK == 1) s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
-    else s = make_buf(a.ws + e * (NK / 256) + t0, rows ? (uint32_t)kb * (uint32_t)nb - (uint32_t)t0 : 0u);
+    else s = make_buf(a.ws + e * (NK / 256) + c0, rows ? (uint32_t)kb * (uint32_t)nb - (uint32_t)c0 : 0u);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 32 + l32;
-      in[i] = r < rows;
-      row[i] = (uint32_t)r * (uint32_t)(K / 2);
-      srow[i] = BLK == 0 ? (uint32_t)r * (uint32_t)kb : BLK == 1 ? (uint32_t)(r / 16) * (uint32_t)kb : (uint32_t)(r / 16);
+      row[i] = r < rows ? (uint32_t)r * (uint32_t)(K / 2) + (uint32_t)at / 2 : kOutside;
+      if (BLK == 2) srow[i] = (uint32_t)(r / 16 + t0 - c0) & 3u;
+      else srow[i] = r < rows ? (uint32_t)(BLK == 0 ? r : r / 16) * (uint32_t)kb : kOutside;
     }
   }
-  // Codes of the lane's k's 32 q .. 32 q + 31.  A row ends inside a word where
-  // K % 32 == 16: two halves then, so that none is read past the last row.
-  NV_DEV nv_u4 codes(int i, int k0, int q) const {
-    const int k = k0 + at + 32 * q;
-    const uint32_t off = row[i] + (uint32_t)(k / 2);
-    if (WORDS) return buf16(w, in[i] && k < K ? off : kOutside);
-    const nv_u2 a = buf8(w, in[i] && k < K ? off : kOutside), b = buf8(w, in[i] && k + 16 < K ? off + 8 : kOutside);
-    return (nv_u4){a.x, a.y, b.x, b.y};
-  }
-  // The lane's four scales of both rows, one in a byte.
-  NV_DEV void scales(int k0, uint32_t v[2]) const {
+  // Codes of the lane's k's 32 q .. 32 q + 31 of row i.
+  NV_DEV nv_u4 codes(int i, int k0, int q) const { return buf16(w, row[i] + 16u * q, (uint32_t)k0 / 2); }
+  // What the lane's four scales of both rows are made from (`scales`).
+  NV_DEV void fetch_scales(int k0, uint32_t v[4]) const {
     const int b = (k0 + at) / 16;
-    if (BLK == 2 || (!WORDS && kb < 4)) {
+    if (BLK == 2) {
+      if (nb >= 4) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t p[4];
+        for (int j = 0; j < 4; ++j)
+          v[j] = buf4(s, b + j < kb ? (uint32_t)(at / 16) * (uint32_t)nb : kOutside, (uint32_t)(k0 / 16 + j) * (uint32_t)nb);
+      } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t off = BLK == 2 ? (uint32_t)(b + j) * (uint32_t)nb + srow[i] : srow[i] + (uint32_t)(b + j);
-          p[j] = buf1(s, in[i] && b + j < kb ? off : kOutside);
-        }
-        v[i] = p[0] | p[1] << 8 | p[2] << 16 | p[3] << 24;
-      }
-      return;
-    }
-    // the last word of a row starts at its fourth last byte: shifted down, it has zeros past the row
-    const int c = b < kb - 4 ? b : kb - 4, d = b - c;
+          v[j] = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = buf4(s, in[i] && b < kb ? srow[i] + (uint32_t)c : kOutside) >> (8 * (d & 3));
+          for (int t = 0; t < 3; ++t) v[j] |= buf1(s, t < nb && b + j < kb ? (uint32_t)(b + j) * (uint32_t)nb + t : kOutside) << (8 * t);
+        }
+      }
+    } else if (k0 + 128 <= K) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = buf4(s, srow[i] + (uint32_t)at / 16, (uint32_t)k0 / 16);
+    } else if (kb >= 4) {
+      // the last word of a row starts at its fourth last byte: shifted down, it has zeros past the row
+      const int c = b < kb - 4 ? b : kb - 4, d = b - c;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = buf4(s, b < kb ? srow[i] + (uint32_t)c : kOutside) >> (8 * (d & 3));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) v[i] |= buf1(s, b + j < kb ? srow[i] + (uint32_t)(b + j) : kOutside) << (8 * j);
+      }
+    }
+  }
+  NV_DEV void scales(const uint32_t v[4], uint32_t ws[2]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (BLK != 2) {
+        ws[i] = v[i];
+        continue;
+      }
+      const uint32_t pick = srow[i] | (4u + srow[i]) << 8;  // that byte of two words; 0x0c gives zero
+      ws[i] = __builtin_amdgcn_perm(v[1], v[0], 0x0c0c0000u | pick) | __builtin_amdgcn_perm(v[3], v[2], pick << 16 | 0x0c0cu);
+    }
   }
 };
 
