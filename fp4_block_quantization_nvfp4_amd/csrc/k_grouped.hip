@@ -182,9 +182,9 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
 }
 
 // BM: rows of a unit of work.  Units past the last whole round of the chip
-// (kGroupedSlots workgroups) are split among more workgroups, as long as
-// these fit: by four where they fill up to a quarter of a round, by two up to
-// a half.  A tile with few rows takes the path made for as many.
+// (kGroupedSlots workgroups) are split among more workgroups where each still
+// gets a CU of its own: by four up to an eighth of a round, by two up to a
+// quarter.  A tile with few rows takes the path made for as many.
 template <bool MX8, int BLK, int BM>
 __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   __shared__ uint16_t lds[2 * (BM < 64 ? 64 : BM) * 128];

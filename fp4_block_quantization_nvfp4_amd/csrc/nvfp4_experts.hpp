@@ -81,12 +81,12 @@ NV_DEV RowRange range_of(const RangeScan& s, int64_t per, int64_t unit) {
 // A workgroup's unit of work among `units`; false for a surplus workgroup.
 // Each XCD (workgroups go to the eight in turn) takes a contiguous run.  With
 // SPLIT the units past the last whole round of kGroupedSlots are shared by two
-// or four workgroups each, as long as these fit into a round: part is then the
-// number of parts times 256 plus the workgroup's own, else 0.
+// or four workgroups each, as long as each of these has a CU of its own: part
+// is then the number of parts times 256 plus the workgroup's own, else 0.
 template <bool SPLIT>
 NV_DEV bool unit_of_block(int64_t units, uint32_t block, int64_t& unit, int& part) {
   const int64_t over = SPLIT ? units % kGroupedSlots : 0;
-  const int split = over * 4 <= kGroupedSlots ? 4 : over * 2 <= kGroupedSlots ? 2 : 1;
+  const int split = over * 8 <= kGroupedSlots ? 4 : over * 4 <= kGroupedSlots ? 2 : 1;
   const int64_t whole = units - (split > 1 ? over : 0), share = (whole + 7) / 8, slot = block >> 3;
   part = 0;
   unit = (block & 7) * share + slot;

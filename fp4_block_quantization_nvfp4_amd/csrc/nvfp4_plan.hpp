@@ -147,12 +147,12 @@ inline int grouped_rows(int64_t T, int64_t E) {
 constexpr int kGroupedSlots = 512;
 // Upper bound of k_grouped's workgroups for E experts and the rows of none (E
 // = 0: all rows in one range): each range adds less than one tile to T / bm,
-// and units that are split in four (up to a quarter of the slots) or two (up
-// to a half) add at most three quarters of the slots.
+// and units that are split in four (up to an eighth of the slots) or two (up
+// to a quarter) add at most three eighths of the slots.
 inline int64_t grouped_grid(int64_t T, int64_t E, int64_t N, int64_t bm) {
   int64_t m = ceil_div(T, bm) + E;
   if (m > T) m = T;
-  return xcd_grid(m * ceil_div(N, 256)) + (bm == 128 ? kGroupedSlots * 3 / 4 : 0);
+  return xcd_grid(m * ceil_div(N, 256)) + (bm == 128 ? kGroupedSlots * 3 / 8 : 0);
 }
 
 }  // namespace nvfp4
