@@ -1,4 +1,5 @@
-"""Build libnvfp4.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Build libnvfp4.so (the HIP kernels and the C ABI) and _layer.so (the torch
+binding of the layer operators) in-tree for gfx950.
 
     python -m fp4_block_quantization_nvfp4_amd.build
 
@@ -12,12 +13,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
+BIND = os.path.join(HERE, "_layer.so")
 ARCH = os.environ.get("NVFP4_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [
@@ -50,9 +53,25 @@ def _run(cmd, verbose):
         print(err, file=sys.stderr)
 
 
+def bind_commands(obj: str, out: str):
+    """Compile and link commands of the binding: host code against torch's
+    headers and libnvfp4.so beside it."""
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(os.path.dirname(HERE), "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cxx = os.environ.get("CXX", "g++")
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", abi, *[a for p in inc for a in ("-I", p)],
+             "-c", "-o", obj, os.path.join(HERE, "bind", "layer.cpp")],
+            [cxx, "-shared", "-o", out, obj, "-L", HERE, "-l:libnvfp4.so", "-Wl,-rpath,$ORIGIN", "-L", libs, "-lc10",
+             "-ltorch_cpu", "-ltorch_python"])
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile every source to an object in parallel, then link the shared
-    library; the result replaces LIB atomically."""
+    library and the binding; each result replaces its file atomically."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     inc = ["-I", os.path.join(os.path.dirname(HERE), "include")]
     compile_flags = [f for f in FLAGS if f != "-shared"]
@@ -62,12 +81,17 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
             obj = os.path.join(tmpd, os.path.basename(src) + ".o")
             objs.append(obj)
             cmds.append([hipcc, *compile_flags, *inc, "-c", "-o", obj, src])
+        bind_obj, bind_tmp = os.path.join(tmpd, "layer.o"), BIND + ".tmp"
+        compile_bind, link_bind = bind_commands(bind_obj, bind_tmp)
+        cmds.append(compile_bind)
         with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(cmds)))) as ex:
             for f in [ex.submit(_run, c, verbose) for c in cmds]:
                 f.result()
         tmp = LIB + ".tmp"
         _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
-    os.replace(tmp, LIB)
+        os.replace(tmp, LIB)
+        _run(link_bind, verbose)
+        os.replace(bind_tmp, BIND)
     return LIB
 
 
