@@ -199,6 +199,7 @@ constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer (all 
 NV_DEV nv_u4 buf16(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, (int)base, 0); }
 NV_DEV nv_u2 buf8(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, (int)base, 0); }
 NV_DEV uint32_t buf4(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)base, 0); }
+NV_DEV uint32_t buf2(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b16(b, (int)off, (int)base, 0); }
 NV_DEV uint32_t buf1(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b8(b, (int)off, (int)base, 0); }
 
 // ------------------------------------------------------------ reductions

@@ -128,13 +128,16 @@ constexpr int64_t kNormBwdGroups = 1024;
 inline int64_t norm_bwd_groups(int64_t rows) { return rows < kNormBwdGroups ? rows : kNormBwdGroups; }
 
 // Matrix products.
-constexpr int kMatvecThreads = 512;
+constexpr int kMatvecThreads = 256;
 constexpr int64_t kMatmulMaxK = int64_t(1) << 20;  // a tile's rows stay below 2^31 bytes
 constexpr int64_t kMatmulMaxE = 65534;             // grid y of k_matvec
-// Fragments of 16 n's per workgroup of k_matvec.
-inline int matvec_frags(int64_t N, int64_t E) {
+// Fragments of 16 n's per workgroup of k_matvec: more of them read x less often,
+// fewer spread a small weight over more CUs.  Four of them beside 16 rows of
+// bf16 in flight do not fit the registers (65536 x 7168, 16 rows: 83 us, with
+// two 63), so they take 8-bit rows or up to four rows an expert.
+inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;
-  return tiles >= 4096 ? 4 : tiles >= 1024 ? 2 : 1;
+  return tiles >= 4096 && (mx8 || T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
 }
 // Few rows an expert: weights dominate, k_matvec.
 inline bool use_matvec(int64_t T, int64_t E) { return T <= 16 * E; }

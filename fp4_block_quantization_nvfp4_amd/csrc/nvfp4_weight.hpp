@@ -6,7 +6,7 @@
 
 namespace nvfp4 {
 
-// Rows row0 .. row0 + rows - 1 of x; rows and k's outside read as zeros.
+// Rows row0 .. row0 + rows - 1 of x; rows outside read as zeros.
 template <bool MX8>
 struct RowsView {
   nv_buf x, s;
@@ -16,26 +16,57 @@ struct RowsView {
     x = make_buf((const char*)a.x + row0 * pitch, (uint32_t)(rows * pitch));
     s = make_buf(MX8 ? a.xs + row0 * ns : nullptr, MX8 ? (uint32_t)(rows * ns) : 0u);
   }
-  // k .. k + 31 of row r as four fragments of eight; k % 32 == 0.
-  NV_DEV void load32(int r, int k, nv_bf8 f[4]) const {
+};
+
+// A wave's piece of 256 k's of 16 rows of x.  It is loaded as whole lines of
+// memory, passes through 8 KB of the wave's own shared memory, and is read as
+// fragments: (q, d) holds for lane (l16, grp) the k's 64 grp + 32 q + 8 d .. + 7
+// of row l16.  k's at or past K read as zeros.  Pieces are loaded without
+// branches, also past the last one: what is in flight can then be counted.
+// Where there are few rows (XR, 4 or 16) only those are loaded; the products
+// of the others are not used.
+template <bool MX8, int XR>
+struct RowsPiece {
+  static constexpr int kLanes = MX8 ? 16 : 32, kLoads = XR * kLanes / 64;  // kLanes: lanes to a row
+  nv_u4 c[kLoads];
+  uint32_t s[2];
+  NV_DEV void load(const RowsView<MX8>& v, int lane, int k0) {
+    const int l16 = lane & 15, grp = lane >> 4, at = lane % kLanes;
+    const bool in = k0 + at * (MX8 ? 16 : 8) < v.K;
+    const uint32_t pitch = (uint32_t)v.K * (MX8 ? 1u : 2u), off = in ? (uint32_t)(lane / kLanes) * pitch + 16u * at : kOutside;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) c[i] = buf16(v.x, off, (uint32_t)(i * (64 / kLanes)) * pitch + (uint32_t)k0 * (MX8 ? 1u : 2u));
     if (MX8) {
-      nv_u4 c[2];
+      const int left = v.ns - k0 / kMxGroup - 2 * grp;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c[h] = buf16(x, k + 16 * h < K ? (uint32_t)(r * K + k + 16 * h) : kOutside);
-      const float sc = e8m0_value(buf1(s, k < K ? (uint32_t)(r * ns + k / kMxGroup) : kOutside));
+      for (int q = 0; q < 2; ++q)
+        s[q] = buf1(v.s, q < left ? (uint32_t)(l16 * v.ns + 2 * grp + q) : kOutside, (uint32_t)k0 / kMxGroup);
+    }
+  }
+  // Chunk c of a row lies at c ^ row: neither this nor the reads meet in a bank.
+  NV_DEV void put(nv_u4* lds, int lane) const {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = i * (64 / kLanes) + lane / kLanes;
+      lds[row * kLanes + ((lane % kLanes) ^ row)] = c[i];
+    }
+  }
+  // Fragments (q, 0..3).
+  NV_DEV void fragments(const nv_u4* lds, int lane, int q, nv_bf8 f[4]) const {
+    const int l16 = lane & 15, grp = lane >> 4;
+    if (!MX8) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const nv_u2 p = mx8_to_bf16(c[h][2 * j], sc), q = mx8_to_bf16(c[h][2 * j + 1], sc);
-          f[2 * h + j] = __builtin_bit_cast(nv_bf8, (nv_u4){p.x, p.y, q.x, q.y});
-        }
-      }
-    } else {
+      for (int d = 0; d < 4; ++d) f[d] = __builtin_bit_cast(nv_bf8, lds[l16 * kLanes + ((8 * grp + 4 * q + d) ^ l16)]);
+      return;
+    }
+    const float sc = e8m0_value(s[q]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t off = k + 8 * j < K ? (uint32_t)(r * K + k + 8 * j) * 2u : kOutside;
-        f[j] = __builtin_bit_cast(nv_bf8, buf16(x, off));
+    for (int h = 0; h < 2; ++h) {
+      const nv_u4 w = lds[l16 * kLanes + ((4 * grp + 2 * q + h) ^ l16)];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const nv_u2 a = mx8_to_bf16(w[2 * j], sc), b = mx8_to_bf16(w[2 * j + 1], sc);
+        f[2 * h + j] = __builtin_bit_cast(nv_bf8, (nv_u4){a.x, a.y, b.x, b.y});
       }
     }
   }
@@ -43,44 +74,56 @@ struct RowsView {
 
 // Rows n0 .. n0 + rows - 1 of expert e's weight [N, K]; BLK 0: a scale for
 // 1x16 elements [N, K / 16]; 1: for 16x16 tiles [N / 16, K / 16]; 2: the same
-// tiles stored as those of the transposed weight, [K / 16, N / 16].  Rows and
-// k's outside read as code 0, scale 0.
+// tiles stored as those of the transposed weight, [K / 16, N / 16].
 template <int BLK>
 struct WeightView {
   nv_buf w, s;
   int K, kb, nb;  // kb blocks along k, nb tiles along n
-  int t0;         // BLK 2: first tile along n
-  NV_DEV WeightView(const MatmulArgs& a, int e, int n0, int most) : K(a.K), kb(a.K / 16), nb(a.N / 16), t0(n0 / 16) {
-    const int rows = a.N - n0 < most ? a.N - n0 : most;
+  NV_DEV WeightView(const MatmulArgs& a, int e, int n0, int most) : K(a.K), kb(a.K / 16), nb(a.N / 16) {
+    const int rows = a.N - n0 < most ? a.N - n0 : most, t0 = n0 / 16;
     const int64_t NK = (int64_t)a.N * a.K;
     w = make_buf(a.w + e * (NK / 2) + (int64_t)n0 * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
     if (BLK == 0) s = make_buf(a.ws + e * (NK / 16) + (int64_t)n0 * kb, (uint32_t)rows * (uint32_t)kb);
     else if (BLK == 1)
       s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
-    else s = make_buf(a.ws + e * (NK / 256), (uint32_t)kb * (uint32_t)nb);
+    else s = make_buf(a.ws + e * (NK / 256) + t0, (uint32_t)kb * (uint32_t)nb - (uint32_t)t0);
   }
-  // Codes of k .. k + 31 of row r (k % 32 == 0).
-  NV_DEV nv_u4 codes(int r, int k) const {
-    const uint32_t off = (uint32_t)r * (uint32_t)(K / 2) + (uint32_t)(k / 2);
-    const nv_u2 a = buf8(w, k < K ? off : kOutside), b = buf8(w, k + 16 < K ? off + 8 : kOutside);
-    return (nv_u4){a.x, a.y, b.x, b.y};
+};
+
+// The same piece of rows 16 i .. 16 i + 15 of a weight, through 2 KB.  k's at
+// or past K have code 0 or scale 0.  WORDS: the four scales of a lane are a
+// word (K % 64 == 0; tiles of the transposed weight always take four bytes).
+template <int BLK, bool WORDS>
+struct WeightPiece {
+  static constexpr bool kWord = BLK != 2 && WORDS;
+  nv_u4 c[2];
+  uint32_t s[kWord ? 1 : 4];
+  NV_DEV void load(const WeightView<BLK>& v, int i, int lane, int k0) {
+    const int l16 = lane & 15, grp = lane >> 4, l8 = lane & 7;
+    const uint32_t pitch = (uint32_t)v.K / 2u;
+    const uint32_t off = k0 + 32 * l8 < v.K ? (uint32_t)(lane / 8) * pitch + 16u * l8 : kOutside;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) c[h] = buf16(v.w, off, (uint32_t)(16 * i + 8 * h) * pitch + (uint32_t)k0 / 2u);
+    const int left = v.kb - k0 / 16 - 4 * grp;  // blocks from the lane's first on
+    const uint32_t step = BLK == 2 ? (uint32_t)v.nb : 1u;
+    const uint32_t at = (BLK == 0 ? (uint32_t)l16 * (uint32_t)v.kb : 0u) + 4u * grp * step;
+    const uint32_t base = (BLK == 2 ? (uint32_t)i : (uint32_t)(BLK == 0 ? 16 * i : i) * (uint32_t)v.kb) + (uint32_t)(k0 / 16) * step;
+    if (kWord) s[0] = buf4(v.s, left > 0 ? at : kOutside, base);
+    else
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[kWord ? 0 : j] = buf1(v.s, j < left ? at + j * step : kOutside, base);
   }
-  // Scale byte of the block that holds k (k % 16 == 0) of row r.
-  NV_DEV uint32_t scale(int r, int k) const {
-    const uint32_t b = (uint32_t)(k / 16);
-    const uint32_t off = BLK == 0 ? (uint32_t)r * (uint32_t)kb + b
-                         : BLK == 1 ? (uint32_t)(r / 16) * (uint32_t)kb + b
-                                    : b * (uint32_t)nb + (uint32_t)(t0 + r / 16);
-    return buf1(s, k < K ? off : kOutside);
+  // Turns the codes as loaded into the lane's 64: word d of c[q] is fragment (q, d).
+  NV_DEV void turn(nv_u4* lds, int lane) {
+    const int l16 = lane & 15, grp = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) lds[(8 * h + lane / 8) * 8 + ((lane & 7) ^ (lane / 8))] = c[h];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) c[q] = lds[l16 * 8 + ((2 * grp + q) ^ (l16 & 7))];
   }
-  NV_DEV void load32(int r, int k, nv_bf8 f[4]) const {
-    const nv_u4 c = codes(r, k);
-    const float s0 = __builtin_amdgcn_cvt_f32_fp8((int)scale(r, k), 0);
-    const float s1 = __builtin_amdgcn_cvt_f32_fp8((int)scale(r, k + 16), 0);
-    f[0] = fp4_to_bf16(c[0], s0);
-    f[1] = fp4_to_bf16(c[1], s0);
-    f[2] = fp4_to_bf16(c[2], s1);
-    f[3] = fp4_to_bf16(c[3], s1);
+  NV_DEV nv_bf8 fragment(int q, int d) const {
+    const int b = 2 * q + (d >> 1);
+    return fp4_to_bf16(c[q][d], kWord ? e4m3_byte(s[0], b) : e4m3_byte(s[kWord ? 0 : b], 0));
   }
 };
 
