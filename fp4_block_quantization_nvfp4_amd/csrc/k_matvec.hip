@@ -20,8 +20,8 @@ namespace nvfp4 {
 
 // This wave's share of the products of 16 R rows of the weight with up to XR
 // rows of x; own: its shared memory.
-template <bool MX8, int BLK, bool WORDS, int R, int XR>
-NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk, nv_u4* own, nv_f4 acc[R]) {
+template <bool MX8, int BLK, bool WORDS, int R, int XR, int G>
+NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk, nv_u4* own, nv_f4 acc[R][G]) {
   constexpr int W = kMatvecThreads / 64;
   const int lane = threadIdx.x & 63;
   RowsPiece<MX8, XR> xp;
@@ -46,20 +46,39 @@ NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk
     __builtin_amdgcn_sched_barrier(0);  // in flight during all of the products
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      nv_bf8 xf[4];
-      now.fragments(own, lane, q, xf);
+      if (RowsPiece<MX8, XR>::G == 1) {
+        nv_bf8 xf[4];
+        now.fragments(own, lane, 0, q, xf);
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
+        for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = mfma16(wp[r].fragment(q, d), xf[d], acc[r]);
+          for (int r = 0; r < R; ++r) acc[r][0] = mfma16(wp[r].fragment(q, d), xf[d], acc[r][0]);
+      } else {
+        nv_bf8 wf[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) wf[r][d] = wp[r].fragment(q, d);
+#pragma unroll
+        for (int g = 0; g < RowsPiece<MX8, XR>::G; ++g) {
+          nv_bf8 xf[4];
+          now.fragments(own, lane, g, q, xf);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[r][g] = mfma16(wf[r][d], xf[d], acc[r][g]);
+        }
+      }
     }
   }
 }
 
-template <bool MX8, int BLK, bool WORDS, int R, bool GROUPED>
-__global__ __launch_bounds__(kMatvecThreads, 3) void k_matvec(MatmulArgs a) {
-  constexpr int W = kMatvecThreads / 64, SPAN = MX8 && R < 4 ? 256 : 512;  // SPAN: 16-byte chunks of a wave's own memory
-  static_assert(SPAN >= R * 128, "the codes fit where x goes, and so do the sums");
+// XM: rows of x that are taken at a time, 16 or 32.
+template <bool MX8, int BLK, bool WORDS, int R, int XM, bool GROUPED>
+__global__ __launch_bounds__(kMatvecThreads, XM == 16 ? 3 : 2) void k_matvec(MatmulArgs a) {
+  constexpr int W = kMatvecThreads / 64, G = XM / 16;
+  constexpr int ROWS = XM * (MX8 ? 16 : 32), SPAN = ROWS > R * 128 ? ROWS : R * 128;  // SPAN: 16-byte chunks of a wave's own memory
+  static_assert(SPAN >= R * G * 64, "the sums fit where codes and rows go");
   __shared__ nv_u4 lds[W * SPAN];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int n0 = (int)blockIdx.x * (16 * R);
@@ -73,54 +92,65 @@ __global__ __launch_bounds__(kMatvecThreads, 3) void k_matvec(MatmulArgs a) {
   const WeightView<BLK> w(a, none ? 0 : rr.e, n0, 16 * R);
   const int nk = none ? 0 : (a.K + 255) / 256;
   nv_u4* own = lds + wave * SPAN;
-  for (int t0 = 0; t0 < rr.rows; t0 += 16) {
-    const int row0 = rr.row0 + t0, rows = rr.rows - t0 < 16 ? rr.rows - t0 : 16;
+  for (int t0 = 0; t0 < rr.rows; t0 += XM) {
+    const int row0 = rr.row0 + t0, rows = rr.rows - t0 < XM ? rr.rows - t0 : XM;
     const RowsView<MX8> x(a, row0, rows);
-    nv_f4 acc[R];
+    nv_f4 acc[R][G];
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (rows <= 4) matvec_sums<MX8, BLK, WORDS, R, 4>(x, w, nk, own, acc);
-    else matvec_sums<MX8, BLK, WORDS, R, 16>(x, w, nk, own, acc);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[r][g] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (XM == 32 && rows > 16) matvec_sums<MX8, BLK, WORDS, R, XM, G>(x, w, nk, own, acc);
+    else if (XM == 32 || rows > 4) matvec_sums<MX8, BLK, WORDS, R, 16, G>(x, w, nk, own, acc);
+    else matvec_sums<MX8, BLK, WORDS, R, 4, G>(x, w, nk, own, acc);
     float* sums = reinterpret_cast<float*>(lds);  // of wave v: at v * SPAN * 4
 #pragma unroll
-    for (int r = 0; r < R; ++r) reinterpret_cast<nv_f4*>(own)[r * 64 + lane] = acc[r];
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int g = 0; g < G; ++g) reinterpret_cast<nv_f4*>(own)[(r * G + g) * 64 + lane] = acc[r][g];
     __syncthreads();
-    for (int i = threadIdx.x; i < R * 256; i += kMatvecThreads) {
-      // lane l of the tile holds rows 4 (l / 16) + i % 4 of the weight for row l % 16 of x
-      const int r = i >> 8, l = (i >> 2) & 63;
-      const int n = n0 + r * 16 + (l >> 4) * 4 + (i & 3), t = l & 15;
+    for (int i = threadIdx.x; i < R * G * 256; i += kMatvecThreads) {
+      // lane l of a tile holds rows 4 (l / 16) + i % 4 of the weight for row l % 16 of x
+      const int r = (i >> 8) / G, g = (i >> 8) % G, l = (i >> 2) & 63;
+      const int n = n0 + r * 16 + (l >> 4) * 4 + (i & 3), t = g * 16 + (l & 15);
       if (n >= a.N || t >= rows) continue;
       float s = 0.0f;
 #pragma unroll
       for (int v = 0; v < W; ++v) s += sums[v * SPAN * 4 + i];
       store_out(a, none ? 0.0f : s * second_scale(a, rr.e, n), row0 + t, n);
     }
-    if (t0 + 16 < rr.rows) __syncthreads();  // the sums are read before the next rows go where they lie
+    if (t0 + XM < rr.rows) __syncthreads();  // the sums are read before the next rows go where they lie
   }
 }
 
-template <bool MX8, int BLK, bool WORDS, int R>
+template <bool MX8, int BLK, bool WORDS, int R, int XM>
 static void matvec_go(const MatmulArgs& a, hipStream_t st) {
   const dim3 grid((uint32_t)ceil_div(a.N, 16 * R), a.ends ? (uint32_t)a.E + 1 : 1);
-  if (a.ends) k_matvec<MX8, BLK, WORDS, R, true><<<grid, kMatvecThreads, 0, st>>>(a);
-  else k_matvec<MX8, BLK, WORDS, R, false><<<grid, kMatvecThreads, 0, st>>>(a);
+  if (a.ends) k_matvec<MX8, BLK, WORDS, R, XM, true><<<grid, kMatvecThreads, 0, st>>>(a);
+  else k_matvec<MX8, BLK, WORDS, R, XM, false><<<grid, kMatvecThreads, 0, st>>>(a);
+}
+
+template <bool MX8, int BLK, bool WORDS>
+static void matvec_size(const MatmulArgs& a, int r, bool more, hipStream_t st) {
+  if (more) r >= 2 ? matvec_go<MX8, BLK, WORDS, 2, 32>(a, st) : matvec_go<MX8, BLK, WORDS, 1, 32>(a, st);
+  else if (r == 4) matvec_go<MX8, BLK, WORDS, 4, 16>(a, st);
+  else r == 2 ? matvec_go<MX8, BLK, WORDS, 2, 16>(a, st) : matvec_go<MX8, BLK, WORDS, 1, 16>(a, st);
 }
 
 template <bool MX8>
-static void matvec_blk(const MatmulArgs& a, int r, hipStream_t st) {
+static void matvec_blk(const MatmulArgs& a, int r, bool more, hipStream_t st) {
   const bool words = a.K % 64 == 0;
-#define NV_MV(B, P) \
-  (r == 4 ? matvec_go<MX8, B, P, 4>(a, st) : r == 2 ? matvec_go<MX8, B, P, 2>(a, st) : matvec_go<MX8, B, P, 1>(a, st))
-  if (a.blocks == 0) words ? NV_MV(0, true) : NV_MV(0, false);
-  else if (a.blocks == 1) words ? NV_MV(1, true) : NV_MV(1, false);
-  else NV_MV(2, false);
-#undef NV_MV
+  if (a.blocks == 0) words ? matvec_size<MX8, 0, true>(a, r, more, st) : matvec_size<MX8, 0, false>(a, r, more, st);
+  else if (a.blocks == 1) words ? matvec_size<MX8, 1, true>(a, r, more, st) : matvec_size<MX8, 1, false>(a, r, more, st);
+  else matvec_size<MX8, 2, false>(a, r, more, st);
 }
 
 int launch_matvec(const MatmulArgs& a, void* stream) {
-  const int r = matvec_frags(a.T, a.N, a.ends ? a.E : 1, a.xs != nullptr);
-  if (a.xs) matvec_blk<true>(a, r, (hipStream_t)stream);
-  else matvec_blk<false>(a, r, (hipStream_t)stream);
+  const int64_t E = a.ends ? a.E : 1;
+  const int r = matvec_frags(a.T, a.N, E, a.xs != nullptr);
+  const bool more = a.T > 16 * E;
+  if (a.xs) matvec_blk<true>(a, r, more, (hipStream_t)stream);
+  else matvec_blk<false>(a, r, more, (hipStream_t)stream);
   return (int)hipGetLastError();
 }
 

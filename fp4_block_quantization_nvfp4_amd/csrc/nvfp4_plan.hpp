@@ -139,15 +139,24 @@ inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;
   return tiles >= 4096 && (mx8 || T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
 }
-// Few rows an expert: weights dominate, k_matvec.
-inline bool use_matvec(int64_t T, int64_t E) { return T <= 16 * E; }
+// Which kernel: few rows an expert, k_matvec, which decodes the weights for 32
+// rows (16 up to 16 an expert) at a time but spreads them over many more
+// workgroups.  Up to 96 rows an expert it is the faster one while the chip is
+// not filled: it takes about passes E N K / 3.5e6 us for some 1/2 + T / (23 E)
+// passes, k_grouped on a part of the chip 1.3 us for 128 k's.  Measured, us:
+// 8 experts 2048 x 2048, 32 rows each 23 (k_grouped 26), 48 rows 32 (24); 4
+// experts 1040 x 4096, 64 rows each 27 (51); 32 experts 2048 x 4096, 24 rows
+// each 75 (65).
+inline bool use_matvec(int64_t T, int64_t E, int64_t N) {
+  return T <= 16 * E || (T <= 96 * E && N * (E + T / 11) <= 72000);
+}
+// Workgroups of k_grouped that run at a time: two on each of 256 CUs.
+constexpr int kGroupedSlots = 512;
 // Row tile of k_grouped.
 inline int grouped_rows(int64_t T, int64_t E) {
   const int64_t per = T / (E > 0 ? E : 1);
   return per >= 128 ? 128 : per >= 64 ? 64 : 32;
 }
-// Workgroups of k_grouped that run at a time: two on each of 256 CUs.
-constexpr int kGroupedSlots = 512;
 // Upper bound of k_grouped's workgroups for E experts and the rows of none (E
 // = 0: all rows in one range): each range adds less than one tile to T / bm,
 // and units that are split in four (up to an eighth of the slots) or two (up

@@ -18,18 +18,18 @@ struct RowsView {
   }
 };
 
-// A wave's piece of 256 k's of 16 rows of x.  It is loaded as whole lines of
-// memory, passes through 8 KB of the wave's own shared memory, and is read as
-// fragments: (q, d) holds for lane (l16, grp) the k's 64 grp + 32 q + 8 d .. + 7
-// of row l16.  k's at or past K read as zeros.  Pieces are loaded without
-// branches, also past the last one: what is in flight can then be counted.
-// Where there are few rows (XR, 4 or 16) only those are loaded; the products
-// of the others are not used.
+// A wave's piece of 256 k's of XR rows of x.  It is loaded as whole lines of
+// memory, passes through the wave's own shared memory, and is read as
+// fragments: (g, q, d) holds for lane (l16, grp) the k's 64 grp + 32 q + 8 d ..
+// + 7 of row 16 g + l16.  k's at or past K read as zeros.  Pieces are loaded
+// without branches, also past the last one: what is in flight can then be
+// counted.  XR is 4 where there are few rows: the products of the others are
+// not used.
 template <bool MX8, int XR>
 struct RowsPiece {
-  static constexpr int kLanes = MX8 ? 16 : 32, kLoads = XR * kLanes / 64;  // kLanes: lanes to a row
+  static constexpr int kLanes = MX8 ? 16 : 32, kLoads = XR * kLanes / 64, G = XR > 16 ? XR / 16 : 1;  // kLanes: lanes to a row
   nv_u4 c[kLoads];
-  uint32_t s[2];
+  uint32_t s[G][2];
   NV_DEV void load(const RowsView<MX8>& v, int lane, int k0) {
     const int l16 = lane & 15, grp = lane >> 4, at = lane % kLanes;
     const bool in = k0 + at * (MX8 ? 16 : 8) < v.K;
@@ -40,7 +40,10 @@ struct RowsPiece {
       const int left = v.ns - k0 / kMxGroup - 2 * grp;
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        s[q] = buf1(v.s, q < left ? (uint32_t)(l16 * v.ns + 2 * grp + q) : kOutside, (uint32_t)k0 / kMxGroup);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          s[g][q] = buf1(v.s, q < left ? (uint32_t)(l16 * v.ns + 2 * grp + q) : kOutside,
+                         (uint32_t)k0 / kMxGroup + (uint32_t)(16 * g * v.ns));
     }
   }
   // Chunk c of a row lies at c ^ row: neither this nor the reads meet in a bank.
@@ -48,21 +51,21 @@ struct RowsPiece {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = i * (64 / kLanes) + lane / kLanes;
-      lds[row * kLanes + ((lane % kLanes) ^ row)] = c[i];
+      lds[row * kLanes + ((lane % kLanes) ^ (row % kLanes))] = c[i];
     }
   }
-  // Fragments (q, 0..3).
-  NV_DEV void fragments(const nv_u4* lds, int lane, int q, nv_bf8 f[4]) const {
-    const int l16 = lane & 15, grp = lane >> 4;
+  // Fragments (g, q, 0..3).
+  NV_DEV void fragments(const nv_u4* lds, int lane, int g, int q, nv_bf8 f[4]) const {
+    const int row = 16 * g + (lane & 15), grp = lane >> 4;
     if (!MX8) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) f[d] = __builtin_bit_cast(nv_bf8, lds[l16 * kLanes + ((8 * grp + 4 * q + d) ^ l16)]);
+      for (int d = 0; d < 4; ++d) f[d] = __builtin_bit_cast(nv_bf8, lds[row * kLanes + ((8 * grp + 4 * q + d) ^ (row % kLanes))]);
       return;
     }
-    const float sc = e8m0_value(s[q]);
+    const float sc = e8m0_value(s[g][q]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const nv_u4 w = lds[l16 * kLanes + ((4 * grp + 2 * q + h) ^ l16)];
+      const nv_u4 w = lds[row * kLanes + ((4 * grp + 2 * q + h) ^ (row % kLanes))];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const nv_u2 a = mx8_to_bf16(w[2 * j], sc), b = mx8_to_bf16(w[2 * j + 1], sc);
@@ -137,13 +140,15 @@ template <int BLK>
 struct WeightStream {
   nv_buf w, s;
   int K, kb, nb, at;         // at: 64 half
+  uint32_t end;              // bytes of codes
   uint32_t row[2], srow[2];  // byte offsets of the lane's rows; BLK 2: srow[i] is the lane's byte of a word of four tiles
   NV_DEV WeightStream(const MatmulArgs& a, int e, int n0, int l32, int half)
       : K(a.K), kb(a.K / 16), nb(a.N / 16), at(64 * half) {
     const int rows = n0 < a.N ? (a.N - n0 < 64 ? a.N - n0 : 64) : 0, t0 = rows ? n0 / 16 : 0, base = rows ? n0 : 0;
     const int c0 = t0 < nb - 4 ? t0 : nb > 4 ? nb - 4 : 0;  // BLK 2: first of the four tiles that a word holds
     const int64_t NK = (int64_t)a.N * a.K;
-    w = make_buf(a.w + e * (NK / 2) + (int64_t)base * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
+    end = (uint32_t)rows * (uint32_t)(a.K / 2);
+    w = make_buf(a.w + e * (NK / 2) + (int64_t)base * (a.K / 2), end);
     if (BLK == 0) s = make_buf(a.ws + e * (NK / 16) + (int64_t)base * kb, (uint32_t)rows * (uint32_t)kb);
     else if (BLK == 1) s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
     else s = make_buf(a.ws + e * (NK / 256) + c0, rows ? (uint32_t)kb * (uint32_t)nb - (uint32_t)c0 : 0u);
@@ -155,8 +160,8 @@ struct WeightStream {
       else srow[i] = r < rows ? (uint32_t)(BLK == 0 ? r : r / 16) * (uint32_t)kb : kOutside;
     }
   }
-  // Codes of the lane's k's 32 q .. 32 q + 31 of row i.
-  NV_DEV nv_u4 codes(int i, int k0, int q) const { return buf16(w, row[i] + 16u * q, (uint32_t)k0 / 2); }
+  // Codes of the lane's k's 32 q .. 32 q + 31 of row i; nothing is read for a step past K.
+  NV_DEV nv_u4 codes(int i, int k0, int q) const { return buf16(w, row[i] + 16u * q, k0 < K ? (uint32_t)k0 / 2 : end); }
   // What the lane's four scales of both rows are made from (`scales`).
   NV_DEV void fetch_scales(int k0, uint32_t v[4]) const {
     const int b = (k0 + at) / 16;
