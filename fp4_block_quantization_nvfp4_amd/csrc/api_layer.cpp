@@ -122,7 +122,8 @@ static nvfp4_status products(const void* x, const uint8_t* x_scales, int64_t T, 
                              const float* amax, int mode, float bound, void* out, int out_dt, void* stream) {
   const nvfp4::MatmulArgs a = {x, x_scales, packed, scales, amax, ends, out, (int)T, (int)E, (int)N, (int)K,
                                blocks, mode, 6.0f * bound, out_dt == NVFP4_BF16};
-  return hip_status(nvfp4::use_matvec(T, E, N) ? nvfp4::launch_matvec(a, stream) : nvfp4::launch_grouped(a, stream));
+  if (nvfp4::use_matvec(T, E, N)) return hip_status(nvfp4::launch_matvec(a, stream));
+  return hip_status(x_scales ? nvfp4::launch_grouped_mx8(a, stream) : nvfp4::launch_grouped_bf16(a, stream));
 }
 
 nvfp4_status nvfp4_matvec(const void* x, const uint8_t* x_scales, int64_t T, int64_t N, int64_t K,

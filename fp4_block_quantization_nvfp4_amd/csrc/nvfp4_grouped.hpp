@@ -16,6 +16,8 @@
 // and surplus workgroups leave at once.  Tiles are numbered per expert in
 // blocks of 8 row tiles, and each XCD takes a contiguous run of them: what
 // runs at one time on an XCD shares rows of x and weights in its L2.
+#pragma once
+
 #include "nvfp4_experts.hpp"
 #include "nvfp4_launch.hpp"
 #include "nvfp4_plan.hpp"
@@ -24,18 +26,18 @@
 namespace nvfp4 {
 
 // The tile of expert e's rows row0 .. row0 + rows - 1 (rows <= BM) and n's from
-// 256 n_tile on; e >= E (rows of no expert) gives zeros.  lds: two buffers of
-// BM x 128, and 8 KB a wave for the way out.
-template <bool MX8, int BLK, int BM>
+// 128 NI n_tile on; e >= E (rows of no expert) gives zeros.  lds: two buffers
+// of BM x 128, and 4 NI KB a wave for the way out.
+template <bool MX8, int BLK, int BM, int NI>
 NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0, int rows, int n_tile) {
   constexpr int MI = BM / 32;
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
   const bool none = a.ends && e >= a.E;
-  const int n0 = n_tile * 256 + wave * 64;
+  const int n0 = n_tile * (128 * NI) + wave * (32 * NI);
 
-  nv_f16 acc[2][MI];
+  nv_f16 acc[NI][MI];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int m = 0; m < MI; ++m)
 #pragma unroll
@@ -43,7 +45,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
 
   const int nk = none ? 0 : (a.K + 127) / 128;
   if (nk) {
-    const WeightStream<BLK> w(a, e, n0, l32, half);
+    const WeightStream<BLK, NI> w(a, e, n0, l32, half);
     const RowsView<MX8> x(a, row0, rows);
     // staging of half a step's rows: 16-byte pieces, PR a row
     constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
@@ -80,13 +82,13 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
         put(buf, r, xp, st[i]);
       }
     };
-    nv_u4 wc[2][2];
-    uint32_t ws[2], wsn[4];  // scales of this step; of the next as fetched
-    nv_u2 wf[2][2][2];
+    nv_u4 wc[NI][2];
+    uint32_t ws[NI], wsn[4];  // scales of this step; of the next as fetched
+    nv_u2 wf[2][NI][2];
     nv_bf8 xf[MI];
     auto fetch_codes = [&](int k0, int q) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) wc[i][q] = w.codes(i, k0, q);
+      for (int i = 0; i < NI; ++i) wc[i][q] = w.codes(i, k0, q);
     };
     // quarter d of the weight fragments of k's 8 s .. 8 s + 7 of each half
     auto decode = [&](int s, int d) {
@@ -115,7 +117,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
 #pragma unroll
     for (int m = 0; m < MI; ++m) load_x(lds, 0, m);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) decode(0, d);
+    for (int d = 0; d < 2 * NI; ++d) decode(0, d);
     // Eight parts of 16 k's a step.  While the matrix cores work on part s,
     // part s + 1 is read and decoded, a piece after each pair of products; the
     // next step's rows are written in parts 2 and 6 and its codes fetched once
@@ -136,10 +138,10 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) acc[i][m] = mfma32(fragment(s, i), xf[m], acc[i][m]);
+          for (int i = 0; i < NI; ++i) acc[i][m] = mfma32(fragment(s, i), xf[m], acc[i][m]);
           load_x(s < 7 ? buf : next, (s + 1) & 7, m);
 #pragma unroll
-          for (int d = m * 4 / MI; d < (m + 1) * 4 / MI; ++d) decode((s + 1) & 7, d);
+          for (int d = m * 2 * NI / MI; d < (m + 1) * 2 * NI / MI; ++d) decode((s + 1) & 7, d);
 #pragma unroll
           for (int i = 0; i < PIECES; ++i) {
             if (i % MI != m) continue;
@@ -158,24 +160,25 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
   if (n0 >= a.N) return;
   // A lane holds, of each 32x32 tile, row l32 of x and n = 8 q + 4 half + 0..3.
   // 32 rows at a time go through the wave's part of shared memory (16-byte
-  // chunk c of row t at c ^ (t % 16)) and leave as whole rows of 64 n's.
-  nv_f4* out = reinterpret_cast<nv_f4*>(lds) + wave * 512;
-  const int n = n0 + (lane & 15) * 4;
+  // chunk c of row t at c ^ t) and leave as whole rows of 32 NI n's.
+  constexpr int ROW = 8 * NI;  // chunks of a row
+  nv_f4* out = reinterpret_cast<nv_f4*>(lds) + wave * (32 * ROW);
+  const int n = n0 + lane % ROW * 4;
   float sc[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) sc[r] = none || n + r >= a.N ? 0.0f : second_scale(a, e, n + r);
 #pragma unroll
   for (int m = 0; m < MI; ++m) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        out[l32 * 16 + ((i * 8 + q * 2 + half) ^ (l32 & 15))] =
+        out[l32 * ROW + ((i * 8 + q * 2 + half) ^ (l32 % ROW))] =
             nv_f4{acc[i][m][q * 4], acc[i][m][q * 4 + 1], acc[i][m][q * 4 + 2], acc[i][m][q * 4 + 3]};
     const int left = rows - m * 32 < 32 ? rows - m * 32 : 32;
 #pragma unroll 1
-    for (int t = lane >> 4; t < left; t += 4) {
-      const nv_f4 v = out[t * 16 + ((lane & 15) ^ (t & 15))];
+    for (int t = lane / ROW; t < left; t += 64 / ROW) {
+      const nv_f4 v = out[t * ROW + ((lane % ROW) ^ (t % ROW))];
       store_out4(a, v[0] * sc[0], v[1] * sc[1], v[2] * sc[2], v[3] * sc[3], row0 + m * 32 + t, n);
     }
   }
@@ -185,10 +188,10 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
 // (kGroupedSlots workgroups) are split among more workgroups where each still
 // gets a CU of its own: by four up to an eighth of a round, by two up to a
 // quarter.  A tile with few rows takes the path made for as many.
-template <bool MX8, int BLK, int BM>
+template <bool MX8, int BLK, int BM, int NI>
 __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   __shared__ uint16_t lds[2 * (BM < 64 ? 64 : BM) * 128];
-  const int ntiles = (a.N + 255) / 256;
+  const int ntiles = (a.N + 128 * NI - 1) / (128 * NI);
   int64_t unit;
   int part;
   RowRange rr = {0, 0, a.T, 0};
@@ -205,27 +208,30 @@ __global__ __launch_bounds__(256, 2) void k_grouped(MatmulArgs a) {
   const int rows = rr.rows - first < of ? rr.rows - first : of;
   if (rows <= 0) return;
   const int64_t row0 = (int64_t)rr.row0 + first;
-  if (BM == 128 && rows > 64) grouped_tile<MX8, BLK, BM>(a, lds, rr.e, row0, rows, n_tile);
-  else if (BM >= 64 && rows > 32) grouped_tile<MX8, BLK, BM < 64 ? BM : 64>(a, lds, rr.e, row0, rows, n_tile);
-  else grouped_tile<MX8, BLK, 32>(a, lds, rr.e, row0, rows, n_tile);
+  if (BM == 128 && rows > 64) grouped_tile<MX8, BLK, BM, NI>(a, lds, rr.e, row0, rows, n_tile);
+  else if (BM >= 64 && rows > 32) grouped_tile<MX8, BLK, BM < 64 ? BM : 64, NI>(a, lds, rr.e, row0, rows, n_tile);
+  else grouped_tile<MX8, BLK, 32, NI>(a, lds, rr.e, row0, rows, n_tile);
+}
+
+template <bool MX8, int BLK, int NI>
+static void grouped_rows_go(const MatmulArgs& a, const GroupedPlan& p, hipStream_t st) {
+  const uint32_t grid = (uint32_t)p.grid;
+  if (p.rows == 128) k_grouped<MX8, BLK, 128, NI><<<grid, 256, 0, st>>>(a);
+  else if (p.rows == 64) k_grouped<MX8, BLK, 64, NI><<<grid, 256, 0, st>>>(a);
+  else k_grouped<MX8, BLK, 32, NI><<<grid, 256, 0, st>>>(a);
 }
 
 template <bool MX8, int BLK>
-static void grouped_go(const MatmulArgs& a, int bm, hipStream_t st) {
-  const uint32_t grid = (uint32_t)grouped_grid(a.T, a.ends ? a.E : 0, a.N, bm);
-  if (bm == 128) k_grouped<MX8, BLK, 128><<<grid, 256, 0, st>>>(a);
-  else if (bm == 64) k_grouped<MX8, BLK, 64><<<grid, 256, 0, st>>>(a);
-  else k_grouped<MX8, BLK, 32><<<grid, 256, 0, st>>>(a);
+static void grouped_go(const MatmulArgs& a, hipStream_t st) {
+  const GroupedPlan p = plan_grouped(a.T, a.ends ? a.E : 0, a.N);
+  if (p.width == 256) grouped_rows_go<MX8, BLK, 2>(a, p, st);
+  else grouped_rows_go<MX8, BLK, 1>(a, p, st);
 }
 
-int launch_grouped(const MatmulArgs& a, void* stream) {
+template <bool MX8>
+static int grouped_launch(const MatmulArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const int bm = grouped_rows(a.T, a.ends ? a.E : 1);
-#define NV_GR(MX8) \
-  (a.blocks == 0 ? grouped_go<MX8, 0>(a, bm, st) : a.blocks == 1 ? grouped_go<MX8, 1>(a, bm, st) : grouped_go<MX8, 2>(a, bm, st))
-  if (a.xs) NV_GR(true);
-  else NV_GR(false);
-#undef NV_GR
+  a.blocks == 0 ? grouped_go<MX8, 0>(a, st) : a.blocks == 1 ? grouped_go<MX8, 1>(a, st) : grouped_go<MX8, 2>(a, st);
   return (int)hipGetLastError();
 }
 

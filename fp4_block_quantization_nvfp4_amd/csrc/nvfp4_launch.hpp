@@ -61,7 +61,7 @@ int launch_swiglu(const void* gate_up, int in_bf16, int64_t rows, int64_t F, uin
 int launch_swiglu_bwd(const void* dout, int in_bf16, int64_t rows, int64_t F, const uint8_t* kept,
                       const uint8_t* kept_scales, void* dgate_up, void* stream);
 
-// Product of rows with 4-bit weights (k_matvec.hip, k_grouped.hip).
+// Product of rows with 4-bit weights (k_matvec.hip, nvfp4_grouped.hpp).
 struct MatmulArgs {
   const void* x;       // [T, K] bf16, or e4m3 codes when xs is set
   const uint8_t* xs;   // NULL, or [T, ceil(K / 32)] e8m0
@@ -77,7 +77,8 @@ struct MatmulArgs {
   int out_bf16;
 };
 int launch_matvec(const MatmulArgs& a, void* stream);
-int launch_grouped(const MatmulArgs& a, void* stream);
+int launch_grouped_mx8(const MatmulArgs& a, void* stream);
+int launch_grouped_bf16(const MatmulArgs& a, void* stream);
 
 // dw[e] = dy^T x over the rows of each expert (k_wgrad.hip).
 struct WgradArgs {

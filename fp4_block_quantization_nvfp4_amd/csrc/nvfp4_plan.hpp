@@ -139,32 +139,37 @@ inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;
   return tiles >= 4096 && (mx8 || T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
 }
-// Which kernel: few rows an expert, k_matvec, which decodes the weights for 32
-// rows (16 up to 16 an expert) at a time but spreads them over many more
-// workgroups.  Up to 96 rows an expert it is the faster one while the chip is
-// not filled: it takes about passes E N K / 3.5e6 us for some 1/2 + T / (23 E)
-// passes, k_grouped on a part of the chip 1.3 us for 128 k's.  Measured, us:
-// 8 experts 2048 x 2048, 32 rows each 23 (k_grouped 26), 48 rows 32 (24); 4
-// experts 1040 x 4096, 64 rows each 27 (51); 32 experts 2048 x 4096, 24 rows
-// each 75 (65).
+// Which kernel: few rows an expert, k_matvec, which decodes the weights anew
+// for every 32 rows (16 up to 16 an expert) but spreads them over many more
+// workgroups.  Up to 96 rows an expert it is the faster one while there is
+// little to decode: its time grows with N T, and with how uneven the experts
+// are, that of k_grouped on a part of the chip only with k.  Measured, us
+// (k_grouped): 8 experts 2048 x 2048, 20 rows each 16.5 (18.8), 32 rows 23.4
+// (18.7); 4 experts 1040 x 4096, 64 rows each 26 (34), 96 rows 37 (31); 6
+// experts 1024 x 1024, 32 rows each 9.3 (11.6), 64 rows 15.1 (12.7); one of 4096
+// x 4096, 96 rows 20 (31).
 inline bool use_matvec(int64_t T, int64_t E, int64_t N) {
-  return T <= 16 * E || (T <= 96 * E && N * (E + T / 11) <= 72000);
+  return T <= 16 * E || (T <= 96 * E && N * T <= (E > 1 ? 280000 : 600000));
 }
 // Workgroups of k_grouped that run at a time: two on each of 256 CUs.
 constexpr int kGroupedSlots = 512;
-// Row tile of k_grouped.
-inline int grouped_rows(int64_t T, int64_t E) {
+// Tile of k_grouped, rows by n's: rows by what an expert has, and half the n's
+// where wide tiles would leave CUs without one (each decodes half as many
+// weights then; 8 experts 2048 x 2048, 64 rows each: 27.4 -> 19.4 us).  The
+// grid is an upper bound: each of E experts and the rows of none (E = 0: all
+// rows in one range) adds less than one tile to T / rows, and units of 128 rows
+// that are split in four (up to an eighth of the slots) or two (up to a
+// quarter) add at most three eighths of the slots.
+struct GroupedPlan {
+  int rows, width;
+  int64_t grid;
+};
+inline GroupedPlan plan_grouped(int64_t T, int64_t E, int64_t N) {
   const int64_t per = T / (E > 0 ? E : 1);
-  return per >= 128 ? 128 : per >= 64 ? 64 : 32;
-}
-// Upper bound of k_grouped's workgroups for E experts and the rows of none (E
-// = 0: all rows in one range): each range adds less than one tile to T / bm,
-// and units that are split in four (up to an eighth of the slots) or two (up
-// to a quarter) add at most three eighths of the slots.
-inline int64_t grouped_grid(int64_t T, int64_t E, int64_t N, int64_t bm) {
-  int64_t m = ceil_div(T, bm) + E;
-  if (m > T) m = T;
-  return xcd_grid(m * ceil_div(N, 256)) + (bm == 128 ? kGroupedSlots * 3 / 8 : 0);
+  const int rows = per >= 128 ? 128 : per >= 64 ? 64 : 32;
+  const int width = (ceil_div(T, rows) + E / 2) * ceil_div(N, 256) <= kGroupedSlots / 2 ? 128 : 256;
+  const int64_t m = ceil_div(T, rows) + E;
+  return {rows, width, xcd_grid((m < T ? m : T) * ceil_div(N, width)) + (rows == 128 ? kGroupedSlots * 3 / 8 : 0)};
 }
 
 }  // namespace nvfp4

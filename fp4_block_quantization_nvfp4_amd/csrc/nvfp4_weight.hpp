@@ -130,21 +130,21 @@ struct WeightPiece {
   }
 };
 
-// A wave's walk along k in steps of 128 over 64 rows of a weight: lane (l32,
-// half) takes, of rows l32 and 32 + l32, the 64 codes from k0 + 64 half on as
+// A wave's walk along k in steps of 128 over 32 NI rows of a weight: lane
+// (l32, half) takes, of rows 32 i + l32, the 64 codes from k0 + 64 half on as
 // two 16-byte words and their four scales as one.  Steps that lie within K
 // take their offset along k from a scalar; the last, partial one is checked
 // lane by lane.  Past N and K the scales read as 0 (the codes there are
 // whatever the next row holds).
-template <int BLK>
+template <int BLK, int NI>
 struct WeightStream {
   nv_buf w, s;
   int K, kb, nb, at;         // at: 64 half
   uint32_t end;              // bytes of codes
-  uint32_t row[2], srow[2];  // byte offsets of the lane's rows; BLK 2: srow[i] is the lane's byte of a word of four tiles
+  uint32_t row[NI], srow[NI];  // byte offsets of the lane's rows; BLK 2: srow[i] is the lane's byte of a word of four tiles
   NV_DEV WeightStream(const MatmulArgs& a, int e, int n0, int l32, int half)
       : K(a.K), kb(a.K / 16), nb(a.N / 16), at(64 * half) {
-    const int rows = n0 < a.N ? (a.N - n0 < 64 ? a.N - n0 : 64) : 0, t0 = rows ? n0 / 16 : 0, base = rows ? n0 : 0;
+    const int rows = n0 < a.N ? (a.N - n0 < 32 * NI ? a.N - n0 : 32 * NI) : 0, t0 = rows ? n0 / 16 : 0, base = rows ? n0 : 0;
     const int c0 = t0 < nb - 4 ? t0 : nb > 4 ? nb - 4 : 0;  // BLK 2: first of the four tiles that a word holds
     const int64_t NK = (int64_t)a.N * a.K;
     end = (uint32_t)rows * (uint32_t)(a.K / 2);
@@ -153,7 +153,7 @@ struct WeightStream {
     else if (BLK == 1) s = make_buf(a.ws + e * (NK / 256) + (int64_t)t0 * kb, (uint32_t)(rows / 16) * (uint32_t)kb);
     else s = make_buf(a.ws + e * (NK / 256) + c0, rows ? (uint32_t)kb * (uint32_t)nb - (uint32_t)c0 : 0u);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int r = i * 32 + l32;
       row[i] = r < rows ? (uint32_t)r * (uint32_t)(K / 2) + (uint32_t)at / 2 : kOutside;
       if (BLK == 2) srow[i] = (uint32_t)(r / 16 + t0 - c0) & 3u;
@@ -162,7 +162,7 @@ struct WeightStream {
   }
   // Codes of the lane's k's 32 q .. 32 q + 31 of row i; nothing is read for a step past K.
   NV_DEV nv_u4 codes(int i, int k0, int q) const { return buf16(w, row[i] + 16u * q, k0 < K ? (uint32_t)k0 / 2 : end); }
-  // What the lane's four scales of both rows are made from (`scales`).
+  // What the lane's four scales of its rows are made from (`scales`).
   NV_DEV void fetch_scales(int k0, uint32_t v[4]) const {
     const int b = (k0 + at) / 16;
     if (BLK == 2) {
@@ -180,24 +180,24 @@ struct WeightStream {
       }
     } else if (k0 + 128 <= K) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i] = buf4(s, srow[i] + (uint32_t)at / 16, (uint32_t)k0 / 16);
+      for (int i = 0; i < NI; ++i) v[i] = buf4(s, srow[i] + (uint32_t)at / 16, (uint32_t)k0 / 16);
     } else if (kb >= 4) {
       // the last word of a row starts at its fourth last byte: shifted down, it has zeros past the row
       const int c = b < kb - 4 ? b : kb - 4, d = b - c;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i] = buf4(s, b < kb ? srow[i] + (uint32_t)c : kOutside) >> (8 * (d & 3));
+      for (int i = 0; i < NI; ++i) v[i] = buf4(s, b < kb ? srow[i] + (uint32_t)c : kOutside) >> (8 * (d & 3));
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < NI; ++i) {
         v[i] = 0;
 #pragma unroll
         for (int j = 0; j < 3; ++j) v[i] |= buf1(s, b + j < kb ? srow[i] + (uint32_t)(b + j) : kOutside) << (8 * j);
       }
     }
   }
-  NV_DEV void scales(const uint32_t v[4], uint32_t ws[2]) const {
+  NV_DEV void scales(const uint32_t v[4], uint32_t ws[NI]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NI; ++i) {
       if (BLK != 2) {
         ws[i] = v[i];
         continue;
