@@ -43,6 +43,8 @@ SIGNATURES = {
     "nvfp4_grouped_matmul": (_i32, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _f32, _vp,
                                     _i32, _vp]),
     "nvfp4_grouped_wgrad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp]),
+    "nvfp4_grouped_wgrad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "nvfp4_grouped_wgrad_split": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _sz, _vp]),
     "nvfp4_selftest_scan": (_i32, [_i32, _u32, _c.c_uint64, _c.c_uint64, _i32, _vp, _vp]),
     "nvfp4_selftest_launch_plan": (_i32, [_i32, _i64, _i64, _i32, _i32, _vp]),
 }

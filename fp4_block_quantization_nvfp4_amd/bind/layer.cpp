@@ -325,9 +325,11 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& ends = array(a[2], ScalarType::Int, E, dy, "ends");
   const int64_t N = dy.size(1), K = x.size(1);
   const Tensor dw = make(dy, {E, N, K}, dt);
-  check(nvfp4_grouped_wgrad(dy.data_ptr(), x.data_ptr(), bytes(xs), dy.size(0), E, N, K, ptr<int32_t>(ends), dw.data_ptr(),
-                            code(dt), stream()),
-        "nvfp4_grouped_wgrad");
+  const int64_t need = (int64_t)nvfp4_grouped_wgrad_workspace_bytes(dy.size(0), E, N, K);
+  const Tensor ws = need ? make(dy, {need}, ScalarType::Byte) : Tensor();
+  check(nvfp4_grouped_wgrad_split(dy.data_ptr(), x.data_ptr(), bytes(xs), dy.size(0), E, N, K, ptr<int32_t>(ends),
+                                  dw.data_ptr(), code(dt), ptr<void>(ws), (size_t)need, stream()),
+        "nvfp4_grouped_wgrad_split");
   return wrap(dw);
   END_HANDLE_TH_ERRORS
 }

@@ -154,17 +154,39 @@ nvfp4_status nvfp4_grouped_matmul(const void* x, const uint8_t* x_scales, int64_
                   out_dt, stream);
 }
 
-nvfp4_status nvfp4_grouped_wgrad(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E,
-                                 int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
-                                 void* stream) {
+static nvfp4_status wgrad(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E, int64_t N,
+                          int64_t K, const int32_t* ends, void* dw, int out_dt, int64_t block, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   if (nvfp4_status st = check_products(T, E, N, K)) return st;
   if (N % 16 != 0) return NVFP4_E_SHAPE;
   if (!dtype_ok(out_dt)) return NVFP4_E_DTYPE;
   if (N == 0 || K == 0) return NVFP4_OK;
   if (!ends || !dw || (T != 0 && (!dy || !x))) return NVFP4_E_NULL;
-  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(ends, 4) || !aligned(dw, 16)) return NVFP4_E_ALIGN;
-  const nvfp4::WgradArgs a = {dy, x, x_scales, ends, dw, (int)T, (int)E, (int)N, (int)K, out_dt == NVFP4_BF16};
+  if (block && !workspace) return NVFP4_E_NULL;
+  if (block && workspace_bytes < nvfp4_grouped_wgrad_workspace_bytes(T, E, N, K)) return NVFP4_E_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(ends, 4) || !aligned(dw, 16) || !aligned(workspace, 16)) return NVFP4_E_ALIGN;
+  const nvfp4::WgradArgs a = {dy, x, x_scales, ends, dw, (int)T, (int)E, (int)N, (int)K, out_dt == NVFP4_BF16,
+                              (int)block, (float*)workspace};
   return hip_status(nvfp4::launch_wgrad(a, stream));
+}
+
+nvfp4_status nvfp4_grouped_wgrad(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E,
+                                 int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
+                                 void* stream) {
+  return wgrad(dy, x, x_scales, T, E, N, K, ends, dw, out_dt, 0, nullptr, 0, stream);
+}
+
+size_t nvfp4_grouped_wgrad_workspace_bytes(int64_t T, int64_t E, int64_t N, int64_t K) {
+  if (check_products(T, E, N, K) != NVFP4_OK) return 0;
+  const int64_t b = nvfp4::wgrad_block(T, E, N, K);
+  return b ? (size_t)((T / b + E + 1) * N * K * 4) : 0;
+}
+
+nvfp4_status nvfp4_grouped_wgrad_split(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E,
+                                       int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t b = check_products(T, E, N, K) == NVFP4_OK ? nvfp4::wgrad_block(T, E, N, K) : 0;
+  return wgrad(dy, x, x_scales, T, E, N, K, ends, dw, out_dt, b, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

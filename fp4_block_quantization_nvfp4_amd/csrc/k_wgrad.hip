@@ -17,7 +17,7 @@
 
 namespace nvfp4 {
 
-constexpr int kWgN = 256, kWgK = 128, kWgT = 64;
+constexpr int kWgT = 64;
 
 // Chunk address (in 16-bit elements) of rows 8 o .. 8 o + 7 of column c.
 NV_DEV int wg_at(int c, int o) { return c * kWgT + ((o ^ ((c >> 1) & 7)) * 8); }
@@ -31,16 +31,37 @@ NV_DEV void transpose2(const uint32_t v[8], nv_u4& c0, nv_u4& c1) {
   }
 }
 
-template <bool MX8>
+// SPLIT: blocks of a.block rows of an expert are units of their own.  An expert
+// of one block is written as without; the sums of more go to a.part, by the
+// number of the block, and k_wgrad_join adds them.
+template <bool MX8, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
   __shared__ uint16_t lx[2][kWgK * kWgT];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
   const int nk = (a.K + kWgK - 1) / kWgK, nn = (a.N + kWgN - 1) / kWgN;
-  const int share = (nk * nn + 7) / 8;  // tiles of one expert on one XCD
-  const int slot = blockIdx.x >> 3, e = slot / share, in = (blockIdx.x & 7) * share + slot % share;
-  if (in >= nk * nn) return;
+  int e, in, part = -1;
+  RowRange rr;
+  if (SPLIT) {
+    int64_t unit;
+    int whole;
+    rr = find_unit<false>(a.ends, a.E, a.T, a.block, nk * nn, blockIdx.x, unit, whole);
+    if (rr.rows <= 0 || rr.e >= a.E) return;
+    e = rr.e;
+    const int local = (int)(unit - (int64_t)rr.before * (nk * nn)), block = local / (nk * nn);
+    in = local - block * (nk * nn);
+    if (rr.rows > a.block) {
+      part = rr.before + block;
+      rr.row0 += block * a.block;
+      rr.rows = rr.rows - block * a.block < a.block ? rr.rows - block * a.block : a.block;
+    }
+  } else {
+    const int share = (nk * nn + 7) / 8, slot = blockIdx.x >> 3;  // share: tiles of one expert on one XCD
+    e = slot / share;
+    in = (blockIdx.x & 7) * share + slot % share;
+    if (in >= nk * nn) return;
+    rr = expert_range(a.ends, a.T, e);
+  }
   const int n0 = (in / nk) * kWgN, k0 = (in % nk) * kWgK;
-  const RowRange rr = expert_range(a.ends, a.T, e);
   const int ns = (a.K + kMxGroup - 1) / kMxGroup;
 
   nv_f4 acc[8][4];  // 128 k's by this wave's 64 n's
@@ -158,17 +179,54 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
       const int n = n0 + wave * 64 + 4 * r + m;
       const nv_f4 v = out[r * 32 + ((lane & 31) ^ r)];
       if (n >= a.N || k >= a.K) continue;
-      const int64_t at = ((int64_t)e * a.N + n) * a.K + k;
-      if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at) = (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      const int64_t at = ((int64_t)(part < 0 ? e : part) * a.N + n) * a.K + k;
+      if (SPLIT && part >= 0) *reinterpret_cast<nv_f4*>(a.part + at) = v;
+      else if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at) = (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
       else *reinterpret_cast<nv_f4*>((float*)a.dw + at) = v;
     }
   }
 }
 
+// Adds the blocks of each expert that has several, in their order, and clears
+// the gradient of those without rows.  Grid y walks the experts.
+__global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
+  const int e = blockIdx.y;
+  RangeScan s(a.ends, a.E, a.T, a.block);
+  while (s.next() && s.base <= e) {
+  }
+  const int l = e & 63;  // the scan holds e's 64
+  const int rows = uniform(__shfl(s.count, l, 64)), blocks = uniform(__shfl(s.own, l, 64));
+  const int64_t first = uniform(__shfl(s.first, l, 64)), size = (int64_t)a.N * a.K;
+  if (rows > 0 && blocks == 1) return;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * 1024) {
+    nv_f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float* p = a.part + first * size + i;
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) {
+      const nv_f4 w = *reinterpret_cast<const nv_f4*>(p + b * size);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] += w[r];
+    }
+    const int64_t at = e * size + i;
+    if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at) = (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    else *reinterpret_cast<nv_f4*>((float*)a.dw + at) = v;
+  }
+}
+
 int launch_wgrad(const WgradArgs& a, void* stream) {
-  const dim3 grid((uint32_t)(a.E * xcd_grid(ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK))));
-  if (a.xs) k_wgrad<true><<<grid, 256, 0, (hipStream_t)stream>>>(a);
-  else k_wgrad<false><<<grid, 256, 0, (hipStream_t)stream>>>(a);
+  const int64_t tiles = ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK);
+  const hipStream_t st = (hipStream_t)stream;
+  if (a.block) {
+    const dim3 grid((uint32_t)xcd_grid((a.T / a.block + a.E + 1) * tiles));
+    if (a.xs) k_wgrad<true, true><<<grid, 256, 0, st>>>(a);
+    else k_wgrad<false, true><<<grid, 256, 0, st>>>(a);
+    const int64_t join = ceil_div((int64_t)a.N * a.K, 1024);
+    k_wgrad_join<<<dim3((uint32_t)(join < 4096 ? join : 4096), (uint32_t)a.E), 256, 0, st>>>(a);
+  } else {
+    const dim3 grid((uint32_t)(a.E * xcd_grid(tiles)));
+    if (a.xs) k_wgrad<true, false><<<grid, 256, 0, st>>>(a);
+    else k_wgrad<false, false><<<grid, 256, 0, st>>>(a);
+  }
   return (int)hipGetLastError();
 }
 

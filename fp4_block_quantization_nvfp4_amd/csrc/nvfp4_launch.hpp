@@ -89,6 +89,8 @@ struct WgradArgs {
   void* dw;            // [E, N, K]
   int T, E, N, K;
   int out_bf16;
+  int block;           // rows of a block (plan_wgrad), 0: whole experts
+  float* part;         // sums of blocks, [T / block + E][N][K]
 };
 int launch_wgrad(const WgradArgs& a, void* stream);
 

@@ -172,4 +172,23 @@ inline GroupedPlan plan_grouped(int64_t T, int64_t E, int64_t N) {
   return {rows, width, xcd_grid((m < T ? m : T) * ceil_div(N, width)) + (rows == 128 ? kGroupedSlots * 3 / 8 : 0)};
 }
 
+// Weight gradient: tiles of kWgN n's by kWgK k's.
+constexpr int kWgN = 256, kWgK = 128;
+// Rows of a block where long experts are split, 0 where they are not.  A
+// workgroup takes about 1.1 us for 64 rows while the chip is not full, a block's
+// sums some 0.05 us a tile to write and read; block rows b cost 1.1 b / 64 +
+// 0.05 tiles T / b us in all, least at b = sqrt(2.9 tiles T).  Split where
+// that and one launch more (8 us) take less than 4/5 of the longest expert
+// (taken as twice the mean), while the sums stay below 256 MB.  One expert 1024 x 512,
+// 16384 rows: 299 us whole, 47 split.
+inline int64_t wgrad_block(int64_t T, int64_t E, int64_t N, int64_t K) {
+  const int64_t tiles = ceil_div(N, kWgN) * ceil_div(K, kWgK);
+  if (T < 1024 || tiles == 0 || tiles * E >= kGroupedSlots) return 0;
+  int64_t b = 256;
+  while (b * b < 3 * tiles * T) b += 64;
+  while ((T / b + E) * N * K * 4 > (int64_t(1) << 28)) b *= 2;
+  const double whole = 1.1 * (double)(E > 1 ? 2 * T / E : T) / 64, split = 1.1 * (double)b / 64 + 0.05 * (double)(tiles * T) / (double)b + 8;
+  return split < 0.8 * whole && b < T ? b : 0;
+}
+
 }  // namespace nvfp4

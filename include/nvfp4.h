@@ -372,6 +372,18 @@ nvfp4_status nvfp4_grouped_wgrad(const void* dy, const void* x, const uint8_t* x
                                  void* stream);
 
 /*
+ * nvfp4_grouped_wgrad_split - the same, with a workspace (16-byte aligned, at
+ * least nvfp4_grouped_wgrad_workspace_bytes) for the sums of blocks of rows:
+ * where few tiles meet many rows, an expert's rows are shared by several
+ * workgroups and their sums added in a fixed order.  The query gives 0 where
+ * nothing is gained by it; the call is then nvfp4_grouped_wgrad.
+ */
+size_t nvfp4_grouped_wgrad_workspace_bytes(int64_t T, int64_t E, int64_t N, int64_t K);
+nvfp4_status nvfp4_grouped_wgrad_split(const void* dy, const void* x, const uint8_t* x_scales, int64_t T, int64_t E,
+                                       int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Test support (not part of the quantization path).
  *
  * nvfp4_selftest_scan - exhaustive scan of one of the gfx950 conversions the
