@@ -123,9 +123,15 @@ inline int norm_threads(int64_t H) {
   const int64_t per = H <= 16 * 1024 ? 16 : 32;
   return (int)ceil_div(ceil_div(H, per), 64) * 64;
 }
-// Norm's gradient: workgroups, each with one partial row of dw.
-constexpr int64_t kNormBwdGroups = 1024;
-inline int64_t norm_bwd_groups(int64_t rows) { return rows < kNormBwdGroups ? rows : kNormBwdGroups; }
+// Norm's gradient: workgroups, each with one partial row of dw.  About sixteen
+// waves on each of 256 CUs, and two rows a workgroup where there are few: a
+// partial row costs as much to write and read as a row.
+inline int64_t norm_bwd_groups(int64_t rows, int64_t H) {
+  const int64_t waves = norm_threads(H) / 64, cu = waves < 1 ? 8 : 16 / waves < 2 ? 2 : 16 / waves > 8 ? 8 : 16 / waves;
+  int64_t g = rows / 2 < 256 ? 256 : rows / 2;
+  if (g > 256 * cu) g = 256 * cu;
+  return rows < g ? rows : g;
+}
 
 // Matrix products.
 constexpr int kMatvecThreads = 256;
