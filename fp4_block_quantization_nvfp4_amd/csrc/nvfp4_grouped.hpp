@@ -111,7 +111,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
       for (int i = 0; i < PIECES; ++i) stage(i, lds, h);
     }
     fetch(128, 0);
-    w.scales(wsn, ws);
+    w.scales(0, wsn, ws);
     w.fetch_scales(128, wsn);
     __syncthreads();
 #pragma unroll
@@ -131,7 +131,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
         if (s == 3) fetch_codes(k1, 0);
         if (s == 7) {
           fetch_codes(k1, 1);
-          w.scales(wsn, ws);
+          w.scales(k1, wsn, ws);
           w.fetch_scales(k1 + 128, wsn);
         }
         __builtin_amdgcn_sched_barrier(0);
