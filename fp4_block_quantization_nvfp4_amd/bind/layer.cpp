@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -105,8 +106,9 @@ const Tensor& scale_bytes(PyObject* o, int64_t T, int64_t n, const Tensor& like,
   return t;
 }
 
+// What at::empty allocates, without its dispatch (half a microsecond each).
 Tensor make(const Tensor& like, at::IntArrayRef sizes, ScalarType dt) {
-  return at::empty(sizes, like.options().dtype(dt).requires_grad(false));
+  return Tensor(at::detail::empty_cuda(sizes, dt, like.device(), std::nullopt));
 }
 
 bool truth(PyObject* o) {

@@ -66,7 +66,7 @@ def bind_commands(obj: str, out: str):
     return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", abi, *[a for p in inc for a in ("-I", p)],
              "-c", "-o", obj, os.path.join(HERE, "bind", "layer.cpp")],
             [cxx, "-shared", "-o", out, obj, "-L", HERE, "-l:libnvfp4.so", "-Wl,-rpath,$ORIGIN", "-L", libs, "-lc10",
-             "-ltorch_cpu", "-ltorch_python"])
+             "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"])
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
