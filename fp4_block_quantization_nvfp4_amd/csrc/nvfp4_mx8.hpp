@@ -52,17 +52,6 @@ NV_DEV void store16(uint16_t* p, const float x[16]) {
   stream_out(q + 1, b);
 }
 
-// Values that a store of x in the row's type would leave, as fp32.
-NV_DEV void round_to(const uint16_t*, float x[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t w = pack_bf16(x[2 * i], x[2 * i + 1]);
-    x[2 * i] = bits2f(w << 16);
-    x[2 * i + 1] = bits2f(w & 0xFFFF0000u);
-  }
-}
-NV_DEV void round_to(const float*, float*) {}
-
 // ------------------------------------------------------------------ mx8
 
 // Biased e8m0 byte of a group whose largest finite magnitude has the bits m:
