@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
   for (int m = 0; m < 4; ++m) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[l16 * 32 + ((4 * i + grp) ^ l16)] = acc[i][m];
-#pragma unroll 1
+#pragma unroll 8
     for (int r = lane >> 5; r < 16; r += 2) {
       const int n = n0 + wave * 64 + 4 * r + m;
       const nv_f4 v = out[r * 32 + ((lane & 31) ^ r)];

@@ -176,7 +176,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
         out[l32 * ROW + ((i * 8 + q * 2 + half) ^ (l32 % ROW))] =
             nv_f4{acc[i][m][q * 4], acc[i][m][q * 4 + 1], acc[i][m][q * 4 + 2], acc[i][m][q * 4 + 3]};
     const int left = rows - m * 32 < 32 ? rows - m * 32 : 32;
-#pragma unroll 1
+#pragma unroll 4
     for (int t = lane / ROW; t < left; t += 64 / ROW) {
       const nv_f4 v = out[t * ROW + ((lane % ROW) ^ (t % ROW))];
       store_out4(a, v[0] * sc[0], v[1] * sc[1], v[2] * sc[2], v[3] * sc[3], row0 + m * 32 + t, n);
