@@ -34,11 +34,15 @@ NV_DEV void transpose2(const uint32_t v[8], nv_u4& c0, nv_u4& c1) {
 // SPLIT: blocks of a.block rows of an expert are units of their own.  An expert
 // of one block is written as without; the sums of more go to a.part, by the
 // number of the block, and k_wgrad_join adds them.
-template <bool MX8, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
+// NM: n's of a lane.  Two instead of four (tiles of 128 n's) where experts have
+// few rows or tiles are few: workgroups need half the registers, twice as many
+// run at a time (8 experts 2048 x 2048, 16 rows each: 18.9 -> 15.3 us; 1777 rows,
+// 5 experts 1040 x 528: 21.1 -> 19.1).
+template <bool MX8, bool SPLIT, int NM>
+__global__ __launch_bounds__(256, NM == 4 ? 2 : 4) void k_wgrad(WgradArgs a) {
   __shared__ uint16_t lx[2][kWgK * kWgT];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
-  const int nk = (a.K + kWgK - 1) / kWgK, nn = (a.N + kWgN - 1) / kWgN;
+  const int nk = (a.K + kWgK - 1) / kWgK, nn = (a.N + 64 * NM - 1) / (64 * NM);
   int e, in, part = -1;
   RowRange rr;
   if (SPLIT) {
@@ -61,24 +65,33 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
     if (in >= nk * nn) return;
     rr = expert_range(a.ends, a.T, e);
   }
-  const int n0 = (in / nk) * kWgN, k0 = (in % nk) * kWgK;
+  const int n0 = (in / nk) * (64 * NM), k0 = (in % nk) * kWgK;
   const int ns = (a.K + kMxGroup - 1) / kMxGroup;
 
-  nv_f4 acc[8][4];  // 128 k's by this wave's 64 n's
+  nv_f4 acc[8][NM];  // 128 k's by this wave's 16 NM n's
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int m = 0; m < 4; ++m) acc[i][m] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m = 0; m < NM; ++m) acc[i][m] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // dy: rows 32 j + 8 grp + t of the step, n's nl .. nl + 3
-  const int nl = n0 + wave * 64 + 4 * l16;
+  // dy: rows 32 j + 8 grp + t of the step, n's nl .. nl + NM - 1
+  const int nl = n0 + wave * (16 * NM) + NM * l16;
   const uint32_t yat = nl < a.N ? (uint32_t)(8 * grp) * (uint32_t)a.N * 2u + (uint32_t)nl * 2u : kOutside;
-  nv_u2 vy[2][8];
+  uint32_t vy[2][NM / 2][8];
   auto fetch_y = [&](int t0, int j) {
     const int left = rr.rows - t0, rows = left < 0 ? 0 : left < kWgT ? left : kWgT;
     const nv_buf by = make_buf((const char*)a.dy + (int64_t)(rr.row0 + t0) * 2 * a.N, (uint32_t)rows * 2u * (uint32_t)a.N);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) vy[j][t] = buf8(by, yat + (uint32_t)(32 * j + t) * (uint32_t)a.N * 2u);
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t at = yat + (uint32_t)(32 * j + t) * (uint32_t)a.N * 2u;
+      if (NM == 4) {
+        const nv_u2 v = buf8(by, at);
+        vy[j][0][t] = v.x;
+        vy[j][NM / 2 - 1][t] = v.y;
+      } else {
+        vy[j][0][t] = buf4(by, at);
+      }
+    }
   };
   // x: words of eight consecutive rows
   constexpr int XI = MX8 ? 1 : 2, XW = MX8 ? 32 : 64, XE = MX8 ? 4 : 2;  // words a row, elements a word
@@ -141,42 +154,37 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(WgradArgs a) {
     fetch_x(t1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      nv_bf8 yf[4];
-      {
-        uint32_t w[2][8];
+      nv_bf8 yf[NM];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[0][t] = vy[j][t].x, w[1][t] = vy[j][t].y;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          nv_u4 c0, c1;
-          transpose2(w[p], c0, c1);
-          yf[2 * p] = __builtin_bit_cast(nv_bf8, c0);
-          yf[2 * p + 1] = __builtin_bit_cast(nv_bf8, c1);
-        }
+      for (int p = 0; p < NM / 2; ++p) {
+        nv_u4 c0, c1;
+        transpose2(vy[j][p], c0, c1);
+        yf[2 * p] = __builtin_bit_cast(nv_bf8, c0);
+        yf[2 * p + 1] = __builtin_bit_cast(nv_bf8, c1);
       }
       fetch_y(t1, j);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const nv_bf8 xf = *reinterpret_cast<const nv_bf8*>(buf + wg_at(i * 16 + l16, 4 * j + grp));
 #pragma unroll
-        for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(xf, yf[m], acc[i][m]);
+        for (int m = 0; m < NM; ++m) acc[i][m] = mfma16(xf, yf[m], acc[i][m]);
       }
     }
     stage_x(lx[(s + 1) & 1]);
     __syncthreads();
   }
   // A lane holds, of each fragment pair (i, m), k = 16 i + 4 grp + 0..3 of n =
-  // 4 l16 + m.  16 n's at a time go through the wave's part of shared memory
+  // NM l16 + m.  16 n's at a time go through the wave's part of shared memory
   // (16-byte chunk c of row l16 at c ^ l16) and leave as rows of 128 k's.
   nv_f4* out = reinterpret_cast<nv_f4*>(&lx[0][0]) + wave * 512;
   const int k = k0 + (lane & 31) * 4;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
+  for (int m = 0; m < NM; ++m) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[l16 * 32 + ((4 * i + grp) ^ l16)] = acc[i][m];
 #pragma unroll 8
     for (int r = lane >> 5; r < 16; r += 2) {
-      const int n = n0 + wave * 64 + 4 * r + m;
+      const int n = n0 + wave * (16 * NM) + NM * r + m;
       const nv_f4 v = out[r * 32 + ((lane & 31) ^ r)];
       if (n >= a.N || k >= a.K) continue;
       const int64_t at = ((int64_t)(part < 0 ? e : part) * a.N + n) * a.K + k;
@@ -213,20 +221,23 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
   }
 }
 
-int launch_wgrad(const WgradArgs& a, void* stream) {
+template <bool MX8>
+static void wgrad_go(const WgradArgs& a, hipStream_t st) {
   const int64_t tiles = ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK);
-  const hipStream_t st = (hipStream_t)stream;
   if (a.block) {
-    const dim3 grid((uint32_t)xcd_grid((a.T / a.block + a.E + 1) * tiles));
-    if (a.xs) k_wgrad<true, true><<<grid, 256, 0, st>>>(a);
-    else k_wgrad<false, true><<<grid, 256, 0, st>>>(a);
+    k_wgrad<MX8, true, 4><<<dim3((uint32_t)xcd_grid((a.T / a.block + a.E + 1) * tiles)), 256, 0, st>>>(a);
     const int64_t join = ceil_div((int64_t)a.N * a.K, 1024);
     k_wgrad_join<<<dim3((uint32_t)(join < 4096 ? join : 4096), (uint32_t)a.E), 256, 0, st>>>(a);
+  } else if (wgrad_narrow(a.T, a.E, tiles)) {
+    k_wgrad<MX8, false, 2><<<dim3((uint32_t)(a.E * xcd_grid(ceil_div(a.N, kWgN / 2) * ceil_div(a.K, kWgK)))), 256, 0, st>>>(a);
   } else {
-    const dim3 grid((uint32_t)(a.E * xcd_grid(tiles)));
-    if (a.xs) k_wgrad<true, false><<<grid, 256, 0, st>>>(a);
-    else k_wgrad<false, false><<<grid, 256, 0, st>>>(a);
+    k_wgrad<MX8, false, 4><<<dim3((uint32_t)(a.E * xcd_grid(tiles))), 256, 0, st>>>(a);
   }
+}
+
+int launch_wgrad(const WgradArgs& a, void* stream) {
+  if (a.xs) wgrad_go<true>(a, (hipStream_t)stream);
+  else wgrad_go<false>(a, (hipStream_t)stream);
   return (int)hipGetLastError();
 }
 

@@ -180,6 +180,9 @@ inline GroupedPlan plan_grouped(int64_t T, int64_t E, int64_t N) {
 
 // Weight gradient: tiles of kWgN n's by kWgK k's.
 constexpr int kWgN = 256, kWgK = 128;
+// Tiles of half the n's: up to 128 rows an expert, where writing the gradient
+// bounds, and while the chip is not full.
+inline bool wgrad_narrow(int64_t T, int64_t E, int64_t tiles) { return T <= 128 * E || tiles * E <= kGroupedSlots / 2; }
 // Rows of a block where long experts are split, 0 where they are not.  A
 // workgroup takes about 1.1 us for 64 rows while the chip is not full, a block's
 // sums some 0.05 us a tile to write and read; block rows b cost 1.1 b / 64 +
