@@ -39,7 +39,7 @@ NV_DEV void transpose2(const uint32_t v[8], nv_u4& c0, nv_u4& c1) {
 // run at a time (8 experts 2048 x 2048, 16 rows each: 18.9 -> 15.3 us; 1777 rows,
 // 5 experts 1040 x 528: 21.1 -> 19.1).
 template <bool MX8, bool SPLIT, int NM>
-__global__ __launch_bounds__(256, NM == 4 ? 2 : 4) void k_wgrad(WgradArgs a) {
+__global__ __launch_bounds__(256, NM == 4 ? 2 : MX8 ? 3 : 4) void k_wgrad(WgradArgs a) {
   __shared__ uint16_t lx[2][kWgK * kWgT];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
   const int nk = (a.K + kWgK - 1) / kWgK, nn = (a.N + 64 * NM - 1) / (64 * NM);
