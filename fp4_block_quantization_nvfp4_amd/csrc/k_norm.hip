@@ -21,33 +21,47 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(const T* __restrict__ x, 
                                                        float eps, uint8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ scales, T* __restrict__ hidden,
                                                        float* __restrict__ rstd_out) {
-  __shared__ float lds[16];
+  // A code next to a border shows the last bits of y.  The sum over the row's
+  // lanes and the root are in 64 bits.  Of 32-bit rows all else is too, from both
+  // addends (8.9 -> 9.9 us at 1021 x 2064, no code off where 32 bits had 1 in 2
+  // million).  Of 16-bit ones 64 bits would cost 67 -> 88 us (8192 x 7168), so y
+  // takes 32 bits with the errors of rstd and of the first product carried along
+  // (67.8 -> 69.6 us, half the codes off).
+  constexpr bool WIDE = sizeof(T) == 4;
+  __shared__ double lds[16];
   const int nt = blockDim.x, ns = (H + kMxGroup - 1) / kMxGroup;
-  const float inv_h = 1.0f / (float)H;
+  const double inv_h = 1.0 / H;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int64_t at = row * H;
-    float h[C][16];
+    float h[C][16], r[C][16];
+    double total = 0.0;
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * nt + threadIdx.x) * 16;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[c][i] = r[c][i] = 0.0f;
       if (j < H) {
         load16(x + at + j, h[c]);
-        if (RES) {
-          float r[16];
-          load16(res + at + j, r);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) h[c][i] += r[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) h[c][i] = 0.0f;
+        if (RES) load16(res + at + j, r[c]);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+      for (int i = 0; i < 16; ++i) {
+        if (WIDE) {
+          const double v = (double)h[c][i] + (double)r[c][i];
+          total = __builtin_fma(v, v, total);
+        } else {
+          if (RES) h[c][i] += r[c][i];
+          sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+        }
+      }
     }
-    sum = block_sum(sum, lds);
-    const float rstd = 1.0f / __builtin_sqrtf(sum * inv_h + eps);
+    const double var = __builtin_fma(block_sum(WIDE ? total : (double)sum, lds), inv_h, (double)eps);
+    const double near = __builtin_amdgcn_rsq(var);  // to 2^-22 or so, then one step of Newton's method
+    const double off = near * (0.5 * __builtin_fma(-var * near, near, 1.0));
+    const double root = off == off ? near + off : near;
+    const float rstd = (float)root;
+    const float rest = __builtin_isinf(rstd) ? 0.0f : (float)(root - (double)rstd);
     if (threadIdx.x == 0) rstd_out[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -55,14 +69,31 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(const T* __restrict__ x, 
       const bool in = j < H;
       float w[16], y[16];
       if (in) {
-        if (RES) store16(hidden + at + j, h[c]);
+        if (RES) {
+          float sum16[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum16[i] = WIDE ? h[c][i] + r[c][i] : h[c][i];
+          store16(hidden + at + j, sum16);
+        }
         load16(weight + j, w);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = 0.0f;
       }
+      if (WIDE && RES) {  // added again: sums kept in 64 bits would take twice the registers
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = h[c][i] * rstd * w[i];
+        for (int i = 0; i < 16; ++i) asm("" : "+v"(h[c][i]), "+v"(r[c][i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (WIDE) {
+          const double v = RES ? (double)h[c][i] + (double)r[c][i] : (double)h[c][i];
+          y[i] = round_odd(v * root * (double)w[i]);
+        } else {
+          const float p = h[c][i] * rstd, e = __builtin_fmaf(h[c][i], rest, __builtin_fmaf(h[c][i], rstd, -p));
+          y[i] = __builtin_fmaf(p, w[i], e * w[i]);
+        }
+      }
       if (!in) {  // a missing half group counts as zeros, also where rstd is not finite
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = 0.0f;

@@ -201,24 +201,37 @@ NV_DEV uint32_t buf1(nv_buf b, uint32_t off, uint32_t base = 0) { return __built
 
 // ------------------------------------------------------------ reductions
 
-NV_DEV float wave_sum(float v) {
+template <typename V>
+NV_DEV V wave_sum(V v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
 }
 
-// Sum over the workgroup; every lane gets it.  `lds` holds one float a wave
+// Sum over the workgroup; every lane gets it.  `lds` holds one number a wave
 // and is free again after the next barrier.
-NV_DEV float block_sum(float v, float* lds) {
+template <typename V>
+NV_DEV V block_sum(V v, V* lds) {
   v = wave_sum(v);
   const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   if (nw == 1) return v;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[wave] = v;
   __syncthreads();
-  float r = 0.0f;
+  V r = 0;
   for (int i = 0; i < nw; ++i) r += lds[i];
   return r;
+}
+
+// fp32 with the last bit set where 64-bit v lies between two fp32 numbers: a
+// second rounding to 8 bits then takes the side of a border that v is on.  (No
+// border is near where r is zero or subnormal.)
+NV_DEV float round_odd(double v) {
+  const float r = (float)v;
+  const double d = v - (double)r;
+  const uint32_t b = f2bits(r), back = (d < 0.0) != (r < 0.0f) ? 1u : 0u;
+  const float a = __builtin_fabsf(r);
+  return d != 0.0 && a >= 0x1p-126f && a < INFINITY ? bits2f((b - back) | 1u) : r;
 }
 
 }  // namespace nvfp4

@@ -1,7 +1,7 @@
 """The layer operators at the sizes where their launch plans change: weight
 gradients whose rows are split among workgroups, row counts around the switch
 from 16 to 32 rows at a time and from there to row tiles, tiles of either
-width, weights a few words wide.  Definitions and tolerances are those of
+width, weights a few words wide; and the codes of 32-bit rows.  Definitions and tolerances are those of
 tests/layer_ref.py and tests/test_gpu_layer.py."""
 import pytest
 import torch
@@ -131,3 +131,31 @@ def test_row_sums_do_not_depend_on_the_tile(T, E, N, K):
     lends = torch.cat((ends[:-1], ends.new_tensor([6 * T])))
     y, z = nv.grouped_matmul(x, ends, p, s, global_amax=a), nv.grouped_matmul(long, lends, p, s, global_amax=a)
     assert torch.equal(y, z[:T])
+
+
+# y of 32-bit rows is in 64 bits up to its codes, off by 2^-40 of its value.
+# With 8 borders of codes in an octave, about 2^-36 of all values are that near
+# to one: of 3 million, 4e-5 may differ.
+
+
+@pytest.mark.parametrize("H", [2064, 16400])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_codes_of_32_bit_rows_are_exact(H, residual):
+    g = gen(H)
+    x, r, w = randn(g, 180, H, dtype=F32), randn(g, 180, H, dtype=F32), randn(g, H, dtype=F32)
+    codes, scales, hidden, rstd = nv.add_rms_norm(x.cuda(), w.cuda(), r.cuda() if residual else None, eps=2.0 ** -20)
+    h = R.f64(x) + R.f64(r) if residual else R.f64(x)
+    root = (h.square().mean(1, keepdim=True) + 2.0 ** -20).rsqrt()
+    c, s = R.mx8_codes(h * root * R.f64(w))
+    assert torch.equal(R.byte(codes), c) and torch.equal(R.byte(scales), s)
+    assert torch.equal(hidden.cpu(), h.float())
+    assert ((R.f64(rstd) - root[:, 0]).abs() <= root[:, 0] * R.U24).all()
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_swiglu_codes_of_32_bit_rows_are_exact(keep):
+    x = randn(gen(5), 1500, 4096, dtype=F32, by=3.0)
+    codes, scales, _, _ = nv.swiglu_checkpoint(x.cuda(), keep=keep)
+    g, u = R.f64(x)[:, :2048], R.f64(x)[:, 2048:]
+    c, s = R.mx8_codes(g / (1 + torch.exp(-g)) * u)
+    assert torch.equal(R.byte(codes), c) and torch.equal(R.byte(scales), s)
