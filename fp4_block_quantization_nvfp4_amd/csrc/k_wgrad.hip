@@ -2,11 +2,12 @@
 // rows t of expert e of dy[t, n] x[t, k], dy bf16, x bf16 or mx8.
 //
 // The sum runs over rows, the slow axis of both operands.  A workgroup of
-// four waves makes 256 n's by 128 k's and walks the rows 64 at a time.  Each
-// wave has 64 n's of its own and takes dy straight into registers: four n's of
-// eight rows a lane, turned into four fragments by byte permutes.  x is shared
-// and goes through shared memory (two buffers): a lane takes a word (two bf16
-// or four e4m3) of eight rows and writes, for each column, the eight rows as
+// four waves makes 256 n's (or 128, below) by 128 k's and walks the rows 64 at
+// a time.  Each wave has 64 n's (32) of its own and takes dy straight into
+// registers: four (two) n's of eight rows a lane, turned into as many fragments
+// by byte permutes.  x is shared and goes through shared memory (two buffers):
+// a lane takes a word (two bf16 or four e4m3) of eight rows and writes, for
+// each column, the eight rows as
 // one 16-byte chunk.  Loads of the next step fill the registers that this one
 // has just consumed.  x is the first operand: a lane then holds four
 // consecutive k's of one n.  Each XCD takes an eighth of every expert's tiles,
