@@ -108,28 +108,37 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(const T* __restrict__ x, 
   }
 }
 
-// 16 bf16 elements of a row as loaded.
+// 16 elements of a row as loaded.  again() makes the compiler take them from
+// there a second time instead of keeping what values() gave.
+template <typename T>
 struct Raw {
-  nv_u4 q[2];
-  NV_DEV void load(const uint16_t* p) {
-    q[0] = reinterpret_cast<const nv_u4*>(p)[0];
-    q[1] = reinterpret_cast<const nv_u4*>(p)[1];
+  nv_u4 q[sizeof(T)];
+  NV_DEV void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) q[i] = reinterpret_cast<const nv_u4*>(p)[i];
   }
-  NV_DEV void load(const float*) {}
+  NV_DEV void again() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) asm("" : "+v"(q[i]));
+  }
   NV_DEV void values(float v[16]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = bits2f(q[i >> 2][i & 3] << 16);
-      v[2 * i + 1] = bits2f(q[i >> 2][i & 3] & 0xFFFF0000u);
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = bits2f(q[i >> 2][i & 3]);
+      else v[i] = bits2f(i & 1 ? q[i >> 3][(i >> 1) & 3] & 0xFFFF0000u : q[i >> 3][(i >> 1) & 3] << 16);
     }
   }
 };
 
 // A workgroup takes every gridDim-th row, keeps its share of dw in registers
-// and leaves one partial row of dw.  bf16 rows up to 16384 have registers left
-// for the weight and for the next row's dy and hidden, which are then in flight
-// during this row's sum (8192 x 7168 with the sum of the partial rows: 118 ->
-// 96 us).
+// and leaves one partial row of dw.  Of rows up to 16384 the weight stays in
+// registers too (2048 x 16384 fp32: 145 -> 126 us), and bf16 rows have some left
+// for the next row's dy and hidden, which are then in flight during this row's
+// sum (8192 x 7168 with the sum of the partial rows: 118 -> 96 us).  Rows over
+// 16384 keep dy and hidden as loaded and dw in shared memory, and read the
+// weight again and dhidden only after the sum: with all of it in registers 37 to
+// 71 of them spilled (4096 x 18432 bf16: 313 -> 181 us, 2048 x 18432 fp32: 283 ->
+// 238).
 template <typename T, int C, bool DH>
 __global__ __launch_bounds__(1024) void k_add_rms_norm_bwd(const T* __restrict__ dy, const T* __restrict__ hidden,
                                                            const T* __restrict__ dhidden,
@@ -140,49 +149,53 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm_bwd(const T* __restrict__
   __shared__ float lds[16];
   const int nt = blockDim.x, j0 = threadIdx.x * 16;
   const float inv_h = 1.0f / (float)H;
-  float dw[C][16], w[C][16];
+  __shared__ float acc[C > 1 ? kNormMaxH : 1];  // dw of long rows; a lane's own places, so no barriers
+  float dw1[16], w1[16];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dw[c][i] = 0.0f;
-  Raw rd, rn;
+  for (int i = 0; i < 16; ++i) dw1[i] = 0.0f;
+  if (C > 1) {
+    for (int i = 0; i < 16 * C; ++i) acc[i * nt + threadIdx.x] = 0.0f;
+  }
+  Raw<T> rd[C], rn[C];
   auto ahead = [&](int64_t row) {
     if (j0 >= H) return;
-    rd.load(dy + row * H + j0);
-    rn.load(hidden + row * H + j0);
+    rd[0].load(dy + row * H + j0);
+    rn[0].load(hidden + row * H + j0);
   };
-  if (AHEAD) {
-    if (j0 < H) load16(weight + j0, w[0]);
-    ahead(blockIdx.x);
-  }
+  if (C == 1 && j0 < H) load16(weight + j0, w1);
+  if (AHEAD) ahead(blockIdx.x);
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int64_t at = row * H;
     const float rstd = rstd_in[row];
-    float d[C][16], n[C][16], dh[C][16];
-    Raw rh;
+    const float* wp = weight;
+    if (C > 1) asm volatile("" : "+s"(wp));  // else the weights stay in registers from row to row
+    float d1[16], n1[16];  // of one chunk, from pass to pass
+    Raw<T> rh1;
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * nt + threadIdx.x) * 16;
       if (j < H) {
-        if (AHEAD) {
-          if (DH) rh.load(dhidden + at + j);
-          rd.values(d[c]);
-          rn.values(n[c]);
-        } else {
-          load16(dy + at + j, d[c]);
-          load16(hidden + at + j, n[c]);
-          if (DH) load16(dhidden + at + j, dh[c]);
-          load16(weight + j, w[c]);
+        float d2[16], n2[16], w2[16];
+        float(&d)[16] = C > 1 ? d2 : d1, (&n)[16] = C > 1 ? n2 : n1, (&w)[16] = C > 1 ? w2 : w1;
+        if (!AHEAD) {
+          rd[c].load(dy + at + j);
+          rn[c].load(hidden + at + j);
         }
+        if (DH && C == 1) rh1.load(dhidden + at + j);
+        if (C > 1) load16(wp + j, w);
+        rd[c].values(d);
+        rn[c].values(n);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          n[c][i] *= rstd;
-          dw[c][i] = __builtin_fmaf(d[c][i], n[c][i], dw[c][i]);
-          d[c][i] *= w[c][i];
-          dot = __builtin_fmaf(d[c][i], n[c][i], dot);
+          n[i] *= rstd;
+          float& dw = C > 1 ? acc[(c * 16 + i) * nt + threadIdx.x] : dw1[i];
+          dw = __builtin_fmaf(d[i], n[i], dw);
+          d[i] *= w[i];
+          dot = __builtin_fmaf(d[i], n[i], dot);
         }
       }
+      if (C > 1) asm volatile("" ::: "memory");
     }
     if (AHEAD && row + gridDim.x < rows) ahead(row + gridDim.x);
     const float mean = block_sum(dot, lds) * inv_h;
@@ -190,20 +203,43 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm_bwd(const T* __restrict__
     for (int c = 0; c < C; ++c) {
       const int j = (c * nt + threadIdx.x) * 16;
       if (j < H) {
-        if (AHEAD && DH) rh.values(dh[c]);
+        float d2[16], n2[16], w[16], dh[16];
+        float(&d)[16] = C > 1 ? d2 : d1, (&n)[16] = C > 1 ? n2 : n1;
+        Raw<T> rh2, &rh = C > 1 ? rh2 : rh1;
+        if (C > 1) {
+          rd[c].again();
+          rn[c].again();
+          rd[c].values(d);
+          rn[c].values(n);
+          load16(wp + j, w);
+          if (DH) rh.load(dhidden + at + j);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            n[i] *= rstd;
+            d[i] *= w[i];
+          }
+        }
+        if (DH) rh.values(dh);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float v = rstd * (d[c][i] - n[c][i] * mean);
-          d[c][i] = DH ? v + dh[c][i] : v;
+          const float v = rstd * (d[i] - n[i] * mean);
+          d[i] = DH ? v + dh[i] : v;
         }
-        store16(dx + at + j, d[c]);
+        store16(dx + at + j, d);
       }
+      if (C > 1) asm volatile("" ::: "memory");
     }
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int j = (c * nt + threadIdx.x) * 16;
-    if (j < H) store16(partial + (int64_t)blockIdx.x * H + j, dw[c]);
+    if (j < H) {
+      if (C > 1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dw1[i] = acc[(c * 16 + i) * nt + threadIdx.x];
+      }
+      store16(partial + (int64_t)blockIdx.x * H + j, dw1);
+    }
   }
 }
 

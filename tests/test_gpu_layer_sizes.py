@@ -1,8 +1,9 @@
 """The layer operators at the sizes where their launch plans change: weight
 gradients whose rows are split among workgroups, row counts around the switch
 from 16 to 32 rows at a time and from there to row tiles, tiles of either
-width, weights a few words wide; and the codes of 32-bit rows.  Definitions and tolerances are those of
-tests/layer_ref.py and tests/test_gpu_layer.py."""
+width, weights a few words wide, long rows of which a workgroup of the norm's
+gradient takes several; and the codes of 32-bit rows.  Definitions and tolerances
+are those of tests/layer_ref.py and tests/test_gpu_layer.py."""
 import pytest
 import torch
 
@@ -10,7 +11,8 @@ import fp4_block_quantization_nvfp4_amd as nv
 from fp4_block_quantization_nvfp4_amd import _lib as L
 from tests import layer_ref as R
 from tests.gpu_util import need_gpu
-from tests.test_gpu_layer import BF, F32, INF, NAN, check_grouped, check_wgrad, gen, randn, rows, split, weights
+from tests.test_gpu_layer import (BF, F32, INF, NAN, check_grouped, check_norm, check_wgrad, gen, randn, rows, split,
+                                  weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +161,15 @@ def test_swiglu_codes_of_32_bit_rows_are_exact(keep):
     g, u = R.f64(x)[:, :2048], R.f64(x)[:, 2048:]
     c, s = R.mx8_codes(g / (1 + torch.exp(-g)) * u)
     assert torch.equal(R.byte(codes), c) and torch.equal(R.byte(scales), s)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(530, 16400), (300, 32752), (1100, 16384)])
+@pytest.mark.parametrize("res", [True, False], ids=["residual", "plain"])
+def test_norm_of_many_long_rows(T, H, dtype, res):
+    """More rows than workgroups: each sums its share of the weight's gradient."""
+    g = gen(T + H)
+    x, r = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype, by=3.0)
+    w = 1 + 0.2 * torch.randn(H, generator=g)
+    dy, dh = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype)
+    check_norm(x, r if res else None, w, upstream=(dy, dh if res else None))
