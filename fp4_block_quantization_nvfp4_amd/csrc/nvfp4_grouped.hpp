@@ -47,39 +47,27 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
   if (nk) {
     const WeightStream<BLK, NI> w(a, e, n0, l32, half);
     const RowsView<MX8> x(a, row0, rows);
-    // staging of half a step's rows: 16-byte pieces, PR a row
-    constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
+    typedef RowsHalf<MX8, BM> Half;
+    constexpr int PR = Half::PR, PIECES = Half::PIECES;
     const int xr = tid / PR, xp = tid % PR;
-    const uint32_t pitch = MX8 ? (uint32_t)a.K : 2u * (uint32_t)a.K;
-    const uint32_t xat = (uint32_t)xr * pitch + (uint32_t)xp * 16u, sat = (uint32_t)(xr * x.ns + xp / 2);
-    nv_u4 st[PIECES];
-    uint32_t sts[PIECES];
-    auto fetch = [&](int k0, int h) {
-      if (HALF < 256 && tid >= HALF) return;
-      const bool in = k0 + 128 <= a.K || k0 + xp * (MX8 ? 16 : 8) < a.K;
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const uint32_t r = (uint32_t)(h * (BM / 2) + i * (256 / PR));
-        st[i] = buf16(x.x, in ? xat : kOutside, (uint32_t)k0 * (MX8 ? 1u : 2u) + r * pitch);
-        if (MX8) sts[i] = buf1(x.s, in ? sat : kOutside, (uint32_t)k0 / kMxGroup + r * (uint32_t)x.ns);
-      }
-    };
+    Half st;
+    auto fetch = [&](int k0, int h) { st.load(x, tid, k0, h); };
     // row r of a buffer: 16 chunks of 16 bytes, chunk c at c ^ (r % 16)
     auto put = [&](uint16_t* buf, int r, int c, nv_u4 v) {
       *reinterpret_cast<nv_u4*>(buf + r * 128 + ((c ^ (r & 15)) * 8)) = v;
     };
     auto stage = [&](int i, uint16_t* buf, int h) {
-      if (HALF < 256 && tid >= HALF) return;
+      if (Half::HALF < 256 && tid >= Half::HALF) return;
       const int r = h * (BM / 2) + i * (256 / PR) + xr;
       if (MX8) {
-        const float sc = e8m0_value(sts[i]);
+        const float sc = e8m0_value(st.s[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const nv_u2 u = mx8_to_bf16(st[i][2 * j], sc), v = mx8_to_bf16(st[i][2 * j + 1], sc);
+          const nv_u2 u = mx8_to_bf16(st.c[i][2 * j], sc), v = mx8_to_bf16(st.c[i][2 * j + 1], sc);
           put(buf, r, 2 * xp + j, (nv_u4){u.x, u.y, v.x, v.y});
         }
       } else {
-        put(buf, r, xp, st[i]);
+        put(buf, r, xp, st.c[i]);
       }
     };
     nv_u4 wc[NI][2];

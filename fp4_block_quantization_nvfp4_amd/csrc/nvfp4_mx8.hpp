@@ -1,5 +1,5 @@
 // Device helpers of the layer operators: 8-bit rows ("mx8"), 4-bit weight
-// decode, range-checked loads, wave sums.
+// decode, wave sums.
 //
 // mx8: e4m3 codes with one e8m0 scale for each 32 consecutive elements of a
 // row (the last group of a row may be shorter).  The scale is the smallest
@@ -9,6 +9,7 @@
 #pragma once
 
 #include "nvfp4_device.hpp"
+#include "nvfp4_buffer.hpp"
 
 namespace nvfp4 {
 
@@ -16,8 +17,6 @@ typedef __bf16 nv_bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 nv_bf8 __attribute__((ext_vector_type(8)));
 typedef float nv_f4 __attribute__((ext_vector_type(4)));
 typedef float nv_f16 __attribute__((ext_vector_type(16)));
-typedef unsigned int nv_u4 __attribute__((ext_vector_type(4)));
-typedef unsigned int nv_u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMxGroup = 32;  // elements under one e8m0 scale
 
@@ -175,29 +174,6 @@ NV_DEV nv_f4 mfma16(nv_bf8 a, nv_bf8 b, nv_f4 c) { return __builtin_amdgcn_mfma_
 // 4][l % 32], r = 0..15.  Twice the work an instruction: a loop that also
 // decodes weights needs the issue slots.
 NV_DEV nv_f16 mfma32(nv_bf8 a, nv_bf8 b, nv_f16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
-
-// ---------------------------------------------------------------- loads
-
-// A buffer of `bytes` bytes: loads outside it return zeros.  p and bytes are
-// the same in all lanes; saying so keeps the compiler from a loop around each
-// load where it cannot see it.
-typedef __amdgpu_buffer_rsrc_t nv_buf;
-NV_DEV nv_buf make_buf(const void* p, uint32_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0,
-                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
-}
-constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer (all are below 2^31 bytes)
-// off is a lane's own offset, base one that all lanes share (kept in a scalar,
-// so a walk along a row costs no vector instruction); their sum is what is
-// checked against the buffer, word by word in a wide load.
-NV_DEV nv_u4 buf16(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, (int)base, 0); }
-NV_DEV nv_u2 buf8(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, (int)base, 0); }
-NV_DEV uint32_t buf4(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)base, 0); }
-NV_DEV uint32_t buf2(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b16(b, (int)off, (int)base, 0); }
-NV_DEV uint32_t buf1(nv_buf b, uint32_t off, uint32_t base = 0) { return __builtin_amdgcn_raw_buffer_load_b8(b, (int)off, (int)base, 0); }
 
 // ------------------------------------------------------------ reductions
 

@@ -75,6 +75,29 @@ struct RowsPiece {
   }
 };
 
+// Half a step's rows of k_grouped as its 256 lanes load them: 128 k's of BM / 2
+// rows in 16-byte pieces, PR a row; lane tid takes piece tid % PR of rows
+// tid / PR + 256 / PR * i.  k's at or past K read as zeros.
+template <bool MX8, int BM>
+struct RowsHalf {
+  static constexpr int PR = MX8 ? 8 : 16, HALF = BM / 2 * PR, PIECES = HALF > 256 ? HALF / 256 : 1;
+  nv_u4 c[PIECES];
+  uint32_t s[PIECES];
+  NV_DEV void load(const RowsView<MX8>& v, int tid, int k0, int h) {
+    if (HALF < 256 && tid >= HALF) return;
+    const int xr = tid / PR, xp = tid % PR;
+    const uint32_t pitch = MX8 ? (uint32_t)v.K : 2u * (uint32_t)v.K;
+    const uint32_t xat = (uint32_t)xr * pitch + (uint32_t)xp * 16u, sat = (uint32_t)(xr * v.ns + xp / 2);
+    const bool in = k0 + 128 <= v.K || k0 + xp * (MX8 ? 16 : 8) < v.K;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const uint32_t r = (uint32_t)(h * (BM / 2) + i * (256 / PR));
+      c[i] = buf16(v.x, in ? xat : kOutside, (uint32_t)k0 * (MX8 ? 1u : 2u) + r * pitch);
+      if (MX8) s[i] = buf1(v.s, in ? sat : kOutside, (uint32_t)k0 / kMxGroup + r * (uint32_t)v.ns);
+    }
+  }
+};
+
 // Rows n0 .. n0 + rows - 1 of expert e's weight [N, K]; BLK 0: a scale for
 // 1x16 elements [N, K / 16]; 1: for 16x16 tiles [N / 16, K / 16]; 2: the same
 // tiles stored as those of the transposed weight, [K / 16, N / 16].
