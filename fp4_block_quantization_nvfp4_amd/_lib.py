@@ -47,6 +47,7 @@ SIGNATURES = {
     "nvfp4_grouped_wgrad_split": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _sz, _vp]),
     "nvfp4_selftest_scan": (_i32, [_i32, _u32, _c.c_uint64, _c.c_uint64, _i32, _vp, _vp]),
     "nvfp4_selftest_launch_plan": (_i32, [_i32, _i64, _i64, _i32, _i32, _vp]),
+    "nvfp4_selftest_layer_plan": (_i32, [_i32, _i64, _i64, _i64, _i64, _i32, _vp]),
 }
 
 

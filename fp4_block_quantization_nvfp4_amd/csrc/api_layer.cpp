@@ -189,4 +189,46 @@ nvfp4_status nvfp4_grouped_wgrad_split(const void* dy, const void* x, const uint
   return wgrad(dy, x, x_scales, T, E, N, K, ends, dw, out_dt, b, workspace, workspace_bytes, stream);
 }
 
+nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t N, int64_t K, int mx8,
+                                       int64_t* plan) {
+  if (entry < 0 || entry > 6) return NVFP4_E_ARG;
+  if (entry < 3) {
+    if (nvfp4_status st = check_rows(T, K)) return st;
+    if (entry == 2 ? !fits(T, 2 * K) : K > nvfp4::kNormMaxH) return NVFP4_E_RANGE;
+  } else {
+    if (entry == 3) E = 1;
+    if (nvfp4_status st = check_products(T, E, N, K)) return st;
+    if (entry > 4 && N % 16 != 0) return NVFP4_E_SHAPE;
+  }
+  if (!plan) return NVFP4_E_NULL;
+  nvfp4::LayerLaunch p[2] = {};
+  int64_t rows = 0;
+  if (entry == 0) p[0] = nvfp4::plan_norm(T, K);
+  if (entry == 1) p[0] = nvfp4::plan_norm_bwd(T, K), p[1] = nvfp4::plan_sum_rows(K);
+  if (entry == 2) p[0] = nvfp4::plan_swiglu(T, K);
+  if (entry == 3 || entry == 4) {
+    if (nvfp4::use_matvec(T, E, N)) {
+      p[0] = nvfp4::plan_matvec(T, entry == 4 ? E : 0, N, mx8 != 0);
+      rows = T > 16 * E ? 32 : 16;
+    } else {
+      const nvfp4::GroupedPlan g = nvfp4::plan_grouped(T, entry == 4 ? E : 0, N);
+      p[0] = {nvfp4::PLAN_GROUPED, g.grid, 1, 256};
+      rows = g.rows;
+    }
+  }
+  if (entry >= 5) {
+    rows = entry == 6 ? nvfp4::wgrad_block(T, E, N, K) : 0;
+    p[0] = nvfp4::plan_wgrad(T, E, N, K, rows);
+    if (rows) p[1] = nvfp4::plan_wgrad_join(E, N, K);
+  }
+  for (int i = 0; i < 2; ++i) {
+    plan[5 * i] = p[i].kernel;
+    plan[5 * i + 1] = p[i].grid;
+    plan[5 * i + 2] = p[i].y;
+    plan[5 * i + 3] = p[i].block;
+    plan[5 * i + 4] = i ? 0 : rows;
+  }
+  return NVFP4_OK;
+}
+
 }  // extern "C"

@@ -125,14 +125,15 @@ __global__ __launch_bounds__(kMatvecThreads, XM == 16 ? 3 : 2) void k_matvec(Mat
 
 template <bool MX8, int BLK, bool WORDS, int R, int XM>
 static void matvec_go(const MatmulArgs& a, hipStream_t st) {
-  const dim3 grid((uint32_t)ceil_div(a.N, 16 * R), a.ends ? (uint32_t)a.E + 1 : 1);
-  if (a.ends) k_matvec<MX8, BLK, WORDS, R, XM, true><<<grid, kMatvecThreads, 0, st>>>(a);
-  else k_matvec<MX8, BLK, WORDS, R, XM, false><<<grid, kMatvecThreads, 0, st>>>(a);
+  const LayerLaunch p = plan_matvec(a.T, a.ends ? a.E : 0, a.N, MX8);
+  const dim3 grid((uint32_t)p.grid, (uint32_t)p.y);
+  if (a.ends) k_matvec<MX8, BLK, WORDS, R, XM, true><<<grid, p.block, 0, st>>>(a);
+  else k_matvec<MX8, BLK, WORDS, R, XM, false><<<grid, p.block, 0, st>>>(a);
 }
 
 template <bool MX8, int BLK, bool WORDS>
 static void matvec_size(const MatmulArgs& a, int r, bool more, hipStream_t st) {
-  if (more) r >= 2 ? matvec_go<MX8, BLK, WORDS, 2, 32>(a, st) : matvec_go<MX8, BLK, WORDS, 1, 32>(a, st);
+  if (more) r == 2 ? matvec_go<MX8, BLK, WORDS, 2, 32>(a, st) : matvec_go<MX8, BLK, WORDS, 1, 32>(a, st);
   else if (r == 4) matvec_go<MX8, BLK, WORDS, 4, 16>(a, st);
   else r == 2 ? matvec_go<MX8, BLK, WORDS, 2, 16>(a, st) : matvec_go<MX8, BLK, WORDS, 1, 16>(a, st);
 }

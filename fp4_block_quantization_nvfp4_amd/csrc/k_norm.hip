@@ -269,9 +269,8 @@ __global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ part
 template <typename T>
 static void norm_fwd(const T* x, const T* res, const float* w, int64_t rows, int H, float eps, uint8_t* codes,
                      uint8_t* scales, T* hidden, float* rstd, hipStream_t st) {
-  const int nt = norm_threads(H);
-  const dim3 grid((uint32_t)(rows < kNormMaxGrid ? rows : kNormMaxGrid));
-#define NV_NORM(C, RES) k_add_rms_norm<T, C, RES><<<grid, nt, 0, st>>>(x, res, w, rows, H, eps, codes, scales, hidden, rstd)
+  const LayerLaunch p = plan_norm(rows, H);
+#define NV_NORM(C, RES) k_add_rms_norm<T, C, RES><<<(uint32_t)p.grid, p.block, 0, st>>>(x, res, w, rows, H, eps, codes, scales, hidden, rstd)
   if (H <= 16 * 1024) {
     if (res) NV_NORM(1, true);
     else NV_NORM(1, false);
@@ -297,9 +296,9 @@ size_t norm_bwd_workspace_bytes(int64_t rows, int64_t H) { return (size_t)norm_b
 
 template <typename T>
 static void norm_bwd(const T* dy, const T* hidden, const T* dh, const float* w, const float* rstd, int64_t rows,
-                     int H, T* dx, float* partial, int grid, hipStream_t st) {
-  const int nt = norm_threads(H);
-#define NV_NORM(C, DH) k_add_rms_norm_bwd<T, C, DH><<<grid, nt, 0, st>>>(dy, hidden, dh, w, rstd, rows, H, dx, partial)
+                     int H, T* dx, float* partial, hipStream_t st) {
+  const LayerLaunch p = plan_norm_bwd(rows, H);
+#define NV_NORM(C, DH) k_add_rms_norm_bwd<T, C, DH><<<(uint32_t)p.grid, p.block, 0, st>>>(dy, hidden, dh, w, rstd, rows, H, dx, partial)
   if (H <= 16 * 1024) {
     if (dh) NV_NORM(1, true);
     else NV_NORM(1, false);
@@ -319,12 +318,13 @@ int launch_add_rms_norm_bwd(const void* dy, const void* hidden, const void* dh, 
   if (grid > 0) {
     if (in_bf16)
       norm_bwd<uint16_t>((const uint16_t*)dy, (const uint16_t*)hidden, (const uint16_t*)dh, w, rstd, rows, (int)H,
-                         (uint16_t*)dx, partial, grid, st);
+                         (uint16_t*)dx, partial, st);
     else
       norm_bwd<float>((const float*)dy, (const float*)hidden, (const float*)dh, w, rstd, rows, (int)H, (float*)dx,
-                      partial, grid, st);
+                      partial, st);
   }
-  k_sum_rows<<<(uint32_t)(H / 16), 256, 0, st>>>(partial, grid, (int)H, dw);
+  const LayerLaunch p = plan_sum_rows(H);
+  k_sum_rows<<<(uint32_t)p.grid, p.block, 0, st>>>(partial, grid, (int)H, dw);
   return (int)hipGetLastError();
 }
 

@@ -116,9 +116,10 @@ __global__ __launch_bounds__(256) void k_swiglu_bwd(const T* __restrict__ dout, 
 int launch_swiglu(const void* gate_up, int in_bf16, int64_t rows, int64_t F, uint8_t* codes, uint8_t* scales,
                   uint8_t* kept, uint8_t* kept_scales, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const uint32_t lanes = (uint32_t)ceil_div(F, kMxGroup) * 2;
-  const dim3 grid((uint32_t)ceil_div(rows * lanes, 256));
-#define NV_SW(T, KEEP) k_swiglu<T, KEEP><<<grid, 256, 0, st>>>((const T*)gate_up, (uint32_t)rows, (uint32_t)F, lanes, codes, scales, kept, kept_scales)
+  const uint32_t lanes = (uint32_t)swiglu_lanes(F);
+  const LayerLaunch p = plan_swiglu(rows, F);
+  const dim3 grid((uint32_t)p.grid);
+#define NV_SW(T, KEEP) k_swiglu<T, KEEP><<<grid, p.block, 0, st>>>((const T*)gate_up, (uint32_t)rows, (uint32_t)F, lanes, codes, scales, kept, kept_scales)
   if (in_bf16) {
     if (kept) NV_SW(uint16_t, true);
     else NV_SW(uint16_t, false);
@@ -133,13 +134,14 @@ int launch_swiglu(const void* gate_up, int in_bf16, int64_t rows, int64_t F, uin
 int launch_swiglu_bwd(const void* dout, int in_bf16, int64_t rows, int64_t F, const uint8_t* kept,
                       const uint8_t* kept_scales, void* dgate_up, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const uint32_t lanes = (uint32_t)ceil_div(F, kMxGroup) * 2;
-  const dim3 grid((uint32_t)ceil_div(rows * lanes, 256));
+  const uint32_t lanes = (uint32_t)swiglu_lanes(F);
+  const LayerLaunch p = plan_swiglu(rows, F);
+  const dim3 grid((uint32_t)p.grid);
   if (in_bf16)
-    k_swiglu_bwd<uint16_t><<<grid, 256, 0, st>>>((const uint16_t*)dout, (uint32_t)rows, (uint32_t)F, lanes, kept,
+    k_swiglu_bwd<uint16_t><<<grid, p.block, 0, st>>>((const uint16_t*)dout, (uint32_t)rows, (uint32_t)F, lanes, kept,
                                                  kept_scales, (uint16_t*)dgate_up);
   else
-    k_swiglu_bwd<float><<<grid, 256, 0, st>>>((const float*)dout, (uint32_t)rows, (uint32_t)F, lanes, kept,
+    k_swiglu_bwd<float><<<grid, p.block, 0, st>>>((const float*)dout, (uint32_t)rows, (uint32_t)F, lanes, kept,
                                               kept_scales, (float*)dgate_up);
   return (int)hipGetLastError();
 }

@@ -224,15 +224,16 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
 
 template <bool MX8>
 static void wgrad_go(const WgradArgs& a, hipStream_t st) {
-  const int64_t tiles = ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK);
+  const LayerLaunch p = plan_wgrad(a.T, a.E, a.N, a.K, a.block);
+  const uint32_t grid = (uint32_t)p.grid;
   if (a.block) {
-    k_wgrad<MX8, true, 4><<<dim3((uint32_t)xcd_grid((a.T / a.block + a.E + 1) * tiles)), 256, 0, st>>>(a);
-    const int64_t join = ceil_div((int64_t)a.N * a.K, 1024);
-    k_wgrad_join<<<dim3((uint32_t)(join < 4096 ? join : 4096), (uint32_t)a.E), 256, 0, st>>>(a);
-  } else if (wgrad_narrow(a.T, a.E, tiles)) {
-    k_wgrad<MX8, false, 2><<<dim3((uint32_t)(a.E * xcd_grid(ceil_div(a.N, kWgN / 2) * ceil_div(a.K, kWgK)))), 256, 0, st>>>(a);
+    k_wgrad<MX8, true, 4><<<grid, p.block, 0, st>>>(a);
+    const LayerLaunch j = plan_wgrad_join(a.E, a.N, a.K);
+    k_wgrad_join<<<dim3((uint32_t)j.grid, (uint32_t)j.y), j.block, 0, st>>>(a);
+  } else if (wgrad_narrow(a.T, a.E, ceil_div(a.N, kWgN) * ceil_div(a.K, kWgK))) {
+    k_wgrad<MX8, false, 2><<<grid, p.block, 0, st>>>(a);
   } else {
-    k_wgrad<MX8, false, 4><<<dim3((uint32_t)(a.E * xcd_grid(tiles))), 256, 0, st>>>(a);
+    k_wgrad<MX8, false, 4><<<grid, p.block, 0, st>>>(a);
   }
 }
 

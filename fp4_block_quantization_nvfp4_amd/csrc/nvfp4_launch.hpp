@@ -89,8 +89,8 @@ struct WgradArgs {
   void* dw;            // [E, N, K]
   int T, E, N, K;
   int out_bf16;
-  int block;           // rows of a block (plan_wgrad), 0: whole experts
-  float* part;         // sums of blocks, [T / block + E][N][K]
+  int block;           // rows of a block (wgrad_block), 0: whole experts
+  float* part;         // sums of blocks, at most T / block + E + 1 of [N][K]
 };
 int launch_wgrad(const WgradArgs& a, void* stream);
 

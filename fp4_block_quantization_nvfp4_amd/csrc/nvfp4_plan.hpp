@@ -1,8 +1,9 @@
 // Launch geometry of every kernel, computed on the host from the shape only.
 // The launchers take their grids from these functions, and the test-support
-// entry point nvfp4_selftest_launch_plan returns the same numbers, so a CPU
-// test can check that every launch stays inside the dispatch limits (grid x
-// workgroup size below 2^32 work-items) for every accepted shape.
+// entry points nvfp4_selftest_launch_plan and nvfp4_selftest_layer_plan return
+// the same numbers, so a CPU test can check that every launch stays inside the
+// dispatch limits (grid x workgroup size below 2^32 work-items along each axis)
+// for every accepted shape.
 #pragma once
 
 #include <stdint.h>
@@ -115,6 +116,23 @@ inline LaunchPlan plan_amax(int64_t M, int64_t K, int per_row) {
 
 // ---- layer operators
 
+enum LayerKernel {
+  PLAN_NORM = 0,
+  PLAN_NORM_BWD = 1,
+  PLAN_SUM_ROWS = 2,
+  PLAN_SWIGLU = 3,  // both directions
+  PLAN_MATVEC = 4,
+  PLAN_GROUPED = 5,
+  PLAN_WGRAD = 6,
+  PLAN_WGRAD_JOIN = 7,
+};
+
+struct LayerLaunch {
+  int kernel;       // LayerKernel
+  int64_t grid, y;  // workgroups along x and y
+  int block;        // lanes per workgroup
+};
+
 // Norm: one workgroup a row, 16 elements a lane (32 for rows over 16384), at
 // most kNormMaxGrid workgroups (further rows in a loop).
 constexpr int64_t kNormMaxH = 32768;
@@ -122,6 +140,9 @@ constexpr int64_t kNormMaxGrid = int64_t(1) << 20;
 inline int norm_threads(int64_t H) {
   const int64_t per = H <= 16 * 1024 ? 16 : 32;
   return (int)ceil_div(ceil_div(H, per), 64) * 64;
+}
+inline LayerLaunch plan_norm(int64_t rows, int64_t H) {
+  return {PLAN_NORM, rows < kNormMaxGrid ? rows : kNormMaxGrid, 1, norm_threads(H)};
 }
 // Norm's gradient: workgroups, each with one partial row of dw.  About sixteen
 // waves on each of 256 CUs, and two rows a workgroup where there are few: a
@@ -132,6 +153,17 @@ inline int64_t norm_bwd_groups(int64_t rows, int64_t H) {
   if (g > 256 * cu) g = 256 * cu;
   return rows < g ? rows : g;
 }
+inline LayerLaunch plan_norm_bwd(int64_t rows, int64_t H) {
+  return {PLAN_NORM_BWD, norm_bwd_groups(rows, H), 1, norm_threads(H)};
+}
+inline LayerLaunch plan_sum_rows(int64_t H) { return {PLAN_SUM_ROWS, H / 16, 1, 256}; }
+
+// Gated activation, both directions: 16 elements a lane, rows padded to whole
+// mx8 groups of 32.
+inline int64_t swiglu_lanes(int64_t F) { return ceil_div(F, 32) * 2; }
+inline LayerLaunch plan_swiglu(int64_t rows, int64_t F) {
+  return {PLAN_SWIGLU, ceil_div(rows * swiglu_lanes(F), 256), 1, 256};
+}
 
 // Matrix products.
 constexpr int kMatvecThreads = 256;
@@ -140,10 +172,16 @@ constexpr int64_t kMatmulMaxE = 65534;             // grid y of k_matvec
 // Fragments of 16 n's per workgroup of k_matvec: more of them read x less often,
 // fewer spread a small weight over more CUs.  Four of them beside 16 rows of
 // bf16 in flight do not fit the registers (65536 x 7168, 16 rows: 83 us, with
-// two 63), so they take 8-bit rows or up to four rows an expert.
+// two 63), so they take 8-bit rows or up to four rows an expert, and not where 32
+// rows are taken at a time.
 inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;
-  return tiles >= 4096 && (mx8 || T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
+  return tiles >= 4096 && (mx8 ? T <= 16 * E : T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
+}
+// E = 0: one expert has all rows.  With experts, grid y has one row more, for
+// the rows that belong to none.
+inline LayerLaunch plan_matvec(int64_t T, int64_t E, int64_t N, bool mx8) {
+  return {PLAN_MATVEC, ceil_div(N, 16 * matvec_frags(T, N, E > 0 ? E : 1, mx8)), E > 0 ? E + 1 : 1, kMatvecThreads};
 }
 // Which kernel: few rows an expert, k_matvec, which decodes the weights anew
 // for every 32 rows (16 up to 16 an expert) but spreads them over many more
@@ -198,6 +236,17 @@ inline int64_t wgrad_block(int64_t T, int64_t E, int64_t N, int64_t K) {
   while ((T / b + E) * N * K * 4 > (int64_t(1) << 28)) b *= 2;
   const double whole = 1.1 * (double)(E > 1 ? 2 * T / E : T) / 64, split = 1.1 * (double)b / 64 + 0.05 * (double)(tiles * T) / (double)b + 8;
   return split < 0.8 * whole && b < T ? b : 0;
+}
+
+inline LayerLaunch plan_wgrad(int64_t T, int64_t E, int64_t N, int64_t K, int64_t block) {
+  const int64_t tiles = ceil_div(N, kWgN) * ceil_div(K, kWgK);
+  if (block) return {PLAN_WGRAD, xcd_grid((T / block + E + 1) * tiles), 1, 256};
+  const int64_t wn = wgrad_narrow(T, E, tiles) ? kWgN / 2 : kWgN;
+  return {PLAN_WGRAD, E * xcd_grid(ceil_div(N, wn) * ceil_div(K, kWgK)), 1, 256};
+}
+inline LayerLaunch plan_wgrad_join(int64_t E, int64_t N, int64_t K) {
+  const int64_t g = ceil_div(N * K, 1024);
+  return {PLAN_WGRAD_JOIN, g < 4096 ? g : 4096, E, 256};
 }
 
 }  // namespace nvfp4

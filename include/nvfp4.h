@@ -429,6 +429,20 @@ nvfp4_status nvfp4_selftest_scan(int kind, uint32_t param, uint64_t first, uint6
 nvfp4_status nvfp4_selftest_launch_plan(int entry, int64_t M, int64_t K, int in_bf16, int variant,
                                         int64_t* plan);
 
+/*
+ * nvfp4_selftest_layer_plan - the same for the layer operators.
+ *   entry    0 add_rms_norm (K is H), 1 its backward, 2 swiglu and its backward
+ *            (K is F), 3 matvec, 4 grouped_matmul, 5 grouped_wgrad,
+ *            6 grouped_wgrad_split.  Sizes that an entry point lacks are not
+ *            read.
+ *   mx8      rows with scales (it selects the kernel of few rows).
+ *   plan     HOST pointer to ten int64: {kernel id, workgroups along x, along y,
+ *            lanes per workgroup, rows of a tile or block (0: none)} of the first
+ *            launch and of the second (zeros: none).
+ */
+nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t N, int64_t K, int mx8,
+                                       int64_t* plan);
+
 #ifdef __cplusplus
 }
 #endif
