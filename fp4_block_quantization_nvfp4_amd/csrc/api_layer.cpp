@@ -122,6 +122,7 @@ static nvfp4_status products(const void* x, const uint8_t* x_scales, int64_t T, 
                              const float* amax, int mode, float bound, void* out, int out_dt, void* stream) {
   const nvfp4::MatmulArgs a = {x, x_scales, packed, scales, amax, ends, out, (int)T, (int)E, (int)N, (int)K,
                                blocks, mode, 6.0f * bound, out_dt == NVFP4_BF16};
+  if (K == 0) return hip_status(nvfp4::launch_zero(out, T * N * (out_dt == NVFP4_BF16 ? 2 : 4), stream));
   if (nvfp4::use_matvec(T, E, N)) return hip_status(nvfp4::launch_matvec(a, stream));
   return hip_status(x_scales ? nvfp4::launch_grouped_mx8(a, stream) : nvfp4::launch_grouped_bf16(a, stream));
 }
@@ -206,7 +207,9 @@ nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t 
   if (entry == 0) p[0] = nvfp4::plan_norm(T, K);
   if (entry == 1) p[0] = nvfp4::plan_norm_bwd(T, K), p[1] = nvfp4::plan_sum_rows(K);
   if (entry == 2) p[0] = nvfp4::plan_swiglu(T, K);
-  if (entry == 3 || entry == 4) {
+  if ((entry == 3 || entry == 4) && K == 0) {
+    p[0] = nvfp4::plan_zero(T * N * 4);
+  } else if (entry == 3 || entry == 4) {
     if (nvfp4::use_matvec(T, E, N)) {
       p[0] = nvfp4::plan_matvec(T, entry == 4 ? E : 0, N, mx8 != 0);
       rows = T > 16 * E ? 32 : 16;

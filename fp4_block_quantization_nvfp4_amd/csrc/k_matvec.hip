@@ -73,6 +73,16 @@ NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk
   }
 }
 
+// Clears `bytes` bytes.
+__global__ __launch_bounds__(256) void k_zero(uint8_t* __restrict__ out, int64_t bytes) {
+  const nv_u4 z = {0, 0, 0, 0};
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16; i < bytes; i += (int64_t)gridDim.x * 4096) {
+    if (i + 16 <= bytes) *reinterpret_cast<nv_u4*>(out + i) = z;
+    else
+      for (int64_t j = i; j < bytes; ++j) out[j] = 0;
+  }
+}
+
 // XM: rows of x that are taken at a time, 16 or 32.
 template <bool MX8, int BLK, bool WORDS, int R, int XM, bool GROUPED>
 __global__ __launch_bounds__(kMatvecThreads, XM == 16 ? 3 : 2) void k_matvec(MatmulArgs a) {
@@ -144,6 +154,12 @@ static void matvec_blk(const MatmulArgs& a, int r, bool more, hipStream_t st) {
   if (a.blocks == 0) words ? matvec_size<MX8, 0, true>(a, r, more, st) : matvec_size<MX8, 0, false>(a, r, more, st);
   else if (a.blocks == 1) words ? matvec_size<MX8, 1, true>(a, r, more, st) : matvec_size<MX8, 1, false>(a, r, more, st);
   else matvec_size<MX8, 2, false>(a, r, more, st);
+}
+
+int launch_zero(void* out, int64_t bytes, void* stream) {
+  const LayerLaunch p = plan_zero(bytes);
+  k_zero<<<(uint32_t)p.grid, p.block, 0, (hipStream_t)stream>>>((uint8_t*)out, bytes);
+  return (int)hipGetLastError();
 }
 
 int launch_matvec(const MatmulArgs& a, void* stream) {

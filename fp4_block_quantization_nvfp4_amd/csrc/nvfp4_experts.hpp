@@ -18,7 +18,8 @@ struct RowRange {
 };
 
 // One wave walks the ranges 64 at a time.  `tile` rows make a tile; a range
-// has ceil(rows / tile) of them.
+// has ceil(rows / tile) of them.  There are at most 2^29 rows (K >= 16), so a
+// tile more does not pass 31 bits.
 struct RangeScan {
   const int* ends;
   int E, T, tile, lane;

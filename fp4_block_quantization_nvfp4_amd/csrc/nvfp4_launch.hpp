@@ -77,6 +77,7 @@ struct MatmulArgs {
   int out_bf16;
 };
 int launch_matvec(const MatmulArgs& a, void* stream);
+int launch_zero(void* out, int64_t bytes, void* stream);  // products with K == 0
 int launch_grouped_mx8(const MatmulArgs& a, void* stream);
 int launch_grouped_bf16(const MatmulArgs& a, void* stream);
 

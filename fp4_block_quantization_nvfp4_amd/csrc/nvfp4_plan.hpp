@@ -125,6 +125,7 @@ enum LayerKernel {
   PLAN_GROUPED = 5,
   PLAN_WGRAD = 6,
   PLAN_WGRAD_JOIN = 7,
+  PLAN_ZERO = 8,
 };
 
 struct LayerLaunch {
@@ -194,6 +195,12 @@ inline LayerLaunch plan_matvec(int64_t T, int64_t E, int64_t N, bool mx8) {
 // x 4096, 96 rows 20 (31).
 inline bool use_matvec(int64_t T, int64_t E, int64_t N) {
   return T <= 16 * E || (T <= 96 * E && N * T <= (E > 1 ? 280000 : 600000));
+}
+// Products without a k (K == 0), which may have more rows than tiles fit a
+// launch: zeros, 16 bytes a lane and turn.
+inline LayerLaunch plan_zero(int64_t bytes) {
+  const int64_t g = ceil_div(bytes, 16 * 256);
+  return {PLAN_ZERO, g < 8192 ? g : 8192, 1, 256};
 }
 // Workgroups of k_grouped that run at a time: two on each of 256 CUs.
 constexpr int kGroupedSlots = 512;

@@ -8,7 +8,7 @@ import pytest
 
 from fp4_block_quantization_nvfp4_amd import _lib as L
 
-NORM, NORM_BWD, SUM_ROWS, SWIGLU, MATVEC, GROUPED, WGRAD, JOIN = range(8)
+NORM, NORM_BWD, SUM_ROWS, SWIGLU, MATVEC, GROUPED, WGRAD, JOIN, ZERO = range(9)
 MOST = 1 << 33
 SLOTS = 512
 
@@ -58,12 +58,13 @@ def test_swiglu_launches():
 
 def products():
     """Accepted (T, E, N, K), the extremes of each among them."""
-    got = [(1 << 29, 1, 16, 16), (1 << 29, 65534, 16, 16),
+    top = (1 << 31) - 1
+    got = [(top, 1, 1, 0), (top, 1, 4, 0), (top, 2, 4, 0), (1 << 30, 65534, 8, 0), (1 << 29, 1, 16, 16), (1 << 29, 65534, 16, 16),
            (1, 65534, 1 << 13, 16), (1 << 20, 65534, 1 << 13, 16), (1 << 13, 1, 1 << 20, 16), (1 << 13, 8, 1 << 20, 1 << 10),
            (1 << 13, 1, 16, 1 << 20), (1 << 13, 512, 16, 1 << 20), (1 << 20, 1, 1 << 13, 1 << 13)]
     r = random.Random(3)
     while len(got) < 400:
-        T, E, N = (int(2 ** r.uniform(0, top)) for top in (29, 16, 20))
+        T, E, N = (int(2 ** r.uniform(0, top)) for top in (30, 16, 20))
         K = 16 * int(2 ** r.uniform(0, 16))
         if E <= 65534 and T * N <= MOST and T * K <= MOST and E * N * K <= MOST:
             got.append((T, E, N, K))
@@ -77,6 +78,9 @@ def test_product_launches(entry, mx8):
         st, a, _ = plan(entry, T, E, N, K, mx8)
         assert st == L.OK, (T, E, N, K)
         check_limits(a, (T, E, N, K))
+        if K == 0:
+            assert a[0] == ZERO
+            continue
         # 32-bit row numbers, a tile added: no overflow
         assert T + max(a[4], 128) < 1 << 31
         if a[0] == MATVEC:
