@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256, NM == 4 ? 2 : MX8 ? 3 : 4) void k_wgrad(WgradA
       uint32_t lo[8], hi[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const nv_u2 p = mx8_to_bf16(vx[0][t], e8m0_value(vs[t]));
+        const nv_u2 p = mx8_to_bf16(vx[0][t], e8m0_scale(vs[t]));
         lo[t] = p.x;
         hi[t] = p.y;
       }

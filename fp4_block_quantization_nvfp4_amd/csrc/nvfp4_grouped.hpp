@@ -60,7 +60,7 @@ NV_DEV void grouped_tile(const MatmulArgs& a, uint16_t* lds, int e, int64_t row0
       if (Half::HALF < 256 && tid >= Half::HALF) return;
       const int r = h * (BM / 2) + i * (256 / PR) + xr;
       if (MX8) {
-        const float sc = e8m0_value(st.s[i]);
+        const float sc = e8m0_scale(st.s[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const nv_u2 u = mx8_to_bf16(st.c[i][2 * j], sc), v = mx8_to_bf16(st.c[i][2 * j + 1], sc);

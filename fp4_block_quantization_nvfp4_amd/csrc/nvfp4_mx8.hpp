@@ -5,7 +5,9 @@
 // row (the last group of a row may be shorter).  The scale is the smallest
 // 2^s, s >= -117, with max |finite value| <= 448 * 2^s; what is not finite is
 // coded as NaN.  s >= -117 keeps every value code * 2^s (smallest 2^-9 *
-// 2^-117) a normal bf16, so mx8 rows enter the matrix cores exactly.
+// 2^-117) a normal bf16, so mx8 rows enter the matrix cores exactly, but for one
+// at the top: finite values above 248 * 2^120 are rounded to 256 * 2^120 = 2^128,
+// which reads back as infinity.
 #pragma once
 
 #include "nvfp4_device.hpp"
@@ -60,9 +62,15 @@ NV_DEV uint32_t mx8_scale_byte(uint32_t m) {
   return (uint32_t)(e > 10 ? e : 10);
 }
 
-// Value of an e8m0 byte (a byte below 1 would be subnormal; the encoder gives
-// 10..247).  Byte 255 decodes to infinity.
-NV_DEV float e8m0_value(uint32_t byte) { return bits2f(byte << 23); }
+// An e8m0 byte as the scale of a conversion instruction, which takes the
+// exponent field alone: byte 0 stands for 2^-127 there, and 255 gives NaN.
+NV_DEV float e8m0_scale(uint32_t byte) { return bits2f(byte << 23); }
+
+// Value of an e8m0 byte, to multiply by: 2^-127 is subnormal, 255 is NaN.  (The
+// encoder gives 10..247.)
+NV_DEV float e8m0_value(uint32_t byte) {
+  return bits2f(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+}
 
 // Magnitude bits of 16 values, the largest finite one; what is not finite
 // counts as 0.
@@ -113,8 +121,8 @@ NV_DEV uint32_t mx8_encode16(const float v[16], nv_u4& codes) {
   return byte;
 }
 
-// Four e4m3 codes times a power of two -> four bf16, exact where the result
-// is a normal number.
+// Four e4m3 codes times a power of two (e8m0_scale) -> four bf16, exact where
+// the result is a normal number; from 2^128 on infinite.
 NV_DEV nv_u2 mx8_to_bf16(uint32_t w, float scale) {
   nv_u2 r;
   r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));

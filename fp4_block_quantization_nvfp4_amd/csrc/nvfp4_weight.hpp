@@ -62,7 +62,7 @@ struct RowsPiece {
       for (int d = 0; d < 4; ++d) f[d] = __builtin_bit_cast(nv_bf8, lds[row * kLanes + ((8 * grp + 4 * q + d) ^ (row % kLanes))]);
       return;
     }
-    const float sc = e8m0_value(s[g][q]);
+    const float sc = e8m0_scale(s[g][q]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const nv_u4 w = lds[row * kLanes + ((4 * grp + 2 * q + h) ^ (row % kLanes))];

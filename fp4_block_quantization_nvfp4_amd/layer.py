@@ -4,7 +4,8 @@
 [T, ceil(K / 32)], one power of two for each 32 consecutive elements of a row
 (the last group may be shorter; K % 16 == 0): the smallest one, from 2^-117
 up, under which no finite value exceeds 448; what is not finite becomes NaN.
-uint8 views of either are taken too.
+Any scale is read: 255 as NaN, values below 2^-126 possibly as zero, those from
+2^128 on as infinite.  uint8 views of either are taken too.
 
 4-bit weights are the outputs of `quantize`, `quantize_4over6`, `quantize_2d`,
 `quantize_rowcol` and `quantize_4over6_2d`, for experts stacked along a first

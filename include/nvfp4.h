@@ -274,8 +274,9 @@ nvfp4_status nvfp4_quantize_4over6_2d(const void* x, nvfp4_dtype dt, int64_t M, 
  * [T, ceil(K / 32)]; the last group of a row may be shorter (K % 16 == 0).
  * The scale is the smallest 2^s, s >= -117, with max |finite value| <=
  * 448 * 2^s, codes are rounded to nearest even, and what is not finite is
- * coded as NaN.  Where mx8 rows are read, any scale byte is taken; values
- * below 2^-126 may count as zero.
+ * coded as NaN.  Where mx8 rows are read, any scale byte is taken, 255 as NaN;
+ * values below 2^-126 may count as zero, and those from 2^128 on are infinite
+ * (finite values above 248 * 2^120 are rounded to 2^128 when coded).
  *
  * Weights are those that nvfp4_quantize, nvfp4_quantize_2d and the
  * four-over-six entry points write: packed [E, N, K/2], scales by `blocks`,

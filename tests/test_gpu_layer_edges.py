@@ -38,3 +38,93 @@ def test_products_without_a_k(T, N, dt, experts):
         st = L.lib().nvfp4_matvec(None, None, T, N, 0, None, None, 0, None, 0, 448.0, p, dt, stream())
     assert st == L.OK
     assert not out[:size].any() and bool((out[size:] == 0x5A).all())
+
+
+def row_values(c, s):
+    """mx8 rows as the format defines them: byte 255 is NaN, and what passes the
+    range of fp32 (2^128, from bytes 247 up) is infinite."""
+    v = R.mx8_values(c, s)
+    v = torch.where(v.abs() >= 2.0 ** 128, torch.copysign(torch.tensor(float("inf"), dtype=v.dtype), v), v)
+    return torch.where((s == 255).repeat_interleave(32, 1)[:, :c.shape[1]], float("nan"), v)
+
+
+LOW, HIGH = [0, 1, 2, 5, 9, 10], [200, 246, 247, 248, 250, 253, 254]
+
+
+@pytest.mark.parametrize("scales", [LOW, HIGH, [255]], ids=["low", "high", "nan"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_swiglu_backward_reads_any_scale(scales, dtype):
+    """Each scale byte with every code, or every one below 1 (below 2^-126 a value
+    may count as zero), beside groups under scale 1."""
+    T, F, G = len(scales), 64, 2
+    c = torch.arange(T * 2 * F).view(T, 2 * F) * 37 % (0x7F if scales is LOW else 0x38)
+    s = torch.full((T, 2 * G), 127)
+    s[:, 0] = torch.tensor(scales)  # the first group of g; below that of u, so that products of both stay in range
+    s[:, 2] = torch.tensor([255 if b == 255 else 230 if b < 127 else 254 - b for b in scales])
+    d = torch.full((T, F), 0.5, dtype=dtype)
+    if scales is LOW:
+        d *= 2.0 ** 10
+    got = R.f64(nv.swiglu_backward(d.cuda(), c.to(torch.uint8).cuda(), s.to(torch.uint8).cuda()))
+    g, u = row_values(c[:, :F], s[:, :G]), row_values(c[:, F:], s[:, G:])
+    if scales == [255]:
+        assert torch.isnan(got[:, :32]).all() and torch.isnan(got[:, F:F + 32]).all()
+        assert torch.isfinite(got[:, 32:F]).all() and torch.isfinite(got[:, F + 32:]).all()
+        return
+    dg, du = R.swiglu_gradient(R.f64(d), g, u)
+    # as check_swiglu: roundings of sigma and of the products; d u and d g may each be off
+    # by d times what counts as zero, 2^-126, and dgate by that times u
+    sig = 1 / (1 + torch.exp(-g))
+    lost = 2.0 ** -125 * R.f64(d).abs()
+    most = dg.abs() * R.half_step(dtype) + 64 * R.U24 * R.f64(d).abs() * u.abs() * sig * (1 + g.abs()) + lost * (1 + u.abs())
+    R.assert_near(got[:, :F], dg, most, "dgate")
+    R.assert_near(got[:, F:], du, du.abs() * (R.half_step(dtype) + 64 * R.U24) + lost, "dup")
+
+
+def one_a_row(T, K, scales):
+    """mx8 rows with one code in each, the groups' scales `scales` in turn."""
+    c = torch.zeros(T, K, dtype=torch.long)
+    at = torch.arange(T) * 5 % K
+    c[torch.arange(T), at] = 0x7E - torch.arange(T) * 3 % 0x7E if scales is LOW else 1 + torch.arange(T) % 0x37
+    s = torch.tensor([scales[(t + j) % len(scales)] for t in range(T) for j in range((K + 31) // 32)]).view(T, -1)
+    return c, s
+
+
+@pytest.mark.parametrize("T", [4, 16, 60, 400])
+@pytest.mark.parametrize("scales", [LOW, HIGH], ids=["low", "high"])
+def test_products_read_any_scale(T, scales):
+    N, K = 48, 160
+    g = torch.Generator().manual_seed(T)
+    c, xs = one_a_row(T, K, scales)
+    p = torch.randint(0, 256, (1, N, K // 2), dtype=torch.uint8, generator=g)
+    s = torch.randint(1, 9, (1, N, K // 16), dtype=torch.uint8, generator=g) + (0x70 if scales is LOW else 0)
+    xv, w = row_values(c, xs), R.weight_values(p, s, "1x16")[0]
+    y = xv @ w.t()
+    most = R.product_bound(xv, w, F32, y) + 2.0 ** -126 * (w.abs().sum(1) + 1)
+    ends = torch.tensor([T], dtype=torch.int32, device="cuda")
+    x, xsd = c.to(torch.uint8).cuda(), xs.to(torch.uint8).cuda()
+    R.assert_near(nv.grouped_matmul(x, ends, p.cuda(), s.cuda(), x_scale=xsd, out_dtype=F32), y, most, "grouped")
+    R.assert_near(nv.matvec(x, p[0].cuda(), s[0].cuda(), x_scale=xsd, out_dtype=F32), y, most, "matvec")
+    dy = (torch.randint(-8, 9, (T, N), generator=g) / 16).to(BF)
+    dw = R.f64(dy).t() @ xv
+    most = (T + 8) * 2.0 ** -23 * (R.f64(dy).abs().t() @ xv.abs()) + 2.0 ** -126 * (T + 1)
+    R.assert_near(nv.grouped_wgrad(dy.cuda(), x, ends, x_scale=xsd)[0], dw, most, "dw")
+
+
+@pytest.mark.parametrize("T", [4, 60, 400])
+def test_products_of_a_nan_scale(T):
+    """Byte 255 makes its 32 elements NaN, codes of zero among them: the row of a
+    product, and in the weight gradient those columns of its own expert."""
+    N, K = 48, 160
+    g = torch.Generator().manual_seed(T)
+    c = torch.randint(0, 0x38, (T, K), generator=g)
+    xs = torch.full((T, K // 32), 127)
+    c[1, 32:64], xs[1, 1] = 0, 255
+    p = torch.randint(0, 256, (2, N, K // 2), dtype=torch.uint8, generator=g).cuda()
+    s = torch.randint(0x30, 0x40, (2, N, K // 16), dtype=torch.uint8, generator=g).cuda()
+    ends = torch.tensor([2, T], dtype=torch.int32, device="cuda")
+    x, xsd = c.to(torch.uint8).cuda(), xs.to(torch.uint8).cuda()
+    keep = torch.arange(T) != 1
+    for y in (nv.grouped_matmul(x, ends, p, s, x_scale=xsd, out_dtype=F32), nv.matvec(x, p[0], s[0], x_scale=xsd, out_dtype=F32)):
+        assert torch.isnan(y[1]).all() and torch.isfinite(y.cpu()[keep]).all()
+    dw = nv.grouped_wgrad(torch.ones(T, N, dtype=BF, device="cuda"), x, ends, x_scale=xsd)
+    assert torch.isnan(dw[0, :, 32:64]).all() and int(torch.isnan(dw).sum()) == 32 * N

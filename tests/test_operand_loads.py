@@ -19,7 +19,7 @@ namespace nvfp4 {
 typedef short nv_bf8 __attribute__((ext_vector_type(8)));
 typedef float nv_f4 __attribute__((ext_vector_type(4)));
 constexpr int kMxGroup = 32;
-NV_DEV float e8m0_value(uint32_t) { return 0.0f; }
+NV_DEV float e8m0_scale(uint32_t) { return 0.0f; }
 NV_DEV nv_u2 mx8_to_bf16(uint32_t, float) { return nv_u2{0, 0}; }
 NV_DEV nv_bf8 fp4_to_bf16(uint32_t, float) { return nv_bf8{}; }
 NV_DEV float e4m3_byte(uint32_t, int) { return 0.0f; }
