@@ -8,7 +8,7 @@ import fp4_block_quantization_nvfp4_amd as nv
 from fp4_block_quantization_nvfp4_amd import _lib as L
 from tests import layer_ref as R
 from tests.gpu_util import need_gpu
-from tests.test_gpu_layer import BF, F32
+from tests.test_gpu_layer import BF, F32, check_norm, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,27 @@ def test_products_of_a_nan_scale(T):
         assert torch.isnan(y[1]).all() and torch.isfinite(y.cpu()[keep]).all()
     dw = nv.grouped_wgrad(torch.ones(T, N, dtype=BF, device="cuda"), x, ends, x_scale=xsd)
     assert torch.isnan(dw[0, :, 32:64]).all() and int(torch.isnan(dw).sum()) == 32 * N
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [96, 2064, 16400])
+@pytest.mark.parametrize("res", [True, False], ids=["residual", "plain"])
+def test_norm_of_rows_far_from_one(H, dtype, res):
+    """Rows whose squares pass the range of fp32 at either end, eps = 0, between
+    ordinary ones: y and rstd are as for any other row."""
+    by = torch.tensor([1.0, 1e20, 2.0 ** 80, 1.0, 1e-24, 2.0 ** -120, 3e37, 1e-20])[:, None]
+    g = gen(H)
+    x, r = randn(g, 8, H, dtype=F32) * by, randn(g, 8, H, dtype=F32) * by
+    w = 1 + 0.2 * torch.randn(H, generator=g)
+    dy, dh = randn(g, 8, H, dtype=dtype), randn(g, 8, H, dtype=dtype)
+    check_norm(x.to(dtype), r.to(dtype) if res else None, w, eps=0.0, upstream=(dy, dh))
+
+
+def test_norm_of_rows_of_subnormals():
+    """1 over the root passes fp32 (rstd infinite); y does not."""
+    x = torch.full((3, 96), 2.0 ** -132).to(BF)
+    x[1], x[2, 5:] = 1.0, 0.0
+    codes, scales, _, rstd = nv.add_rms_norm(x.cuda(), torch.ones(96, device="cuda"), eps=0.0)
+    h = R.f64(x)
+    R.assert_mx8(codes, scales, h / h.square().mean(1, keepdim=True).sqrt(), 2.0 ** -20, "norm")
+    assert torch.isinf(rstd[0]) and rstd[1] == 1
