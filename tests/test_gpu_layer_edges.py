@@ -152,3 +152,19 @@ def test_norm_of_rows_of_subnormals():
     h = R.f64(x)
     R.assert_mx8(codes, scales, h / h.square().mean(1, keepdim=True).sqrt(), 2.0 ** -20, "norm")
     assert torch.isinf(rstd[0]) and rstd[1] == 1
+
+
+@pytest.mark.parametrize("H", [16, 2064])
+@pytest.mark.parametrize("big", [0, 1, 31, 63])
+def test_norm_weight_gradient_keeps_small_terms(H, big):
+    """One large term and 63 that are below half its last place each but not
+    together: 64 rows are a partial sum each, and these are joined in pairs, so a
+    result is off by at most the six roundings of its way there (and four of the
+    terms), not by one a row."""
+    T = 64
+    dy = torch.full((T, H), 1.9 * 2.0 ** -25)
+    dy[big] = 1.0
+    one = torch.ones(T, H)
+    _, dw = nv.add_rms_norm_backward(dy.cuda(), one.cuda(), torch.ones(H, device="cuda"), torch.ones(T, device="cuda"))
+    want = R.f64(dy).sum(0)
+    R.assert_near(dw, want, 10 * R.U24 * want, "dweight")
