@@ -48,7 +48,7 @@ def _run(cmd, verbose):
     # the host pass does not know the packed-fp32 feature name; that warning is expected
     err = "\n".join(l for l in res.stderr.splitlines() if "packed-fp32-ops" not in l and l.strip())
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}): {' '.join(cmd)}\n{res.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}): {' '.join(cmd)}\n{res.stderr}")
     if err and verbose:
         print(err, file=sys.stderr)
 
@@ -69,9 +69,18 @@ def bind_commands(obj: str, out: str):
              "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"])
 
 
+def _compile_bind(obj: str, out: str, verbose: bool):
+    """Compiles the binding; the command that links it."""
+    compile_bind, link_bind = bind_commands(obj, out)
+    _run(compile_bind, verbose)
+    return link_bind
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile every source to an object in parallel, then link the shared
-    library and the binding; each result replaces its file atomically."""
+    library and the binding; each result replaces its file atomically.  The
+    library is made whether or not the binding can be: what fails there is raised
+    afterwards, and a binding of an older library is taken away."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     inc = ["-I", os.path.join(os.path.dirname(HERE), "include")]
     compile_flags = [f for f in FLAGS if f != "-shared"]
@@ -81,17 +90,21 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
             obj = os.path.join(tmpd, os.path.basename(src) + ".o")
             objs.append(obj)
             cmds.append([hipcc, *compile_flags, *inc, "-c", "-o", obj, src])
-        bind_obj, bind_tmp = os.path.join(tmpd, "layer.o"), BIND + ".tmp"
-        compile_bind, link_bind = bind_commands(bind_obj, bind_tmp)
-        cmds.append(compile_bind)
-        with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(cmds)))) as ex:
+        bind_tmp = BIND + ".tmp"
+        with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(cmds) + 1))) as ex:
+            bind = ex.submit(_compile_bind, os.path.join(tmpd, "layer.o"), bind_tmp, verbose)
             for f in [ex.submit(_run, c, verbose) for c in cmds]:
                 f.result()
         tmp = LIB + ".tmp"
         _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
         os.replace(tmp, LIB)
-        _run(link_bind, verbose)
-        os.replace(bind_tmp, BIND)
+        try:
+            _run(bind.result(), verbose)
+            os.replace(bind_tmp, BIND)
+        except BaseException:
+            if os.path.exists(BIND):
+                os.remove(BIND)
+            raise
     return LIB
 
 
