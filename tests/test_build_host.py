@@ -40,7 +40,7 @@ def test_both_are_replaced(made):
     assert made["commands"][-1] == "_layer.so.tmp" and made["commands"].count("libnvfp4.so.tmp") == 1
 
 
-@pytest.mark.parametrize("what", ["layer.cpp", "-ltorch_python"], ids=["compile", "link"])
+@pytest.mark.parametrize("what", [os.path.join("bind", "layer.cpp"), "-ltorch_python"], ids=["compile", "link"])
 def test_a_binding_that_fails_leaves_the_library(made, what):
     made["fail"] = what
     with pytest.raises(RuntimeError):
