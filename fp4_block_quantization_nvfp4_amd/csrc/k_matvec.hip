@@ -8,9 +8,14 @@
 // and turned into fragments in shared memory: read by fragments, 16 rows of 64
 // bytes, the same loop moves 2.3 TB/s instead of 4.8 (65536 x 7168, 16 rows).
 // The next piece is in flight while one is decoded and multiplied.  The waves'
-// sums join in shared memory, in a fixed order.  With experts, grid y walks
-// the experts and the rows of one are taken 16 at a time; the row of the grid
-// past the last expert clears the rows that belong to none.
+// sums join in shared memory, in a fixed order.
+//
+// With experts, the rows of each, and those of none (cleared), make tiles of 16
+// (or 32), and the workgroups along grid y take all experts' tiles in turn.  T <=
+// 16 E rows are at most 2 E + 1 tiles (T <= 96 E in 32s: 4 E + 1), so E + 1
+// workgroups have two (four) each, however uneven the experts are.  Where a
+// workgroup had all rows of one expert, 2048 rows of one of 128 experts 4096 x 2048
+// took 637 us, now 139 (even: 194, 197); 512 of one of 32 150, now 34 (even 40, 39).
 #include "nvfp4_experts.hpp"
 #include "nvfp4_launch.hpp"
 #include "nvfp4_plan.hpp"
@@ -21,9 +26,9 @@ namespace nvfp4 {
 // This wave's share of the products of 16 R rows of the weight with up to XR
 // rows of x; own: its shared memory.
 template <bool MX8, int BLK, bool WORDS, int R, int XR, int G>
-NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk, nv_u4* own, nv_f4 acc[R][G]) {
+NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk, nv_u4* own, int first, int lane,
+                        nv_f4 acc[R][G]) {
   constexpr int W = kMatvecThreads / 64;
-  const int lane = threadIdx.x & 63;
   RowsPiece<MX8, XR> xp;
   WeightPiece<BLK, WORDS> wp[R], wn[R];
   auto load = [&](int kt) {
@@ -31,7 +36,6 @@ NV_DEV void matvec_sums(const RowsView<MX8>& x, const WeightView<BLK>& w, int nk
     for (int r = 0; r < R; ++r) wn[r].load(w, r, lane, kt * 256);
     xp.load(x, lane, kt * 256);
   };
-  const int first = uniform(threadIdx.x >> 6);
   load(first);
   for (int k = first; k < nk; k += W) {
 #pragma unroll
@@ -90,29 +94,31 @@ __global__ __launch_bounds__(kMatvecThreads, XM == 16 ? 3 : 2) void k_matvec(Mat
   constexpr int ROWS = XM * (MX8 ? 16 : 32), SPAN = ROWS > R * 128 ? ROWS : R * 128;  // SPAN: 16-byte chunks of a wave's own memory
   static_assert(SPAN >= R * G * 64, "the sums fit where codes and rows go");
   __shared__ nv_u4 lds[W * SPAN];
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
   const int n0 = (int)blockIdx.x * (16 * R);
-  RowRange rr = {0, 0, a.T, 0};
-  if (GROUPED) {
-    if ((int)blockIdx.y < a.E) rr = expert_range(a.ends, a.T, blockIdx.y);
-    else rr = expert_range(a.ends, a.T, a.E - 1), rr.row0 += rr.rows, rr.rows = a.T - rr.row0, rr.e = a.E;
-  }
-  if (rr.rows <= 0) return;
-  const bool none = rr.e >= a.E;
-  const WeightView<BLK> w(a, none ? 0 : rr.e, n0, 16 * R);
-  const int nk = none ? 0 : (a.K + 255) / 256;
   nv_u4* own = lds + wave * SPAN;
-  for (int t0 = 0; t0 < rr.rows; t0 += XM) {
-    const int row0 = rr.row0 + t0, rows = rr.rows - t0 < XM ? rr.rows - t0 : XM;
+  int tiles = GROUPED ? a.T : (a.T + XM - 1) / XM;  // with experts their tiles, once known
+  for (int unit = blockIdx.y; unit < tiles; unit += gridDim.y) {
+    RowRange rr = {0, 0, a.T, 0};
+    if (GROUPED) rr = range_of_tile(a.ends, a.E, a.T, XM, unit, tiles);
+    const int t0 = (unit - rr.before) * XM, left = rr.rows - t0;
+    if (left <= 0) return;
+    if (unit != (int)blockIdx.y) __syncthreads();  // the sums are read before the next rows go where they lie
+    int lane = threadIdx.x & 63;
+    asm("" : "+v"(lane));  // else what follows from it stays in registers from tile to tile
+    const bool none = GROUPED && rr.e >= a.E;
+    const WeightView<BLK> w(a, none ? 0 : rr.e, n0, 16 * R);
+    const int nk = none ? 0 : (a.K + 255) / 256;
+    const int row0 = rr.row0 + t0, rows = left < XM ? left : XM;
     const RowsView<MX8> x(a, row0, rows);
     nv_f4 acc[R][G];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int g = 0; g < G; ++g) acc[r][g] = nv_f4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (XM == 32 && rows > 16) matvec_sums<MX8, BLK, WORDS, R, XM, G>(x, w, nk, own, acc);
-    else if (XM == 32 || rows > 4) matvec_sums<MX8, BLK, WORDS, R, 16, G>(x, w, nk, own, acc);
-    else matvec_sums<MX8, BLK, WORDS, R, 4, G>(x, w, nk, own, acc);
+    if (XM == 32 && rows > 16) matvec_sums<MX8, BLK, WORDS, R, XM, G>(x, w, nk, own, wave, lane, acc);
+    else if (XM == 32 || rows > 4) matvec_sums<MX8, BLK, WORDS, R, 16, G>(x, w, nk, own, wave, lane, acc);
+    else matvec_sums<MX8, BLK, WORDS, R, 4, G>(x, w, nk, own, wave, lane, acc);
     float* sums = reinterpret_cast<float*>(lds);  // of wave v: at v * SPAN * 4
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -129,7 +135,6 @@ __global__ __launch_bounds__(kMatvecThreads, XM == 16 ? 3 : 2) void k_matvec(Mat
       for (int v = 0; v < W; ++v) s += sums[v * SPAN * 4 + i];
       store_out(a, none ? 0.0f : s * second_scale(a, rr.e, n), row0 + t, n);
     }
-    if (t0 + XM < rr.rows) __syncthreads();  // the sums are read before the next rows go where they lie
   }
 }
 

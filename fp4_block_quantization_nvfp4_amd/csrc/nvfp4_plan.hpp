@@ -179,8 +179,8 @@ inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;
   return tiles >= 4096 && (mx8 ? T <= 16 * E : T <= 4 * E) ? 4 : tiles >= 1024 ? 2 : 1;
 }
-// E = 0: one expert has all rows.  With experts, grid y has one row more, for
-// the rows that belong to none.
+// E = 0: one expert has all rows.  With experts, the E + 1 workgroups along grid y
+// take all ranges' tiles in turn (the rows of none are a range too).
 inline LayerLaunch plan_matvec(int64_t T, int64_t E, int64_t N, bool mx8) {
   return {PLAN_MATVEC, ceil_div(N, 16 * matvec_frags(T, N, E > 0 ? E : 1, mx8)), E > 0 ? E + 1 : 1, kMatvecThreads};
 }

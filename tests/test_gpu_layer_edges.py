@@ -8,7 +8,7 @@ import fp4_block_quantization_nvfp4_amd as nv
 from fp4_block_quantization_nvfp4_amd import _lib as L
 from tests import layer_ref as R
 from tests.gpu_util import need_gpu
-from tests.test_gpu_layer import BF, F32, check_norm, gen, randn
+from tests.test_gpu_layer import BF, F32, check_grouped, check_norm, gen, randn, rows, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,51 @@ def test_norm_weight_gradient_keeps_small_terms(H, big):
     _, dw = nv.add_rms_norm_backward(dy.cuda(), one.cuda(), torch.ones(H, device="cuda"), torch.ones(T, device="cuda"))
     want = R.f64(dy).sum(0)
     R.assert_near(dw, want, 10 * R.U24 * want, "dweight")
+
+
+HOT = [(512, 32, 80, 272, 7), (300, 20, 48, 144, 0), (2000, 130, 64, 80, 100), (700, 8, 176, 80, 7), (90, 1, 64, 272, 0),
+       (400, 70, 32, 64, 69)]
+
+
+@pytest.mark.parametrize("T,E,N,K,e", HOT)
+@pytest.mark.parametrize("kind", ["all", "most", "none"])
+@pytest.mark.parametrize("mx8", [False, True], ids=["bf16", "mx8"])
+def test_one_expert_has_nearly_all_rows(T, E, N, K, e, kind, mx8):
+    """Rows of one expert that many workgroups share, with others' and none's."""
+    counts = torch.zeros(E, dtype=torch.int32)
+    if kind == "most":
+        counts += 1
+    counts[e] += {"all": T, "most": T - E - 3, "none": 5}[kind]
+    ends = torch.cumsum(counts, 0).int()
+    x, xs, xv = rows(T + e, T, K, mx8)
+    p, s, a = weights(E, E, N, K)
+    y = check_grouped(x, xs, xv, ends, p, s, a, "1x16", F32, what=kind)
+    assert torch.equal(y, nv.grouped_matmul(x, ends.cuda(), p, s, x_scale=xs, global_amax=a, out_dtype=F32))
+
+
+def test_one_hot_expert_takes_no_longer_than_even_ones():
+    """Its rows are shared by the workgroups of all experts: the time stays near
+    that of an even split, which reads 32 times the weights (of one workgroup's
+    making, it was 3.7 times that)."""
+    T, E, N, K = 512, 32, 4096, 2048
+    p = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda")
+    s = torch.full((E, N, K // 16), 0x38, dtype=torch.uint8, device="cuda")
+    x = torch.randn(T, K, device="cuda").to(BF)
+
+    def time(counts):
+        ends = torch.cumsum(torch.tensor(counts), 0).int().cuda()
+        for _ in range(20):
+            nv.grouped_matmul(x, ends, p, s)
+        got = []
+        for _ in range(9):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(20):
+                nv.grouped_matmul(x, ends, p, s)
+            b.record()
+            b.synchronize()
+            got.append(a.elapsed_time(b))
+        return sorted(got)[4]
+
+    even, hot = time([T // E] * E), time([0] * 5 + [T] + [0] * (E - 6))
+    assert hot < 1.5 * even, (hot, even)

@@ -136,6 +136,23 @@ def test_grouped_grids_hold_every_unit():
     assert len(seen) == 6
 
 
+def test_matvec_workgroups_have_few_tiles_each():
+    """Whatever the experts' rows, tiles of 16 rows are at most two a workgroup,
+    of 32 rows four."""
+    rng = random.Random(9)
+    seen = set()
+    for _ in range(2000):
+        E, N = rng.choice((1, 2, 8, 63, 64, 130, 1000)), int(2 ** rng.uniform(0, 13))
+        T = int(2 ** rng.uniform(0, 16))
+        st, a, _ = plan(4, T, E, N, 64)
+        if a[0] != MATVEC:
+            continue
+        seen.add(a[4])
+        tiles = sum(ceil(n, a[4]) for n in ranges(rng, T, E))
+        assert ceil(tiles, a[2]) <= (2 if a[4] == 16 else 4), (T, E, N, a, tiles)
+    assert seen == {16, 32}
+
+
 def test_wgrad_launches_and_workspace():
     rng = random.Random(6)
     splits = 0
