@@ -184,17 +184,23 @@ inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
 inline LayerLaunch plan_matvec(int64_t T, int64_t E, int64_t N, bool mx8) {
   return {PLAN_MATVEC, ceil_div(N, 16 * matvec_frags(T, N, E > 0 ? E : 1, mx8)), E > 0 ? E + 1 : 1, kMatvecThreads};
 }
-// Which kernel: few rows an expert, k_matvec, which decodes the weights anew
-// for every 32 rows (16 up to 16 an expert) but spreads them over many more
-// workgroups.  Up to 96 rows an expert it is the faster one while there is
-// little to decode: its time grows with N T, and with how uneven the experts
-// are, that of k_grouped on a part of the chip only with k.  Measured, us
-// (k_grouped): 8 experts 2048 x 2048, 20 rows each 16.5 (18.8), 32 rows 23.4
-// (18.7); 4 experts 1040 x 4096, 64 rows each 26 (34), 96 rows 37 (31); 6
-// experts 1024 x 1024, 32 rows each 9.3 (11.6), 64 rows 15.1 (12.7); one of 4096
-// x 4096, 96 rows 20 (31).
+// Which kernel.  k_matvec decodes the weights anew for every 32 rows (16 up to 16
+// an expert) but spreads them over many more workgroups; k_grouped decodes them
+// once for up to 128 rows.  Up to 16 rows an expert the weights bound, and it is
+// k_matvec; past that while its work, tiles of 32 rows times fragments of 16 n's,
+// stays near what the chip runs at a time (512 workgroups of two fragments).  How
+// many tiles T rows make goes by the experts' rows: T / 32 + E / 2 is taken, what
+// rows that differ from expert to expert come to.  Measured, us, k_matvec
+// (k_grouped), such rows: 8 experts 2048 x 2048, 160 rows 13.1 (15.3), 256 rows 16.3
+// (15.3); 16 of 1024 x 2048, 320 rows 13.0 (15.2); 6 of 1024 x 1024, 192 rows 8.5
+// (9.6), 384 rows 11.2 (11.4); 4 of 1040 x 4096, 256 rows 20 (30); 32 of 512 x 512,
+// 1024 rows 10.9 (7.1).  Even rows come to fewer tiles: 8 of 2048 x 2048, 256 rows
+// 10.0 (15.3).  One expert: 4096 x 4096, 96 rows 17 (31); 16384 x 4096, 32 rows 16
+// (34).  Of up to 16 rows an expert small weights are the exception: 128 of 512 x
+// 512, 1024 rows 15.4 (9.4); 32 of 4096 x 2048, 256 rows 41 (43).
 inline bool use_matvec(int64_t T, int64_t E, int64_t N) {
-  return T <= 16 * E || (T <= 96 * E && N * T <= (E > 1 ? 280000 : 600000));
+  if (T <= 16 * E) return true;
+  return T <= 96 * E && (E > 1 ? (T + 16 * E) * ceil_div(N, 16) <= 32 * 1152 : N * T <= 600000);
 }
 // Products without a k (K == 0), which may have more rows than tiles fit a
 // launch: zeros, 16 bytes a lane and turn.

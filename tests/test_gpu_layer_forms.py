@@ -64,7 +64,7 @@ def weight(seed, E, N, K, blocks):
     (2500, 3, 3600, 272, (128, 256)), (2304, 1, 4112, 528, (128, 256)),
     (2048, 32, 1552, 144, (64, 256)), (1100, 16, 2576, 336, (64, 256)),
     (700, 16, 2320, 272, (32, 256)), (900, 40, 1552, 128, (32, 256)),
-    (700, 3, 400, 272, (128, 128)), (200, 3, 1552, 400, (64, 128)), (150, 3, 2000, 208, (32, 128))])
+    (700, 3, 400, 272, (128, 128)), (200, 3, 2576, 400, (64, 128)), (150, 3, 3200, 208, (32, 128))])
 def test_grouped_tiles(T, E, N, K, tile, blocks, mx8):
     assert tile_of(T, E, N, K, mx8) == tile
     x, xs, xv = rows(T + K, T, K, mx8)

@@ -188,3 +188,16 @@ def test_plan_refusals():
     assert plan(4, 16, 0)[0] == L.E_SHAPE and plan(5, 16, 1, 24, 16)[0] == L.E_SHAPE
     assert plan(3, 1 << 31)[0] == L.E_RANGE and plan(2, 1 << 20, K=8192)[0] == L.E_RANGE
     assert L.lib().nvfp4_selftest_layer_plan(0, 16, 1, 16, 16, 0, None) == L.E_NULL
+
+
+# (E, N, rows in all) and the kernel that was the faster one there, by 5% or more
+# on rows that differ from expert to expert; with k from 512 to 8192
+MEASURED = [(8, 2048, 128, MATVEC), (8, 2048, 160, MATVEC), (8, 2048, 256, GROUPED), (8, 2048, 384, GROUPED), (6, 1024, 192, MATVEC),
+            (6, 1024, 576, GROUPED), (4, 1040, 256, MATVEC), (4, 1040, 384, MATVEC), (16, 1024, 320, MATVEC), (32, 512, 544, MATVEC),
+            (32, 512, 1024, GROUPED), (32, 512, 2048, GROUPED), (64, 2048, 1088, GROUPED), (64, 2048, 2048, GROUPED), (1, 4096, 96, MATVEC),
+            (1, 16384, 32, MATVEC), (1, 1024, 96, MATVEC), (32, 4096, 64, MATVEC), (16, 4096, 192, MATVEC), (8, 4096, 96, MATVEC)]
+
+
+@pytest.mark.parametrize("E,N,T,kernel", MEASURED)
+def test_products_take_the_kernel_that_was_faster(E, N, T, kernel):
+    assert plan(4, T, E, N, 2048)[1][0] == kernel
