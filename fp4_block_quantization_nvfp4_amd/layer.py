@@ -12,9 +12,15 @@ Any scale is read: 255 as NaN, values below 2^-126 possibly as zero, those from
 axis.  As in `dequantize`, `tile16`, `global_amax`, `row_scaled` and `bound`
 name the producer's scales.
 
-Every function runs on torch's current stream, allocates its outputs with
-torch and computes in the HIP kernels.  The rows are contiguous tensors; there
-is no CPU path.
+Every function runs on torch's current stream, on the current device, allocates
+its outputs with torch and computes in the HIP kernels.  The rows are contiguous
+tensors; there is no CPU path.
+
+Nothing is recorded for autograd: inputs that require a gradient are taken as
+they are, and the outputs require none.  A training step calls the gradients by
+name, as examples/expert_layer.py does: `add_rms_norm_backward`,
+`swiglu_backward`, `grouped_matmul` with the transposed weights and
+`grouped_wgrad`.
 """
 from __future__ import annotations
 

@@ -216,3 +216,14 @@ def test_one_hot_expert_takes_no_longer_than_even_ones():
 
     even, hot = time([T // E] * E), time([0] * 5 + [T] + [0] * (E - 6))
     assert hot < 1.5 * even, (hot, even)
+
+
+def test_nothing_is_recorded_for_autograd():
+    """As layer.py says: inputs that require a gradient are taken, outputs require none."""
+    x = torch.randn(8, 64, device="cuda").to(BF).requires_grad_()
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    p, s, a = weights(1, 1, 32, 64)
+    codes, scales, hidden, rstd = nv.add_rms_norm(x, w, x)
+    assert not any(t.requires_grad for t in (codes, scales, hidden, rstd, nv.matvec(x, p[0], s[0], global_amax=a)))
+    same = nv.add_rms_norm(x.detach(), w.detach(), x.detach())
+    assert all(torch.equal(t.view(torch.uint8), u.view(torch.uint8)) for t, u in zip((codes, scales, hidden, rstd), same))
