@@ -28,12 +28,17 @@ constexpr ScalarType F8 = ScalarType::Float8_e4m3fn, E8 = ScalarType::Float8_e8m
 
 #define REFUSE_IF(cond, ...) TORCH_CHECK_VALUE(!(cond), __VA_ARGS__)
 
-void* stream() {
+// The current stream.  The kernels run on the current device, where another
+// device's memory may not be mapped: `on`, whose device all tensors share, has
+// to be there.
+void* stream(const Tensor& on) {
   PyObject* dev = PyObject_CallNoArgs(g_device);
   if (!dev) throw python_error();
-  PyObject* s = PyObject_CallOneArg(g_stream, dev);
+  const long current = PyLong_AsLong(dev);
+  PyObject* s = current == on.get_device() ? PyObject_CallOneArg(g_stream, dev) : nullptr;
   Py_DECREF(dev);
-  if (!s) throw python_error();
+  if (PyErr_Occurred()) throw python_error();
+  REFUSE_IF(!s, "tensors on the current device, cuda:", current, ", are required: these are on cuda:", on.get_device());
   void* p = PyLong_AsVoidPtr(s);
   Py_DECREF(s);
   if (!p && PyErr_Occurred()) throw python_error();
@@ -156,7 +161,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor c = make(x, {T, H}, F8), s = make(x, {T, groups(H)}, E8), rstd = make(x, {T}, ScalarType::Float);
   const Tensor hidden = res.defined() ? make(x, {T, H}, x.scalar_type()) : Tensor();
   check(nvfp4_add_rms_norm(x.data_ptr(), ptr<void>(res), code(x.scalar_type()), ptr<float>(w), T, H, (float)eps,
-                           ptr<uint8_t>(c), ptr<uint8_t>(s), ptr<void>(hidden), ptr<float>(rstd), stream()),
+                           ptr<uint8_t>(c), ptr<uint8_t>(s), ptr<void>(hidden), ptr<float>(rstd), stream(x)),
         "nvfp4_add_rms_norm");
   return pack(c, s, hidden.defined() ? hidden : x, rstd);
   END_HANDLE_TH_ERRORS
@@ -178,7 +183,7 @@ PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor ws = make(dy, {need < 4 ? 4 : need}, ScalarType::Byte);
   check(nvfp4_add_rms_norm_backward(dy.data_ptr(), hidden.data_ptr(), ptr<void>(dh), code(dy.scalar_type()),
                                     ptr<float>(w), ptr<float>(rstd), T, H, dx.data_ptr(), ptr<float>(dw),
-                                    ws.data_ptr(), (size_t)ws.numel(), stream()),
+                                    ws.data_ptr(), (size_t)ws.numel(), stream(dy)),
         "nvfp4_add_rms_norm_backward");
   return pack(dx, dw);
   END_HANDLE_TH_ERRORS
@@ -195,7 +200,7 @@ PyObject* swiglu_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor c = make(x, {T, F}, F8), s = make(x, {T, groups(F)}, E8);
   const Tensor kept = keep ? make(x, {T, 2 * F}, F8) : Tensor(), ks = keep ? make(x, {T, 2 * groups(F)}, E8) : Tensor();
   check(nvfp4_swiglu(x.data_ptr(), code(x.scalar_type()), T, F, ptr<uint8_t>(c), ptr<uint8_t>(s), ptr<uint8_t>(kept),
-                     ptr<uint8_t>(ks), stream()),
+                     ptr<uint8_t>(ks), stream(x)),
         "nvfp4_swiglu");
   return pack(c, s, kept, ks);
   END_HANDLE_TH_ERRORS
@@ -211,7 +216,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   REFUSE_IF(kept.size(0) != T || kept.size(1) != 2 * F || kept.device() != d.device(), "kept must be [T, 2F] on dout's device");
   const Tensor& ks = scale_bytes(a[2], T, 2 * groups(F), d, "kept_scales");
   const Tensor out = make(d, {T, 2 * F}, d.scalar_type());
-  check(nvfp4_swiglu_backward(d.data_ptr(), code(d.scalar_type()), T, F, bytes(kept), bytes(ks), out.data_ptr(), stream()),
+  check(nvfp4_swiglu_backward(d.data_ptr(), code(d.scalar_type()), T, F, bytes(kept), bytes(ks), out.data_ptr(), stream(d)),
         "nvfp4_swiglu_backward");
   return wrap(out);
   END_HANDLE_TH_ERRORS
@@ -284,7 +289,7 @@ PyObject* matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ScalarType dt = out_type(a[8]);
   const Tensor out = make(x, {x.size(0), w.N}, dt);
   check(nvfp4_matvec(x.data_ptr(), bytes(xs), x.size(0), w.N, x.size(1), bytes(w.packed), bytes(w.scale), blocks,
-                     ptr<float>(w.amax), w.mode, w.bound, out.data_ptr(), code(dt), stream()),
+                     ptr<float>(w.amax), w.mode, w.bound, out.data_ptr(), code(dt), stream(x)),
         "nvfp4_matvec");
   return wrap(out);
   END_HANDLE_TH_ERRORS
@@ -306,7 +311,7 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ScalarType dt = out_type(a[10]);
   const Tensor out = make(x, {x.size(0), w.N}, dt);
   check(nvfp4_grouped_matmul(x.data_ptr(), bytes(xs), x.size(0), E, w.N, x.size(1), ptr<int32_t>(ends), bytes(w.packed),
-                             bytes(w.scale), blocks, ptr<float>(w.amax), w.mode, w.bound, out.data_ptr(), code(dt), stream()),
+                             bytes(w.scale), blocks, ptr<float>(w.amax), w.mode, w.bound, out.data_ptr(), code(dt), stream(x)),
         "nvfp4_grouped_matmul");
   return wrap(out);
   END_HANDLE_TH_ERRORS
@@ -330,7 +335,7 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t need = (int64_t)nvfp4_grouped_wgrad_workspace_bytes(dy.size(0), E, N, K);
   const Tensor ws = need ? make(dy, {need}, ScalarType::Byte) : Tensor();
   check(nvfp4_grouped_wgrad_split(dy.data_ptr(), x.data_ptr(), bytes(xs), dy.size(0), E, N, K, ptr<int32_t>(ends),
-                                  dw.data_ptr(), code(dt), ptr<void>(ws), (size_t)need, stream()),
+                                  dw.data_ptr(), code(dt), ptr<void>(ws), (size_t)need, stream(dy)),
         "nvfp4_grouped_wgrad_split");
   return wrap(dw);
   END_HANDLE_TH_ERRORS

@@ -227,3 +227,38 @@ def test_nothing_is_recorded_for_autograd():
     assert not any(t.requires_grad for t in (codes, scales, hidden, rstd, nv.matvec(x, p[0], s[0], global_amax=a)))
     same = nv.add_rms_norm(x.detach(), w.detach(), x.detach())
     assert all(torch.equal(t.view(torch.uint8), u.view(torch.uint8)) for t, u in zip((codes, scales, hidden, rstd), same))
+
+
+ELSEWHERE = """
+import torch
+torch.zeros(1, device="cuda")
+here = torch._C._cuda_getDevice
+torch._C._cuda_getDevice = lambda: here() + 1  # as if another device were the current one
+import fp4_block_quantization_nvfp4_amd as nv
+x, w = torch.ones(4, 64, device="cuda", dtype=torch.bfloat16), torch.ones(64, device="cuda")
+p, s = torch.zeros(1, 32, 32, dtype=torch.uint8, device="cuda"), torch.zeros(1, 32, 4, dtype=torch.uint8, device="cuda")
+ends, one = torch.tensor([4], dtype=torch.int32, device="cuda"), torch.ones(4, device="cuda")
+kept = torch.zeros(4, 128, dtype=torch.uint8, device="cuda"), torch.zeros(4, 4, dtype=torch.uint8, device="cuda")
+for call in (lambda: nv.add_rms_norm(x, w), lambda: nv.add_rms_norm_backward(x, x, w, one), lambda: nv.swiglu_checkpoint(x),
+             lambda: nv.swiglu_backward(x, *kept), lambda: nv.matvec(x, p[0], s[0]), lambda: nv.grouped_matmul(x, ends, p, s),
+             lambda: nv.grouped_wgrad(x, x, ends)):
+    try:
+        call()
+    except ValueError as e:
+        assert "current device" in str(e), e
+    else:
+        raise SystemExit("not refused")
+print("refused")
+"""
+
+
+def test_tensors_of_another_device_are_refused():
+    """Before anything is launched, on the host: the child takes its device for
+    another one."""
+    import os
+    import subprocess
+    import sys
+
+    res = subprocess.run([sys.executable, "-c", ELSEWHERE], capture_output=True, text=True, timeout=100,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert res.returncode == 0 and "refused" in res.stdout, res.stdout + res.stderr
