@@ -262,3 +262,31 @@ def test_tensors_of_another_device_are_refused():
     res = subprocess.run([sys.executable, "-c", ELSEWHERE], capture_output=True, text=True, timeout=100,
                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert res.returncode == 0 and "refused" in res.stdout, res.stdout + res.stderr
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [2080, 16640])
+@pytest.mark.parametrize("res", [True, False], ids=["residual", "plain"])
+@pytest.mark.parametrize("by", [1.0, 2.0 ** 90, 2.0 ** -100], ids=["one", "large", "small"])
+def test_norm_codes_next_to_borders_are_exact(H, dtype, res, by):
+    """Every y lies within two units of its last place in fp32 from a border
+    between two codes, or between two scales: the side that it is on in 64 bits
+    counts.  |h| is 1, 5 or 7 with mean square 25, so that the root is known."""
+    g = gen(H)
+    pick = torch.rand(H // 2, generator=g) < 0.5
+    size = torch.stack((torch.where(pick, 1.0, 5.0), torch.where(pick, 7.0, 5.0)), 1).view(-1)
+    border = (16 + 2 * torch.randint(0, 7, (H,), generator=g) + 1).double() / 16 * torch.exp2(-torch.randint(0, 9, (H,), generator=g).double())
+    border[::32] = 1.75  # of a group's scale
+    border = border.view(-1, 32)
+    border[:, 1:].clamp_(max=27 / 16)
+    w = (border.view(-1) * 5 / size.double()).float()
+    # a place off on either side too; always where the quotient is exact (|h| = 1 or 5),
+    # since on a border itself the root's last bits in 64 would decide
+    side = torch.randint(0, 2, (H,), generator=g) * 2 - 1
+    w = torch.where((size == 7) & (torch.rand(H, generator=g) < 0.5), w, torch.nextafter(w, w + side))
+    h = size * (torch.randint(0, 2, (6, H), generator=g) * 2 - 1)
+    r = torch.randint(-3, 4, (6, H), generator=g).float() if res else torch.zeros(6, H)
+    x = (h - r) * by
+    codes, scales, _, _ = nv.add_rms_norm(x.to(dtype).cuda(), w.cuda(), (r * by).to(dtype).cuda() if res else None, eps=0.0)
+    c, s = R.mx8_codes(h.double() / 5 * w.double())
+    assert torch.equal(R.byte(scales), s) and torch.equal(R.byte(codes), c)
