@@ -147,7 +147,9 @@ inline LayerLaunch plan_norm(int64_t rows, int64_t H) {
 }
 // Norm's gradient: workgroups, each with one partial row of dw.  About sixteen
 // waves on each of 256 CUs, and two rows a workgroup where there are few: a
-// partial row costs as much to write and read as a row.
+// partial row costs as much to write and read as a row.  Of rows over 16384, whose
+// dw takes 128 KB of shared memory, one workgroup of 9 to 16 waves runs on a CU at a
+// time and the second of the two follows it.
 inline int64_t norm_bwd_groups(int64_t rows, int64_t H) {
   const int64_t waves = norm_threads(H) / 64, cu = waves < 1 ? 8 : 16 / waves < 2 ? 2 : 16 / waves > 8 ? 8 : 16 / waves;
   int64_t g = rows / 2 < 256 ? 256 : rows / 2;
@@ -172,8 +174,8 @@ constexpr int64_t kMatmulMaxK = int64_t(1) << 20;  // a tile's rows stay below 2
 constexpr int64_t kMatmulMaxE = 65534;             // grid y of k_matvec
 // Fragments of 16 n's per workgroup of k_matvec: more of them read x less often,
 // fewer spread a small weight over more CUs.  Four of them beside 16 rows of
-// bf16 in flight do not fit the registers (65536 x 7168, 16 rows: 83 us, with
-// two 63), so they take 8-bit rows or up to four rows an expert, and not where 32
+// bf16 in flight do not fit the registers (65536 x 7168, 16 rows: 83 us, where
+// two took 63, 54 now), so they take 8-bit rows or up to four rows an expert, and not where 32
 // rows are taken at a time.
 inline int matvec_frags(int64_t T, int64_t N, int64_t E, bool mx8) {
   const int64_t tiles = ceil_div(N, 16) * E;

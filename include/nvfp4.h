@@ -303,7 +303,8 @@ typedef enum { NVFP4_BLOCK_1X16 = 0, NVFP4_BLOCK_16X16 = 1, NVFP4_BLOCK_16X16_T 
  * of H elements: y_j = h_j * rstd * weight_j, rstd = 1 / sqrt(mean h^2 + eps),
  * y written as mx8.  hidden receives h rounded to the rows' type, rstd [T]
  * one fp32 a row; y is taken from the unrounded h.  residual and hidden are
- * both given or both NULL (then h = x and nothing is written for it).
+ * both given or both NULL (then h = x and nothing is written for it).  hidden
+ * does not overlap x or residual, which are read again after it is written.
  * weight [H] fp32; H % 16 == 0; eps >= 0.
  */
 nvfp4_status nvfp4_add_rms_norm(const void* x, const void* residual, nvfp4_dtype dt, const float* weight,
