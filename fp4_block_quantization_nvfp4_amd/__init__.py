@@ -15,6 +15,16 @@ from .api import (  # noqa: F401
     quantize_rowcol,
     quantize_4over6,
 )
+from .attention import (  # noqa: F401
+    PagedCache,
+    cache_attention,
+    norm_rope,
+    norm_rope_backward,
+    norm_rope_write,
+    read_cache,
+    rotary_frequencies,
+    write_cache,
+)
 from .layer import (  # noqa: F401
     add_rms_norm,
     add_rms_norm_backward,

@@ -45,10 +45,36 @@ SIGNATURES = {
     "nvfp4_grouped_wgrad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp]),
     "nvfp4_grouped_wgrad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "nvfp4_grouped_wgrad_split": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "nvfp4_norm_rope": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "nvfp4_norm_rope_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_norm_rope_backward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_norm_rope_write": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_write_cache": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp]),
+    "nvfp4_read_cache": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _vp]),
+    "nvfp4_cache_attention_workspace_bytes": (_sz, [_i64, _i64, _vp, _i64, _i64]),
+    "nvfp4_cache_attention": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "nvfp4_selftest_scan": (_i32, [_i32, _u32, _c.c_uint64, _c.c_uint64, _i32, _vp, _vp]),
     "nvfp4_selftest_launch_plan": (_i32, [_i32, _i64, _i64, _i32, _i32, _vp]),
     "nvfp4_selftest_layer_plan": (_i32, [_i32, _i64, _i64, _i64, _i64, _i32, _vp]),
+    "nvfp4_selftest_attention_plan": (_i32, [_i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp]),
 }
+
+
+class Heads(_c.Structure):
+    """nvfp4_heads"""
+    _fields_ = [("at", _vp), ("heads", _i64), ("token", _i64), ("head", _i64)]
+
+
+class Cache(_c.Structure):
+    """nvfp4_cache"""
+    _fields_ = [("k", _vp), ("k_scales", _vp), ("v", _vp), ("v_scales", _vp), ("k_amax", _vp), ("v_amax", _vp),
+                ("pages", _i64), ("page_size", _i64), ("heads", _i64), ("dim", _i64)]
+
+
+class Rope(_c.Structure):
+    """nvfp4_rope"""
+    _fields_ = [("positions", _vp), ("freqs", _vp), ("rotated", _i64), ("interleaved", _i32), ("multiplier", _c.c_double),
+                ("eps", _c.c_double), ("q_weight", _vp), ("k_weight", _vp)]
 
 
 class NVFP4Error(RuntimeError):

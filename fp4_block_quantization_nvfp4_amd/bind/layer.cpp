@@ -1,4 +1,4 @@
-// Torch binding of the layer operators (layer.py): checks the arguments,
+// Torch binding of the layer operators (layer.py, attention.py): checks the arguments,
 // allocates the outputs and calls the C ABI.  Native, since single-token calls
 // are bound by the host: the same steps in Python with ctypes take 12 to 16 us
 // a call, more than their kernels.
@@ -13,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "nvfp4.h"
@@ -341,9 +342,198 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------- attention on an NVFP4 cache
+
+// Rows of heads [T, H, D]: the elements of a row lie side by side, tokens and heads as they like.
+const Tensor& head_rows(PyObject* o, const char* what, nvfp4_heads& h) {
+  const Tensor& x = tensor(o, what);
+  REFUSE_IF(x.dim() != 3, what, ": a 3-D [T, heads, D] tensor is required");
+  REFUSE_IF(!row_dtype(x.scalar_type()), what, ": float32 or bfloat16 input required");
+  REFUSE_IF(x.numel() != 0 && x.stride(2) != 1 && x.size(2) != 1, what, ": the elements of a head must be contiguous");
+  // a stride that is not walked along may be anything
+  h = {x.data_ptr(), x.size(1), x.size(0) > 1 ? x.stride(0) : 0, x.size(1) > 1 ? x.stride(1) : 0};
+  const int64_t unit = x.scalar_type() == ScalarType::Float ? 4 : 8;
+  REFUSE_IF(x.numel() != 0 && (reinterpret_cast<uintptr_t>(h.at) % 16 != 0 || h.token % unit != 0 || h.head % unit != 0), what,
+            ": rows must start at multiples of 16 bytes");
+  return x;
+}
+
+const Tensor& like_rows(PyObject* o, const Tensor& like, int64_t H, const char* what, nvfp4_heads& h) {
+  const Tensor& x = head_rows(o, what, h);
+  REFUSE_IF(x.size(0) != like.size(0) || x.size(2) != like.size(2) || x.scalar_type() != like.scalar_type() || x.device() != like.device() ||
+                (H >= 0 && x.size(1) != H),
+            what, " must be a ", like.scalar_type(), " [", like.size(0), ", ", H >= 0 ? std::to_string(H) : std::string("heads"), ", ", like.size(2),
+            "] tensor on the same device");
+  return x;
+}
+
+// positions, freqs, q_weight, k_weight, interleaved, multiplier, eps
+struct Rope {
+  Tensor positions, freqs, qw, kw;
+  nvfp4_rope r;
+  Rope(PyObject* const* a, const Tensor& q) {
+    const int64_t D = q.size(2);
+    const bool ok = THPVariable_Check(a[1]) && THPVariable_Unpack(a[1]).dim() == 1;
+    REFUSE_IF(!ok, "freqs must be a 1-D float64 tensor");
+    const int64_t half = THPVariable_Unpack(a[1]).size(0);
+    freqs = array(a[1], ScalarType::Double, half, q, "freqs");
+    positions = array(a[0], ScalarType::Int, q.size(0), q, "positions");
+    if (a[2] != Py_None) qw = array(a[2], ScalarType::Float, D, q, "q_weight");
+    if (a[3] != Py_None) kw = array(a[3], ScalarType::Float, D, q, "k_weight");
+    const int inter = truth(a[4]);
+    const double mult = PyFloat_AsDouble(a[5]), eps = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) throw python_error();
+    r = {ptr<int32_t>(positions), ptr<double>(freqs), 2 * half, inter, mult, eps, ptr<float>(qw), ptr<float>(kw)};
+  }
+};
+
+// k, k_scale, v, v_scale, k_amax, v_amax of a cache
+struct Pages {
+  Tensor t[4], ka, va;
+  nvfp4_cache c;
+  explicit Pages(PyObject* const* a) {
+    static const char* const kNames[] = {"cache.k", "cache.k_scale", "cache.v", "cache.v_scale"};
+    for (int i = 0; i < 4; ++i) {
+      const Tensor& x = tensor(a[i], kNames[i]);
+      REFUSE_IF(x.dim() != 4 || x.scalar_type() != ScalarType::Byte || !x.is_contiguous(), kNames[i], " must be a contiguous 4-D uint8 tensor");
+      t[i] = x;
+    }
+    const int64_t P = t[0].size(0), H = t[0].size(1), S = t[0].size(2), half = t[0].size(3);
+    REFUSE_IF(half % 8 != 0 || half == 0, "cache.k must be [pages, heads, page_size, dim / 2] with dim % 16 == 0");
+    for (int i = 1; i < 4; ++i)
+      REFUSE_IF(t[i].device() != t[0].device() || t[i].sizes() != at::IntArrayRef({P, H, S, i == 2 ? half : half / 8}), kNames[i],
+                " must be ", at::IntArrayRef({P, H, S, i == 2 ? half : half / 8}), " on the same device");
+    if (a[4] != Py_None) ka = array(a[4], ScalarType::Float, H, t[0], "k_amax");
+    if (a[5] != Py_None) va = array(a[5], ScalarType::Float, H, t[0], "v_amax");
+    c = {ptr<uint8_t>(t[0]), ptr<uint8_t>(t[1]), ptr<uint8_t>(t[2]), ptr<uint8_t>(t[3]), ptr<float>(ka), ptr<float>(va), P, S, H, 2 * half};
+  }
+};
+
+// (q, k, positions, freqs, q_weight, k_weight, interleaved, multiplier, eps)
+PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 9, "norm_rope");
+  nvfp4_heads hq, hk;
+  const Tensor& q = head_rows(a[0], "q", hq);
+  const Tensor& k = like_rows(a[1], q, -1, "k", hk);
+  const Rope r(a + 2, q);
+  const Tensor qo = make(q, q.sizes(), q.scalar_type()), ko = make(q, k.sizes(), q.scalar_type());
+  check(nvfp4_norm_rope(&hq, &hk, code(q.scalar_type()), q.size(0), q.size(2), &r.r, qo.data_ptr(), ko.data_ptr(), stream(q)),
+        "nvfp4_norm_rope");
+  return pack(qo, ko);
+  END_HANDLE_TH_ERRORS
+}
+
+// (dq, dk, q, k, positions, freqs, q_weight, k_weight, interleaved, multiplier, eps)
+PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 11, "norm_rope_backward");
+  nvfp4_heads hdq, hdk, hq, hk;
+  const Tensor& q = head_rows(a[2], "q", hq);
+  const Tensor& k = like_rows(a[3], q, -1, "k", hk);
+  const Tensor& dq = like_rows(a[0], q, q.size(1), "dq", hdq);
+  const Tensor& dk = like_rows(a[1], q, k.size(1), "dk", hdk);
+  const Rope r(a + 4, q);
+  const int64_t T = q.size(0), D = q.size(2);
+  const Tensor qo = make(q, dq.sizes(), q.scalar_type()), ko = make(q, dk.sizes(), q.scalar_type());
+  const bool weights = r.qw.defined() || r.kw.defined();
+  const int64_t need = weights ? (int64_t)nvfp4_norm_rope_backward_workspace_bytes(T, D) : 0;
+  const Tensor dw = weights ? make(q, {2, D}, ScalarType::Float) : Tensor(), ws = need ? make(q, {need}, ScalarType::Byte) : Tensor();
+  check(nvfp4_norm_rope_backward(&hdq, &hdk, &hq, &hk, code(q.scalar_type()), T, D, &r.r, qo.data_ptr(), ko.data_ptr(),
+                                 ptr<float>(dw), ptr<void>(ws), (size_t)need, stream(q)),
+        "nvfp4_norm_rope_backward");
+  return pack(qo, ko, r.qw.defined() ? dw.select(0, 0) : Tensor(), r.kw.defined() ? dw.select(0, 1) : Tensor());
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, slots, k, k_scale, v, v_scale, k_amax, v_amax of the cache, positions, freqs, q_weight, k_weight,
+// interleaved, multiplier, eps)
+PyObject* norm_rope_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 17, "norm_rope_write");
+  nvfp4_heads hq, hk, hv;
+  const Tensor& q = head_rows(a[0], "q", hq);
+  const Pages c(a + 4);
+  const Tensor& k = like_rows(a[1], q, c.c.heads, "k", hk);
+  like_rows(a[2], k, c.c.heads, "v", hv);
+  REFUSE_IF(q.size(2) != c.c.dim || q.device() != c.t[0].device(), "q, k and v must have the cache's head size, on its device");
+  const Tensor& slots = array(a[3], ScalarType::Int, q.size(0), q, "slots");
+  const Rope r(a + 10, q);
+  const Tensor qo = make(q, q.sizes(), q.scalar_type());
+  check(nvfp4_norm_rope_write(&hq, &hk, &hv, code(q.scalar_type()), q.size(0), &r.r, &c.c, ptr<int32_t>(slots), qo.data_ptr(),
+                              stream(q)),
+        "nvfp4_norm_rope_write");
+  return wrap(qo);
+  END_HANDLE_TH_ERRORS
+}
+
+// (k, v, slots, k, k_scale, v, v_scale, k_amax, v_amax of the cache)
+PyObject* write_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 9, "write_cache");
+  nvfp4_heads hk, hv;
+  const Tensor& k = head_rows(a[0], "k", hk);
+  const Pages c(a + 3);
+  like_rows(a[1], k, c.c.heads, "v", hv);
+  REFUSE_IF(k.size(1) != c.c.heads || k.size(2) != c.c.dim || k.device() != c.t[0].device(),
+            "k and v must have the cache's heads and head size, on its device");
+  const Tensor& slots = array(a[2], ScalarType::Int, k.size(0), k, "slots");
+  check(nvfp4_write_cache(&hk, &hv, code(k.scalar_type()), k.size(0), &c.c, ptr<int32_t>(slots), stream(k)), "nvfp4_write_cache");
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// (slots, k, k_scale, v, v_scale, k_amax, v_amax of the cache, out_dtype)
+PyObject* read_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 8, "read_cache");
+  const Pages c(a + 1);
+  const Tensor& s = tensor(a[0], "slots");
+  const Tensor& slots = array(a[0], ScalarType::Int, s.numel(), c.t[0], "slots");
+  const ScalarType dt = out_type(a[7]);
+  const int64_t T = slots.numel();
+  const Tensor k = make(slots, {T, c.c.heads, c.c.dim}, dt), v = make(slots, {T, c.c.heads, c.c.dim}, dt);
+  check(nvfp4_read_cache(&c.c, ptr<int32_t>(slots), T, k.data_ptr(), v.data_ptr(), code(dt), stream(slots)), "nvfp4_read_cache");
+  return pack(k, v);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, k_scale, v, v_scale, k_amax, v_amax of the cache, table, lens, ends or None, scale or None, causal)
+PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 12, "cache_attention");
+  nvfp4_heads hq;
+  const Tensor& q = head_rows(a[0], "q", hq);
+  REFUSE_IF(q.scalar_type() != ScalarType::BFloat16, "q: bfloat16 is required");
+  const Pages c(a + 1);
+  REFUSE_IF(q.size(2) != c.c.dim || q.device() != c.t[0].device(), "q must have the cache's head size, on its device");
+  REFUSE_IF(q.size(1) % c.c.heads != 0, "q must have a multiple of the cache's heads");
+  const bool ok = THPVariable_Check(a[7]) && THPVariable_Unpack(a[7]).dim() == 2;
+  REFUSE_IF(!ok, "table must be a 2-D int32 tensor");
+  const int64_t B = THPVariable_Unpack(a[7]).size(0), width = THPVariable_Unpack(a[7]).size(1), T = q.size(0);
+  const Tensor& table = array(a[7], ScalarType::Int, B * width, q, "table");
+  const Tensor& lens = array(a[8], ScalarType::Int, B, q, "lens");
+  const Tensor none;
+  const Tensor& ends = a[9] == Py_None ? none : array(a[9], ScalarType::Int, B, q, "ends");
+  REFUSE_IF(!ends.defined() && T != B, "without ends q must have one query for each of the table's ", B, " sequences");
+  double scale = a[10] == Py_None ? 1.0 / std::sqrt((double)c.c.dim) : PyFloat_AsDouble(a[10]);
+  if (PyErr_Occurred()) throw python_error();
+  const bool causal = truth(a[11]);
+  const Tensor out = make(q, q.sizes(), ScalarType::BFloat16), lse = make(q, {T, q.size(1)}, ScalarType::Float);
+  const int64_t need = (int64_t)nvfp4_cache_attention_workspace_bytes(T, q.size(1), &c.c, B, width);
+  const Tensor ws = need ? make(q, {need}, ScalarType::Byte) : Tensor();
+  check(nvfp4_cache_attention(&hq, T, &c.c, ptr<int32_t>(table), B, width, ptr<int32_t>(lens), ptr<int32_t>(ends), (float)scale, causal,
+                              out.data_ptr(), ptr<float>(lse), ptr<void>(ws), (size_t)need, stream(q)),
+        "nvfp4_cache_attention");
+  return pack(out, lse);
+  END_HANDLE_TH_ERRORS
+}
+
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {ENTRY(add_rms_norm), ENTRY(add_rms_norm_backward), ENTRY(swiglu_checkpoint), ENTRY(swiglu_backward),
-                          ENTRY(matvec),       ENTRY(grouped_matmul),        ENTRY(grouped_wgrad),     {nullptr, nullptr, 0, nullptr}};
+                          ENTRY(matvec),       ENTRY(grouped_matmul),        ENTRY(grouped_wgrad),     ENTRY(norm_rope),
+                          ENTRY(norm_rope_backward), ENTRY(norm_rope_write),  ENTRY(write_cache),     ENTRY(read_cache),
+                          ENTRY(cache_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 PyObject* attribute(const char* module, const char* name) {

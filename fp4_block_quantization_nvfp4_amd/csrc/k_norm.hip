@@ -366,8 +366,12 @@ int launch_add_rms_norm_bwd(const void* dy, const void* hidden, const void* dh, 
       norm_bwd<float>((const float*)dy, (const float*)hidden, (const float*)dh, w, rstd, rows, (int)H, (float*)dx,
                       partial, st);
   }
+  return launch_sum_rows(partial, grid, H, dw, stream);
+}
+
+int launch_sum_rows(const float* partial, int n, int64_t H, float* out, void* stream) {
   const LayerLaunch p = plan_sum_rows(H);
-  k_sum_rows<<<(uint32_t)p.grid, p.block, 0, st>>>(partial, grid, (int)H, dw);
+  k_sum_rows<<<(uint32_t)p.grid, p.block, 0, (hipStream_t)stream>>>(partial, n, (int)H, out);
   return (int)hipGetLastError();
 }
 

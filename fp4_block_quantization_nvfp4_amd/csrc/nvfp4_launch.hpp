@@ -95,6 +95,60 @@ struct WgradArgs {
 };
 int launch_wgrad(const WgradArgs& a, void* stream);
 
+// ---- attention on an NVFP4 cache
+
+// Rows of heads: token t, head h at `at` + t * token + h * head (elements).
+struct HeadsView {
+  const void* at;
+  int64_t token, head;
+  int heads;
+};
+
+// Keys and values of `pages` pages of 2^shift slots for each head: codes
+// [pages, heads, 2^shift, dim / 2], scales [pages, heads, 2^shift, dim / 16].
+struct CacheView {
+  uint8_t *k, *ks, *v, *vs;
+  const float *ka, *va;  // amax of each head, or NULL
+  int pages, heads, dim, shift;
+};
+
+// Norm and rotation of a token's rows (k_rope.hip); with slots, keys and values
+// are written to the cache, and k_out is not used.
+struct RopeArgs {
+  HeadsView q, k, v;
+  int T, D, R;             // tokens, head size, rotated elements
+  int in_bf16, interleaved;
+  const int* positions;
+  const double* freqs;
+  double mult, eps;
+  const float *qw, *kw;    // NULL: no norm
+  void *q_out, *k_out;     // [T, heads, D]
+  CacheView c;
+  const int* slots;        // NULL: no cache
+};
+int launch_norm_rope(const RopeArgs& a, void* stream);
+// dq, dk: gradients of the outputs; dw [2, D]: of the two weights (NULL: no norm).
+size_t rope_bwd_workspace_bytes(int64_t T, int64_t D);
+int launch_norm_rope_bwd(const RopeArgs& a, const HeadsView& dq, const HeadsView& dk, float* dw, void* ws, void* stream);
+int launch_read_cache(const CacheView& c, const int* slots, int64_t T, void* k, void* v, int out_bf16, void* stream);
+// n partial rows of H, added in a fixed order (k_norm.hip).
+int launch_sum_rows(const float* partial, int n, int64_t H, float* out, void* stream);
+
+struct AttendArgs {
+  HeadsView q;             // [T, heads, dim] bf16
+  CacheView c;
+  const int* table;        // [B, width] pages
+  const int* lens;         // [B] keys
+  const int* ends;         // [B] cumulative queries, or NULL: one each
+  uint16_t* out;           // [T, heads, dim] bf16
+  float* lse;              // [T, heads]
+  float* part;             // workspace of the split kernel
+  float scale;
+  int T, B, width, causal;
+  int most;                // rows (queries times heads that share keys) of a sequence that the split kernel takes
+};
+int launch_attend(const AttendArgs& a, int which, void* stream);  // which: 1 the split kernel, 2 the tiled one, 3 both
+
 // Test support: exhaustive conversion scans (k_selftest.hip).
 int launch_selftest_scan(int kind, uint32_t param, uint64_t first, uint64_t count, int chunk_log2,
                          uint32_t* records, void* stream);

@@ -264,4 +264,77 @@ inline LayerLaunch plan_wgrad_join(int64_t E, int64_t N, int64_t K) {
   return {PLAN_WGRAD_JOIN, g < 4096 ? g : 4096, E, 256};
 }
 
+// ---- attention on an NVFP4 cache
+
+enum AttentionKernel {
+  PLAN_ROPE = 0,
+  PLAN_ROPE_BWD = 1,
+  PLAN_ROPE_SUM = 2,
+  PLAN_READ_CACHE = 3,
+  PLAN_ATTEND_SPLIT = 4,
+  PLAN_ATTEND_JOIN = 5,
+  PLAN_ATTEND_TILES = 6,
+};
+
+// Norm and rotation: LN lanes to a row, sixteen elements each, 64 / LN rows a
+// wave and pass; `rows` rows of each token.  A wave has one token; few tokens
+// share theirs among several waves.
+constexpr int64_t kRopeMaxD = 512;
+inline int rope_lanes(int64_t D) {
+  int n = 4;
+  while (16 * n < D) n *= 2;
+  return n;
+}
+inline int64_t rope_passes(int64_t rows, int64_t D) { return ceil_div(rows, 64 / rope_lanes(D)); }
+inline int64_t rope_chunks(int64_t T, int64_t rows, int64_t D) {
+  const int64_t p = rope_passes(rows, D), c = T > 0 ? ceil_div(4096, T) : 1;
+  return c < 1 ? 1 : c < p ? c : p;
+}
+inline LayerLaunch plan_rope(int64_t T, int64_t rows, int64_t D) {
+  const int64_t g = ceil_div(T * rope_chunks(T, rows, D), 4);
+  return {PLAN_ROPE, g < kNormMaxGrid ? g : kNormMaxGrid, 1, 256};  // further tokens in a loop
+}
+inline int64_t rope_bwd_groups(int64_t T) {
+  const int64_t g = ceil_div(T, 4);
+  return g < 1024 ? g : 1024;
+}
+inline LayerLaunch plan_rope_bwd(int64_t T) { return {PLAN_ROPE_BWD, rope_bwd_groups(T), 1, 256}; }
+inline LayerLaunch plan_rope_sum(int64_t D) { return {PLAN_ROPE_SUM, 2 * D / 16, 1, 256}; }
+inline LayerLaunch plan_read_cache(int64_t T, int64_t heads, int64_t D) {
+  return {PLAN_READ_CACHE, ceil_div(T * heads * (D / 16), 256), 2, 256};
+}
+
+// Attention.  Rows: queries times the heads that share keys.  The split kernel takes sequences of up
+// to kAttendFew rows, and all where no sequence can have more; the tiled one the others.
+constexpr int kAttendFew = 32;
+constexpr int64_t kAttendPieces = 1024;  // workgroups of the split kernel at most
+constexpr int kAttendTile = 128;         // keys of a tile of its work
+constexpr int kAttendRows = 128;         // rows of a unit of the tiled kernel
+
+inline int attend_kernels(int64_t T, int64_t Hq, int64_t Hk, bool ends) { return ends && T * (Hq / Hk) > kAttendFew ? 3 : 1; }
+// Tiles of the split kernel at most: with units of sixteen rows, of keys that the table's rows name.
+inline int64_t attend_split_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
+  const int64_t G = Hq / Hk, few = ceil_div(G > kAttendFew ? G : kAttendFew, 16);
+  const int64_t units = B * few * Hk;
+  return units * (keys > 0 ? ceil_div(keys, kAttendTile) : 1) + ceil_div(T * G, 16) * Hk;
+}
+inline int64_t attend_pieces(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
+  const int64_t n = attend_split_tiles(T, B, Hq, Hk, keys);
+  return n < kAttendPieces ? n : kAttendPieces;
+}
+inline LayerLaunch plan_attend_split(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
+  return {PLAN_ATTEND_SPLIT, attend_pieces(T, B, Hq, Hk, keys), 1, 256};
+}
+inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
+  if (keys <= kAttendTile) return {0, 0, 0, 0};  // no unit has two tiles
+  return {PLAN_ATTEND_JOIN, attend_pieces(T, B, Hq, Hk, keys), 4, 256};
+}
+inline size_t attend_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  return keys <= kAttendTile ? 0 : (size_t)(attend_pieces(T, B, Hq, Hk, keys) * 2 * (16 * D + 32) * 4);
+}
+// Units of the tiled kernel at most: each sequence adds less than one to T * G / rows.
+inline LayerLaunch plan_attend_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk) {
+  return {PLAN_ATTEND_TILES, (ceil_div(T * (Hq / Hk), kAttendRows) + B) * Hk, 1, 256};
+}
+
 }  // namespace nvfp4

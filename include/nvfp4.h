@@ -385,6 +385,119 @@ nvfp4_status nvfp4_grouped_wgrad_split(const void* dy, const void* x, const uint
                                        int64_t N, int64_t K, const int32_t* ends, void* dw, nvfp4_dtype out_dt,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention whose keys and values are stored in NVFP4
+ *
+ * Queries, keys and values of T tokens are rows of D elements: token t, head h
+ * at `at` + t * token + h * head elements (nvfp4_heads), so that views of one
+ * projection are taken as they are.  Rows are 16-byte aligned: `at` is, and the
+ * strides are multiples of 16 bytes.  Outputs are dense [T, heads, D].
+ *
+ * A cache holds `pages` pages of `page_size` slots (a power of two, 16 to 65536)
+ * for each of `heads` heads: codes [pages, heads, page_size, dim / 2] and scales
+ * [pages, heads, page_size, dim / 16] of keys and of values.  A slot's row is
+ * what nvfp4_quantize writes for it (round to nearest), with the second-level
+ * scale amax[h] / 2688 of its head, or none (k_amax, v_amax NULL).  Slot numbers
+ * are page * page_size + the place in the page.  dim % 16 == 0, up to 512; for
+ * attention dim % 32 == 0, up to 256.  Codes are 16-byte aligned, scales 2-byte,
+ * the other arrays 4-byte (freqs 8-byte, weights 16-byte).
+ *
+ * Sizes: T < 2^31, at most 65536 heads, T * heads * D <= 2^33, pages * page_size
+ * < 2^31 (NVFP4_E_RANGE).  Rows whose sums or scores are not finite give NaN as
+ * the formulas do.
+ */
+typedef struct {
+  const void* at;
+  int64_t heads, token, head; /* strides in elements */
+} nvfp4_heads;
+
+typedef struct {
+  uint8_t *k, *k_scales, *v, *v_scales;
+  const float *k_amax, *v_amax; /* [heads] or NULL */
+  int64_t pages, page_size, heads, dim;
+} nvfp4_cache;
+
+/*
+ * Norm and rotation of a row x [D] at a position: y = x * rstd * weight, rstd =
+ * 1 / sqrt(mean x^2 + eps) (weight NULL: y = x); then the pairs (y_i, y_(i +
+ * rotated / 2)), or (y_2i, y_(2i + 1)) where they are interleaved, are turned by
+ * position * freqs[i], a product in 64 bits, and taken times multiplier:
+ * a' = a c - b s, b' = b c + a s.  Elements from `rotated` on are not turned.
+ * rotated % 16 == 0, 0 <= rotated <= D; eps >= 0.
+ */
+typedef struct {
+  const int32_t* positions; /* [T]; not read where rotated == 0 */
+  const double* freqs;      /* [rotated / 2] */
+  int64_t rotated;
+  int interleaved;
+  double multiplier, eps;
+  const float *q_weight, *k_weight; /* [D] or NULL */
+} nvfp4_rope;
+
+/* nvfp4_norm_rope - queries and keys of T tokens, computed in 64 bits and rounded to fp32, and from there to bf16. */
+nvfp4_status nvfp4_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, nvfp4_dtype dt, int64_t T, int64_t D,
+                             const nvfp4_rope* rope, void* q_out, void* k_out, void* stream);
+
+/*
+ * nvfp4_norm_rope_backward - gradient of the above from the gradients dq_out and
+ * dk_out of its outputs and from its inputs (not read for a side without a
+ * weight): dq, dk dense, in the rows' type; dweights [2, D] fp32, of q_weight and
+ * of k_weight (zeros for one that is NULL; not written where both are).
+ * workspace: nvfp4_norm_rope_backward_workspace_bytes(T, D), 16-byte aligned;
+ * needed with a weight alone.
+ */
+size_t nvfp4_norm_rope_backward_workspace_bytes(int64_t T, int64_t D);
+nvfp4_status nvfp4_norm_rope_backward(const nvfp4_heads* dq_out, const nvfp4_heads* dk_out, const nvfp4_heads* q,
+                                      const nvfp4_heads* k, nvfp4_dtype dt, int64_t T, int64_t D,
+                                      const nvfp4_rope* rope, void* dq, void* dk, float* dweights, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_norm_rope_write - nvfp4_norm_rope whose keys, rounded to dt, go to the
+ * cache with the values v, token t to slots[t]; only q_out is written besides.  A
+ * slot that is negative or past the cache is skipped.  Slots differ from each
+ * other: one that is named twice holds parts of either row.
+ */
+nvfp4_status nvfp4_norm_rope_write(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v, nvfp4_dtype dt,
+                                   int64_t T, const nvfp4_rope* rope, const nvfp4_cache* cache, const int32_t* slots,
+                                   void* q_out, void* stream);
+
+/* nvfp4_write_cache - keys and values of T tokens to slots[t], as above. */
+nvfp4_status nvfp4_write_cache(const nvfp4_heads* k, const nvfp4_heads* v, nvfp4_dtype dt, int64_t T,
+                               const nvfp4_cache* cache, const int32_t* slots, void* stream);
+
+/* nvfp4_read_cache - keys and values [T, heads, dim] of slots[t], as nvfp4_dequantize; zeros for a slot that is
+ * negative or past the cache. */
+nvfp4_status nvfp4_read_cache(const nvfp4_cache* cache, const int32_t* slots, int64_t T, void* k, void* v,
+                              nvfp4_dtype out_dt, void* stream);
+
+/*
+ * nvfp4_cache_attention - queries of B sequences over their keys in the cache.
+ * Sequence b has the queries from ends[b - 1] (0 for the first) up to ends[b]
+ * (ends NULL: T == B and query b alone, or B == 0) and lens[b] keys, key j in page
+ * table[b * width + j / page_size].  Query i of n sees the keys j <= lens[b] - n +
+ * i (causal: the sequence's last queries and keys are the same tokens), or all.
+ * q->heads is a multiple of the cache's: head h reads keys of head h / (q->heads /
+ * heads).  out [T, q->heads, dim] bf16 = sum of p_j v_j, p = softmax(scale q .
+ * k_j), and lse [T, q->heads] fp32 = log of the sum of exp(scale q . k_j); a query
+ * without keys, or past the last end, gets 0 and -infinity.
+ *
+ * q is bf16.  ends are clamped to [0, T] and to the ones before them, lens to at
+ * least 0.  A query that sees a key whose page is not in the cache, and every one
+ * of a sequence longer than width * page_size, gets NaN.  width >= 1, scale >
+ * 0.  Sums have a fixed order.  Further limits (NVFP4_E_RANGE): B <= 2^20, B * heads
+ * <= 2^22, width * page_size <= 2^30, and B * max(2, ceil(G / 16)) * heads *
+ * ceil(width * page_size / 128) + ceil(T * G / 16) * heads < 2^31, G = q->heads /
+ * heads.  workspace: at least
+ * nvfp4_cache_attention_workspace_bytes (0: may be NULL), 16-byte aligned.
+ */
+size_t nvfp4_cache_attention_workspace_bytes(int64_t T, int64_t q_heads, const nvfp4_cache* cache, int64_t B,
+                                             int64_t width);
+nvfp4_status nvfp4_cache_attention(const nvfp4_heads* q, int64_t T, const nvfp4_cache* cache, const int32_t* table,
+                                   int64_t B, int64_t width, const int32_t* lens, const int32_t* ends, float scale,
+                                   int causal, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /*
  * Test support (not part of the quantization path).
  *
@@ -444,6 +557,17 @@ nvfp4_status nvfp4_selftest_launch_plan(int entry, int64_t M, int64_t K, int in_
  */
 nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t N, int64_t K, int mx8,
                                        int64_t* plan);
+
+/*
+ * nvfp4_selftest_attention_plan - the same for the operators on a cache.
+ *   entry    0 norm_rope, 1 its backward, 2 norm_rope_write, 3 write_cache, 4
+ *            read_cache, 5 cache_attention with ends, 6 without.  Hq, Hk: heads of
+ *            queries and of keys; keys: width * page_size.
+ *   plan     HOST pointer to twelve int64: {kernel id, workgroups along x, along
+ *            y, lanes per workgroup} of up to three launches (zeros: none).
+ */
+nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
+                                           int64_t keys, int64_t* plan);
 
 #ifdef __cplusplus
 }
