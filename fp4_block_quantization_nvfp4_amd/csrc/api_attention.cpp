@@ -266,8 +266,8 @@ nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int
     if (entry == 4) p[0] = nvfp4::plan_read_cache(T, Hk, D);
     if (entry >= 5) {
       if (nvfp4::attend_split_tiles(T, B, Hq, Hk, keys) >= int64_t(1) << 31) return NVFP4_E_RANGE;
-      p[0] = nvfp4::plan_attend_split(T, B, Hq, Hk, keys);
-      p[1] = nvfp4::plan_attend_join(T, B, Hq, Hk, keys);
+      p[0] = nvfp4::plan_attend_split(T, B, Hq, Hk, D, keys);
+      p[1] = nvfp4::plan_attend_join(T, B, Hq, Hk, D, keys);
       if (nvfp4::attend_kernels(T, Hq, Hk, entry == 5) & 2) p[2] = nvfp4::plan_attend_tiles(T, B, Hq, Hk);
     }
   }

@@ -5,17 +5,16 @@
 //
 // Bound by reading the cache, 9/16 byte an element.  The queries of a sequence
 // and of the heads that share keys form rows, sixteen to a unit; a unit's keys
-// are tiles of 128.  All tiles of all units are one line, cut into as many even
-// pieces as there are workgroups, whatever the sequences' lengths: a long one is
-// shared by many, short ones are taken several by one.  A unit that lies in
-// several pieces leaves its parts (sums, maxima) in the workspace, and a second
-// launch joins them in order.
+// are tiles of 64.  All tiles of all units are one line, cut into even pieces, one
+// a wave, whatever the sequences' lengths: a long one is shared by many waves,
+// short ones are taken several by one.  A unit that lies in several pieces leaves
+// its parts (sums, maxima) in the workspace, and a second launch joins them in
+// order.
 //
-// Of a tile a wave takes 32 keys: keys times queries (transposed, a lane has one
+// A wave takes 32 keys at a time: keys times queries (transposed, a lane has one
 // query's scores), the running maximum and sum of the softmax, weights back into
-// the matrix cores as they lie, with values read across from shared memory
-// (turned by the load).  The four waves keep sums of their own and join at the
-// piece's end.
+// the matrix cores as they lie, with values read across from the wave's own shared
+// memory (turned by the load).  Waves never wait for each other.
 #include "nvfp4_attend.hpp"
 
 namespace nvfp4 {
@@ -28,11 +27,43 @@ struct SplitCount {
   NV_DEV int operator()(bool real, int n, int L) const { return real && (int64_t)n * G > most ? 0 : units(n) * tiles(L); }
 };
 
-// Piece i of `total` tiles among `pieces`.
-NV_DEV int piece_start(int total, int pieces, int i) { return (int)((int64_t)total * i / pieces); }
+NV_DEV int min_of(int64_t a, int b) { return a < b ? (int)a : b; }
+
+// What the join needs of a unit whose first part is this piece's; parts 0: no unit.
+// The parts: `head` pieces from here on, then one of each of `middle` workgroups,
+// then the others from the first piece of workgroup w1 on.  (The join scanned the
+// sequences itself before: 10 to 27 us.)
+struct JoinHeader {
+  int parts, head, middle, w1, unit, q0, n, shared;
+};
+
+// The pieces: the waves take as many tiles each, and a unit lies in at most
+// kMostParts pieces (the join takes them one after the other).
+constexpr int kMostParts = 512;
+struct Pieces {
+  int total, per;
+  NV_DEV Pieces(const SplitCount& count, int total_, int longest, int pieces) : total(total_) {
+    const int even = (total + pieces - 1) / pieces, most = (count.tiles(longest) + kMostParts - 1) / kMostParts;
+    per = even > most ? even : most;
+  }
+  NV_DEV int start(int piece) const { return min_of((int64_t)per * piece, total); }
+  // Whether the four pieces of workgroup w lie in the unit of tiles begin .. end - 1.
+  NV_DEV bool shared(int w, int begin, int end) const { return start(4 * w) >= begin && start(4 * w + 4) <= end; }
+  // Of a unit up to tile `end` whose first part is this piece of workgroup w0, which has
+  // up to `most` parts of it.
+  NV_DEV JoinHeader header(int w0, int piece, int most, int end, int unit, const Sequence& q, bool one) const {
+    const int last = (end - 1) / per, w1 = last / 4;  // the piece that has the unit's last tile
+    const int head = most < last - piece + 1 ? most : last - piece + 1, middle = w1 == w0 ? 0 : w1 - w0 - 1;
+    const int tail = w1 == w0 ? 0 : start(4 * w1 + 4) <= end ? 1 : last - 4 * w1 + 1;
+    return {head + middle + tail, head, middle, w1, unit, q.q0, q.n, one ? 1 : 0};
+  }
+};
 
 // A partial result: sixteen rows of D sums, then their maxima, then their sums of weights.
 NV_DEV int64_t part_size(int D) { return 16 * (int64_t)D + 32; }
+// The workspace: two partial results for each piece (of a unit that began before it,
+// and of one that it begins), then the headers.
+NV_DEV JoinHeader* headers(const AttendArgs& a, int D, int pieces) { return reinterpret_cast<JoinHeader*>(a.part + 2 * (int64_t)pieces * part_size(D)); }
 
 // Sixteen rows of unit `unit` of sequence s: row r is query r / G, head r % G of the unit's shared head.
 struct UnitRow {
@@ -43,15 +74,15 @@ NV_DEV UnitRow unit_row(const Sequence& s, int G, int Hk, int unit, int r) {
   return {i < s.n ? s.q0 + i : -1, h * G + m - i * G};
 }
 
+// Four elements of a row, from its sums o, maximum and sum of weights.
 NV_DEV void write_row(const AttendArgs& a, const UnitRow& u, int d, nv_f4 o, float m, float l, float vdec) {
-  if (u.token < 0 || d >= a.c.dim) return;
   const float inv = l == 0.0f ? 0.0f : vdec / l;
   const int64_t row = (int64_t)u.token * a.q.heads + u.head;
   nv_u2 w;
   w.x = pack_bf16(o[0] * inv, o[1] * inv);
   w.y = pack_bf16(o[2] * inv, o[3] * inv);
   *reinterpret_cast<nv_u2*>(a.out + row * a.c.dim + d) = w;
-  if (d == 0) a.lse[row] = l == 0.0f ? -INFINITY : (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l)));
+  if (d == 0) a.lse[row] = l == 0.0f ? -INFINITY : log_sum(m, l);
 }
 
 template <int DP>
@@ -59,37 +90,50 @@ struct SplitShape {
   static constexpr int NS = DP / 32, NT = DP / 16;        // steps of 32 along d; tiles of 16 of it
   static constexpr int RUN = DP / 4;                      // elements of a key that a lane loads
   static constexpr int ROW = DP + 4;                      // floats of a row of sums in shared memory
-  static constexpr int WAVE = 16 * ROW * 4 > 32 * DP * 2 ? 16 * ROW * 4 : 32 * DP * 2;
+  static constexpr int WAVE = 16 * ROW * 4;               // holds 32 keys' values too
+  static_assert(32 * DP * 2 <= WAVE, "values, or sums");
 };
 
-// Raw keys or values of 16 slots: a lane has RUN elements of key lane % 16.
+// Where a head's keys and values of one page lie, and a lane's offsets into a
+// group of 16 slots of it: a lane has DP / 4 elements of key lane % 16.
+template <int DP>
+struct PageView {
+  static constexpr int PIECES = DP == 256 ? 2 : 1;
+  const uint8_t *k, *ks, *v, *vs;  // of the head, page 0
+  int64_t page;                    // bytes of a page's codes
+  uint32_t row, co[PIECES], so[PIECES];
+  NV_DEV PageView(const CacheView& c, int h, int lane) : page(((int64_t)c.heads << c.shift) * (c.dim / 2)), row((uint32_t)(c.dim / 2)) {
+    const int64_t at = ((int64_t)h << c.shift) * (c.dim / 2);
+    k = c.k + at, v = c.v + at, ks = c.ks + at / 8, vs = c.vs + at / 8;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const uint32_t d = (uint32_t)(lane >> 4) * (DP / 4) + 32 * i;
+      co[i] = d < (uint32_t)c.dim ? (uint32_t)(lane & 15) * row + d / 2 : kOutside;
+      so[i] = d < (uint32_t)c.dim ? (uint32_t)(lane & 15) * (row / 8) + d / 16 : kOutside;
+    }
+  }
+};
+
+// Raw keys or values of 16 slots.
 template <int DP>
 struct RawKeys {
-  static constexpr int NS = DP / 32;
-  uint32_t w[NS];
-  uint32_t s[DP == 256 ? 2 : 1];
-  NV_DEV void load(const uint8_t* codes, const uint8_t* scales, const AttendArgs& a, int page, int h, int at, int rows, int lane) {
-    const int D = a.c.dim, grp = lane >> 4;
-    const int64_t row0 = ((int64_t)page * a.c.heads + h) << a.c.shift;
-    const nv_buf cb = make_buf(codes + row0 * (D / 2), (uint32_t)rows * (uint32_t)(D / 2));
-    const nv_buf sb = make_buf(scales + row0 * (D / 16), (uint32_t)rows * (uint32_t)(D / 16));
-    const uint32_t r = (uint32_t)(at + (lane & 15));
-    const uint32_t co = r * (uint32_t)(D / 2), so = r * (uint32_t)(D / 16);
-    if constexpr (DP == 64) {
-      const bool in = 16 * grp < D;
-      const nv_u2 v = buf8(cb, in ? co + 8 * grp : kOutside);
-      w[0] = v.x;
-      w[1] = v.y;
-      s[0] = buf1(sb, in ? so + grp : kOutside);
-    } else {
+  static constexpr int NS = DP / 32, PIECES = PageView<DP>::PIECES;
+  uint32_t w[NS], s[PIECES];
+  // codes, scales: of the page, up to the last slot that may be read; at: the first
+  // slot's offset into the codes, not past their end (a scalar)
+  NV_DEV void load(const PageView<DP>& p, nv_buf codes, nv_buf scales, uint32_t at) {
 #pragma unroll
-      for (int i = 0; i < NS / 4; ++i) {
-        const int d = 8 * NS * grp + 32 * i;
-        const bool in = d < D;
-        const nv_u4 v = buf16(cb, in ? co + d / 2 : kOutside);
+    for (int i = 0; i < PIECES; ++i) {
+      if constexpr (DP == 64) {
+        const nv_u2 x = __builtin_amdgcn_raw_buffer_load_b64(codes.at, (int)p.co[i], (int)at, 0);
+        w[0] = x.x;
+        w[1] = x.y;
+        s[i] = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales.at, (int)p.so[i], (int)(at >> 3), 0);
+      } else {
+        const nv_u4 x = __builtin_amdgcn_raw_buffer_load_b128(codes.at, (int)p.co[i], (int)at, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-        s[i] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb.at, (int)(in ? so + d / 16 : kOutside), 0, 0);
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
+        s[i] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales.at, (int)p.so[i], (int)(at >> 3), 0);
       }
     }
   }
@@ -101,38 +145,74 @@ struct RawKeys {
 };
 
 template <int DP>
-__global__ __launch_bounds__(256) void k_attend_split(const AttendArgs a) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const AttendArgs a) {
   using S = SplitShape<DP>;
   constexpr int NS = S::NS, NT = S::NT;
-  __shared__ __align__(16) uint8_t lds[4][S::WAVE];
+  __shared__ __align__(16) uint8_t lds[4][S::WAVE];  // values of 32 keys, or sums
   __shared__ float stat[2][4][16];
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
   const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
-  const SplitCount count{G, Hk, a.most, 128};
+  const SplitCount count{G, Hk, a.most, kAttendTile};
   SequenceScan<SplitCount> scan(a, count);
   const int total = scan.total();
-  int tile = piece_start(total, gridDim.x, blockIdx.x);
-  const int stop = piece_start(total, gridDim.x, blockIdx.x + 1);
-  if (tile >= stop) return;
-  scan.restart();
+  const Pieces cut(count, total, scan.longest, 4 * gridDim.x);
+  const int piece = 4 * blockIdx.x + wv, first = cut.start(4 * blockIdx.x);
+  int tile = cut.start(piece);
+  const int stop = cut.start(piece + 1);
+  JoinHeader* join = a.part ? headers(a, D, 4 * gridDim.x) + piece : nullptr;
+  if (join && lane == 0) *join = JoinHeader{};
+  bool shared = false;
   Sequence q{};
-  while (tile < stop) {
-    if (!scan.find(tile, q)) break;
-    const int kt = count.tiles(q.L), u = (tile - q.first) / kt, j0 = tile - q.first - u * kt;
-    const int j1 = j0 + (stop - tile) < kt ? j0 + (stop - tile) : kt;
+  if (first < total) {
+    scan.restart();
+    if (scan.find(first, q)) {
+      const int kt = count.tiles(q.L), begin = first - (first - q.first) % kt;
+      shared = cut.shared(blockIdx.x, begin, begin + kt);
+    }
+  }
+  while (tile < stop || shared) {
+    if (tile < stop && !scan.find(tile, q)) break;
+    const int at = tile < stop ? tile : first;  // a wave without a tile joins in all the same
+    const int kt = count.tiles(q.L), u = (at - q.first) / kt, j0 = at - q.first - u * kt;
+    const int j1 = tile < stop ? (j0 + (stop - tile) < kt ? j0 + (stop - tile) : kt) : j0;
     const int h = u % Hk;
     const UnitRow mine = unit_row(q, G, Hk, u, col);
+    const int keys = uniform(j1 * kAttendTile < q.L ? j1 * kAttendTile : q.L);  // end of the piece
+    PageWindow pages(a, q, j0 * kAttendTile < keys ? j0 * kAttendTile : 0);
     // a lane's query: RUN elements of row `col`
     nv_u4 raw[NS];
-    uint32_t big = 0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int d = S::RUN * grp + 8 * i;
       raw[i] = (nv_u4){0, 0, 0, 0};
       if (mine.token >= 0 && d < D)
         raw[i] = *reinterpret_cast<const nv_u4*>((const uint16_t*)a.q.at + mine.token * a.q.token + mine.head * a.q.head + d);
-      big = amax_bits(raw[i], big);
     }
+    const PageView<DP> view(a.c, h, lane);
+    // without branches, so that what is in flight is not waited for; outside the piece nothing is read
+    auto load = [&](RawKeys<DP>(&K)[2], RawKeys<DP>(&V)[2], int key0) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int k = key0 + 16 * g, left = keys - k;
+        const int p = left > 0 ? pages(k) : -1;
+        const int at = k & ((1 << a.c.shift) - 1), rows = p < 0 ? 0 : at + (left < 16 ? left : 16);
+        const int64_t off = p < 0 ? 0 : p * view.page;
+        const uint32_t bytes = (uint32_t)rows * view.row, first = (uint32_t)at * view.row;
+        const uint32_t base = (uint32_t)uniform((int)(first < bytes ? first : bytes));
+        K[g].load(view, make_buf(view.k + off, bytes), make_buf(view.ks + off / 8, bytes / 8), base);
+        V[g].load(view, make_buf(view.v + off, bytes), make_buf(view.vs + off / 8, bytes / 8), base);
+        if (left > 0 && p < 0) {
+#pragma unroll
+          for (int i = 0; i < RawKeys<DP>::PIECES; ++i) K[g].s[i] = kNanScales;
+        }
+      }
+    };
+    RawKeys<DP> K0[2], V0[2], K1[2], V1[2];
+    int key0 = uniform(j0 * kAttendTile);
+    load(K0, V0, key0);
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) big = amax_bits(raw[i], big);
     {
       const uint32_t o = (uint32_t)__shfl_xor((int)big, 16, 64);
       big = o > big ? o : big;
@@ -144,29 +224,15 @@ __global__ __launch_bounds__(256) void k_attend_split(const AttendArgs a) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) Q[i] = query_to_f16(raw[i], factor);
     const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
-    const float by = a.scale * kLog2e / factor * kdec;
+    const float by = score_scale(a.scale * kLog2e / factor * kdec);
     const int limit = mine.token < 0 ? 0 : seen_by(a, q, mine.token - q.q0);
+    const int least = seen_by(a, q, u / Hk * 16 / G);  // what all rows of the unit see
     nv_f4 O[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) O[i] = (nv_f4){0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
     uint8_t* vs = lds[wv];
-    for (int j = j0; j < j1; ++j) {
-      const int key0 = j * 128 + wv * 32;
-      if (key0 >= q.L) break;
-      RawKeys<DP> K[2], V[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int k = key0 + 16 * g, left = q.L - k;
-        const int p = left > 0 ? page_of(a, q, k) : 0;
-        const int at = k & ((1 << a.c.shift) - 1), rows = p < 0 || left <= 0 ? 0 : at + (left < 16 ? left : 16);
-        K[g].load(a.c.k, a.c.ks, a, p < 0 ? 0 : p, h, at, rows, lane);
-        V[g].load(a.c.v, a.c.vs, a, p < 0 ? 0 : p, h, at, rows, lane);
-        if (p < 0) {
-#pragma unroll
-          for (int i = 0; i < (DP == 256 ? 2 : 1); ++i) K[g].s[i] = kNanScales;
-        }
-      }
+    auto step = [&](const RawKeys<DP>(&K)[2], const RawKeys<DP>(&V)[2], int key0) {
       nv_f4 Sc[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -174,34 +240,6 @@ __global__ __launch_bounds__(256) void k_attend_split(const AttendArgs a) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) Sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(K[g].values(i), Q[i], Sc[g], 0, 0, 0);
       }
-      float top = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = key0 + 16 * g + 4 * grp + r;
-          const float s = key < limit ? Sc[g][r] * by : -INFINITY;
-          Sc[g][r] = s;
-          top = fmaxf(top, s);
-        }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-      const float alpha = exp2_fast(m - base);
-      m = mn;
-      l *= alpha;
-      float w[8];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          w[4 * g + r] = exp2_fast(Sc[g][r] - base + kWeightBits);
-          l += w[4 * g + r];
-        }
-      nv_u4 pw;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pw[i] = pack_f16(w[2 * i], w[2 * i + 1]);
-      const nv_h8 P = __builtin_bit_cast(nv_h8, pw);
       // values to shared memory, key by key; eight elements c of a key at c ^ key
 #pragma unroll
       for (int g = 0; g < 2; ++g)
@@ -210,6 +248,37 @@ __global__ __launch_bounds__(256) void k_attend_split(const AttendArgs a) {
           const int key = 16 * g + col, c = NS * grp + i;
           *reinterpret_cast<nv_h8*>(vs + key * DP * 2 + ((c ^ (key & 7)) << 4)) = V[g].values(i);
         }
+      if (key0 + 32 > least) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (key0 + 16 * g + 4 * grp + r >= limit) Sc[g][r] = -INFINITY;
+      }
+      const float top = quarter_max(fmaxf(fmaxf(fmaxf(Sc[0][0], Sc[0][1]), fmaxf(Sc[0][2], Sc[0][3])),
+                                          fmaxf(fmaxf(Sc[1][0], Sc[1][1]), fmaxf(Sc[1][2], Sc[1][3])))) * by;
+      if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+        const float mn = fmaxf(m, top), alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) O[i][r] *= alpha;
+      }
+      const float up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+      float w[8];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          w[4 * g + r] = exp2_fast(__builtin_fmaf(Sc[g][r], by, up));
+          l += w[4 * g + r];
+        }
+      nv_u4 pw;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pw[i] = pack_f16(w[2 * i], w[2 * i + 1]);
+      const nv_h8 P = __builtin_bit_cast(nv_h8, pw);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -217,97 +286,170 @@ __global__ __launch_bounds__(256) void k_attend_split(const AttendArgs a) {
         nv_h4 part[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          // lane 4 x + y of a group of sixteen names a quarter of key 4 grp + x, and gets element (its number) of all four
           const int key = 16 * g + 4 * grp + (col >> 2), c = 2 * i + ((col & 3) >> 1);
-          typedef __attribute__((address_space(3))) short lds_s;
-          typedef short s4 __attribute__((ext_vector_type(4)));
-          typedef __attribute__((address_space(3))) s4 lds_s4;
-          const uint32_t off = (uint32_t)(uintptr_t)(lds_s*)(vs + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (col & 1));
-          part[g] = __builtin_bit_cast(nv_h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(uintptr_t)off));
+          part[g] = read_turned(vs + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (col & 1));
         }
         const nv_h8 A = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        nv_f4 o = O[i];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] *= alpha;
-        O[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A, P, o, 0, 0, 0);
+        O[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A, P, O[i], 0, 0, 0);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
+    };
+    // the next 32 keys are on their way while these are used
+    for (; key0 < keys; key0 += 64) {
+      load(K1, V1, key0 + 32);
+      step(K0, V0, key0);
+      load(K0, V0, key0 + 64);
+      if (key0 + 32 < keys) step(K1, V1, key0 + 32);
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    // the four waves' sums are joined
-    float* mysum = reinterpret_cast<float*>(lds[wv]);
+    l = quarter_sum(l);
+    if (shared) {
+      float* mysum = reinterpret_cast<float*>(lds[wv]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<nv_f4*>(mysum + col * S::ROW + 16 * i + 4 * grp) = O[i];
-    if (grp == 0) {
-      stat[0][wv][col] = m;
-      stat[1][wv][col] = l;
-    }
-    __syncthreads();
-    const bool whole = j0 == 0 && j1 == kt;
-    float* part = a.part + (2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0)) * part_size(D);
-    for (int e = threadIdx.x; e < 16 * (DP / 4); e += 256) {
-      const int r = e / (DP / 4), d = e % (DP / 4) * 4;
-      float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
-      nv_f4 o = (nv_f4){0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = exp2_fast(stat[0][w][r] - (mm == -INFINITY ? 0.0f : mm));
-        ll = __builtin_fmaf(stat[1][w][r], f, ll);
-        const nv_f4 x = *reinterpret_cast<const nv_f4*>(reinterpret_cast<const float*>(lds[w]) + r * S::ROW + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<nv_f4*>(mysum + col * S::ROW + 16 * i + 4 * grp) = O[i];
+      if (grp == 0) {
+        stat[0][wv][col] = m;
+        stat[1][wv][col] = l;
       }
-      if (whole) {
-        write_row(a, unit_row(q, G, Hk, u, r), d, o, mm, ll, vdec);
-      } else if (d < D) {
-        *reinterpret_cast<nv_f4*>(part + r * D + d) = o;
-        if (d == 0) {
-          part[16 * D + r] = mm;
-          part[16 * D + 16 + r] = ll;
+      __syncthreads();
+      const int begin = first - (first - q.first) % kt;
+      const bool whole = first == begin && cut.start(4 * blockIdx.x + 4) == begin + kt;
+      if (threadIdx.x == 0 && first == begin && !whole) *join = cut.header(blockIdx.x, 4 * blockIdx.x, 1, begin + kt, u, q, true);
+      float* part = a.part + (8 * (int64_t)blockIdx.x + (first == begin ? 1 : 0)) * part_size(D);
+      for (int e = threadIdx.x; e < 16 * (DP / 4); e += 256) {
+        const int r = e / (DP / 4), d = e % (DP / 4) * 4;
+        const UnitRow row = unit_row(q, G, Hk, u, r);
+        if (row.token < 0 || d >= D) continue;
+        float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
+        nv_f4 o = (nv_f4){0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = exp2_fast(stat[0][w][r] - (mm == -INFINITY ? 0.0f : mm));
+          ll = __builtin_fmaf(stat[1][w][r], f, ll);
+          const nv_f4 x = *reinterpret_cast<const nv_f4*>(reinterpret_cast<const float*>(lds[w]) + r * S::ROW + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+        }
+        if (whole) {
+          write_row(a, row, d, o, mm, ll, vdec);
+        } else {
+          *reinterpret_cast<nv_f4*>(part + r * D + d) = o;
+          if (d == 0) {
+            part[16 * D + r] = mm;
+            part[16 * D + 16 + r] = ll;
+          }
         }
       }
+      break;
     }
-    __syncthreads();
+    if (j0 == 0 && j1 < kt && lane == 0) *join = cut.header(blockIdx.x, piece, 4 - wv, tile + kt, u, q, false);
+    if (mine.token >= 0) {
+      const bool whole = j0 == 0 && j1 == kt;
+      float* part = a.part + (2 * (int64_t)piece + (j0 == 0 ? 1 : 0)) * part_size(D);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int d = 16 * i + 4 * grp;
+        if (d >= D) continue;
+        if (whole) write_row(a, mine, d, O[i], m, l, vdec);
+        else *reinterpret_cast<nv_f4*>(part + col * D + d) = O[i];
+      }
+      if (!whole && grp == 0) {
+        part[16 * D + col] = m;
+        part[16 * D + 16 + col] = l;
+      }
+    }
     tile += j1 - j0;
   }
 }
 
-// Workgroup (i, y) joins rows 4 y .. 4 y + 3 of the unit that starts in piece i
-// and goes on in the next ones.
+// A wave joins rows y, y + 4, .. (y: grid y) of the unit that begins in its piece
+// and goes on in the next ones; of a unit that workgroups share, all four waves of
+// its first do.  D / 4 lanes take four sums each, groups of them every so many'th
+// part, four parts in flight at a time.
 __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a, int pieces) {
-  const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk, i = blockIdx.x;
-  const SplitCount count{G, Hk, a.most, 128};
-  SequenceScan<SplitCount> scan(a, count);
-  const int total = scan.total(), start = piece_start(total, pieces, i), stop = piece_start(total, pieces, i + 1);
-  if (start >= stop) return;
-  scan.restart();
-  Sequence q{};
-  if (!scan.find(stop - 1, q)) return;
-  const int kt = count.tiles(q.L), u = (stop - 1 - q.first) / kt, begin = q.first + u * kt, end = begin + kt;
-  if (begin < start || end <= stop) return;
-  const float vdec = a.c.va ? a.c.va[u % Hk] / 2688.0f : 1.0f;
-  for (int e = threadIdx.x; e < D; e += 256) {
-    const int r = 4 * blockIdx.y + e / (D / 4), d = e % (D / 4) * 4;
-    const UnitRow row = unit_row(q, G, Hk, u, r);
-    if (row.token < 0) continue;
+  constexpr int FLY = 4;
+  __shared__ nv_f4 sums[4][64];
+  __shared__ float stat[2][4];
+  const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk, lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
+  const JoinHeader* all = headers(a, D, pieces) + 4 * blockIdx.x;
+  const bool shared = all[0].shared != 0;
+  const JoinHeader j = all[shared ? 0 : wv];
+  if (j.parts == 0) return;
+  const int i = 4 * blockIdx.x + (shared ? 0 : wv);
+  const Sequence q{0, j.q0, j.n, 0, 0, 0};
+  const float vdec = a.c.va ? a.c.va[j.unit % Hk] / 2688.0f : 1.0f;
+  const int lanes = D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32 : 64, groups = 64 / lanes * (shared ? 4 : 1);
+  const int g = lane / lanes * (shared ? 4 : 1) + (shared ? wv : 0), d = lane % lanes * 4;
+  const bool in = d < D;
+  for (int r = blockIdx.y; r < 16; r += 4) {
+    const UnitRow row = unit_row(q, G, Hk, j.unit, r);
+    if (row.token < 0) break;
     float m = -INFINITY, l = 0.0f;
     nv_f4 o = (nv_f4){0, 0, 0, 0};
-    for (int p = i; p < pieces && (p == i || piece_start(total, pieces, p) < end); ++p) {
-      if (p != i && piece_start(total, pieces, p) >= piece_start(total, pieces, p + 1)) continue;
-      const float* part = a.part + (2 * (int64_t)p + (p == i ? 1 : 0)) * part_size(D);
-      const float pm = part[16 * D + r], mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
-      const float f = exp2_fast(m - base), g = exp2_fast(pm - base);
-      l = __builtin_fmaf(part[16 * D + 16 + r], g, l * f);
-      const nv_f4 x = *reinterpret_cast<const nv_f4*>(part + r * D + d);
+    for (int v0 = 0; v0 < j.parts; v0 += FLY * groups) {
+      float pm[FLY], pl[FLY];
+      nv_f4 x[FLY];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(x[k], g, o[k] * f);
+      for (int k = 0; k < FLY; ++k) {
+        const int v = v0 + k * groups + g;
+        const int p = v < j.head ? i + v : v < j.head + j.middle ? 4 * (i / 4 + 1 + v - j.head) : 4 * j.w1 + v - j.head - j.middle;
+        pm[k] = -INFINITY;
+        pl[k] = 0.0f;
+        x[k] = (nv_f4){0, 0, 0, 0};
+        if (v < j.parts && in) {
+          const float* part = a.part + (2 * (int64_t)p + (p == i ? 1 : 0)) * part_size(D);
+          pm[k] = part[16 * D + r];
+          pl[k] = part[16 * D + 16 + r];
+          x[k] = *reinterpret_cast<const nv_f4*>(part + r * D + d);
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) mn = fmaxf(mn, pm[k]);
+      const float base = mn == -INFINITY ? 0.0f : mn, f = exp2_fast(m - base);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= f;
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        const float w = exp2_fast(pm[k] - base);
+        l = __builtin_fmaf(pl[k], w, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(x[k][e], w, o[e]);
+      }
       m = mn;
     }
-    write_row(a, row, d, o, m, l, vdec);
+    // the groups' sums, in pairs, then the waves'
+    for (int off = lanes; off < 64; off <<= 1) {
+      const float om = __shfl_xor(m, off, 64), ol = __shfl_xor(l, off, 64), mn = fmaxf(m, om), base = mn == -INFINITY ? 0.0f : mn;
+      const float f = exp2_fast(m - base), w = exp2_fast(om - base);
+      l = l * f + ol * w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = o[e] * f + __shfl_xor(o[e], off, 64) * w;
+      m = mn;
+    }
+    if (shared) {
+      __syncthreads();
+      sums[wv][lane] = o;
+      if (lane == 0) {
+        stat[0][wv] = m;
+        stat[1][wv] = l;
+      }
+      __syncthreads();
+      m = fmaxf(fmaxf(stat[0][0], stat[0][1]), fmaxf(stat[0][2], stat[0][3]));
+      l = 0.0f;
+      o = (nv_f4){0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = exp2_fast(stat[0][w] - (m == -INFINITY ? 0.0f : m));
+        l = __builtin_fmaf(stat[1][w], f, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(sums[w][lane][e], f, o[e]);
+      }
+    }
+    if (lane < lanes && in && (!shared || wv == 0)) write_row(a, row, d, o, m, l, vdec);
   }
 }
 
@@ -316,12 +458,12 @@ int launch_attend_tiles(const AttendArgs& a, hipStream_t st);
 int launch_attend(const AttendArgs& a, int which, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   if (which & 1) {
-    const LayerLaunch p = plan_attend_split(a.T, a.B, a.q.heads, a.c.heads, (int64_t)a.width << a.c.shift);
+    const LayerLaunch p = plan_attend_split(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
     if (a.c.dim <= 64) k_attend_split<64><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
     else if (a.c.dim <= 128) k_attend_split<128><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
     else k_attend_split<256><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
-    const LayerLaunch j = plan_attend_join(a.T, a.B, a.q.heads, a.c.heads, (int64_t)a.width << a.c.shift);
-    if (j.grid) k_attend_join<<<dim3((uint32_t)j.grid, (uint32_t)j.y), j.block, 0, st>>>(a, (int)p.grid);
+    const LayerLaunch j = plan_attend_join(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
+    if (j.grid) k_attend_join<<<dim3((uint32_t)j.grid, (uint32_t)j.y), j.block, 0, st>>>(a, 4 * (int)p.grid);
   }
   if (which & 2) return launch_attend_tiles(a, st);
   return (int)hipGetLastError();

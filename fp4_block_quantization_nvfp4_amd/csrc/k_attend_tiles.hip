@@ -13,12 +13,17 @@
 namespace nvfp4 {
 
 struct TileCount {
-  int G, Hk, most;
+  int G, Hk, most, rows;
   NV_DEV int operator()(bool real, int n, int) const {
-    return !real || (int64_t)n * G <= most ? 0 : (int)(((int64_t)n * G + kAttendRows - 1) / kAttendRows) * Hk;
+    return !real || (int64_t)n * G <= most ? 0 : (int)(((int64_t)n * G + rows - 1) / rows) * Hk;
   }
 };
 
+#ifndef TILES_W
+#define TILES_W 4
+#define TILES_RB 1
+#define TILES_OCC 2
+#endif
 constexpr int kKeys = 64;  // keys of a tile
 
 // A lane's part of a tile as loaded: RUN elements of key tid / 4, and the same of the value.
@@ -73,56 +78,61 @@ struct RawTile {
   }
 };
 
-template <int DP>
-__global__ __launch_bounds__(256) void k_attend_tiles(const AttendArgs a) {
+// W waves, each with RB blocks of 32 rows.
+template <int DP, int W, int RB>
+__global__ __launch_bounds__(64 * W, TILES_OCC) void k_attend_tiles(const AttendArgs a) {
   constexpr int NQ = DP / 16, NT = DP / 32;  // steps of 16 along d; tiles of 32 of it
   constexpr int TILE = kKeys * DP * 2;       // bytes of a tile's keys, or values
+  constexpr int ROWS = 32 * RB * W;
   __shared__ __align__(16) uint8_t lds[4 * TILE];
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
   const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
-  const TileCount count{G, Hk, a.most};
+  const TileCount count{G, Hk, a.most, ROWS};
   SequenceScan<TileCount> scan(a, count);
   Sequence s{};
   if (!scan.find(blockIdx.x, s)) return;
   // the last rows first: with a causal mask they have the most keys
-  const int u = (int)blockIdx.x - s.first, h = u % Hk, units = (int)(((int64_t)s.n * G + kAttendRows - 1) / kAttendRows);
-  const int m0 = (units - 1 - u / Hk) * kAttendRows;
-  const int row = m0 + 32 * wv + col, mine = row / G;
-  const bool real = mine < s.n;
-  const int head = h * G + row - mine * G;
-  nv_u4 raw[NQ];
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int d = 16 * i + 8 * half;
-    raw[i] = (nv_u4){0, 0, 0, 0};
-    if (real && d < D) raw[i] = *reinterpret_cast<const nv_u4*>((const uint16_t*)a.q.at + (int64_t)(s.q0 + mine) * a.q.token + head * a.q.head + d);
-    big = amax_bits(raw[i], big);
-  }
-  {
-    const uint32_t o = (uint32_t)__shfl_xor((int)big, 32, 64);
-    big = o > big ? o : big;
-  }
-  const float factor = query_factor(big);
-  nv_h8 Q[NQ];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) Q[i] = query_to_f16(raw[i], factor);
+  const int u = (int)blockIdx.x - s.first, h = u % Hk, units = (int)(((int64_t)s.n * G + ROWS - 1) / ROWS);
+  const int m0 = (units - 1 - u / Hk) * ROWS;
   const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
-  const float by = a.scale * kLog2e / factor * kdec;
-  const int limit = real ? seen_by(a, s, mine) : 0;
+  nv_h8 Q[RB][NQ];
+  float by[RB], m[RB], l[RB];
+  int limit[RB];
+  nv_f16 O[RB][NT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int row = m0 + 32 * (RB * wv + b) + col, i = row / G, head = h * G + row - i * G;
+    nv_u4 raw[NQ];
+    uint32_t big = 0;
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+      const int d = 16 * k + 8 * half;
+      raw[k] = (nv_u4){0, 0, 0, 0};
+      if (i < s.n && d < D) raw[k] = *reinterpret_cast<const nv_u4*>((const uint16_t*)a.q.at + (int64_t)(s.q0 + i) * a.q.token + head * a.q.head + d);
+      big = amax_bits(raw[k], big);
+    }
+    const uint32_t o = (uint32_t)__shfl_xor((int)big, 32, 64);
+    const float factor = query_factor(o > big ? o : big);
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) Q[b][k] = query_to_f16(raw[k], factor);
+    by[b] = score_scale(a.scale * kLog2e / factor * kdec);
+    limit[b] = i < s.n ? seen_by(a, s, i) : 0;
+    m[b] = -INFINITY;
+    l[b] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) O[b][t][r] = 0.0f;
+  }
   // keys that the unit's rows see, and those that all of them do
-  const int m1 = m0 + kAttendRows - 1, last = m1 / G < s.n ? m1 / G : s.n - 1;
+  const int m1 = m0 + ROWS - 1, last = m1 / G < s.n ? m1 / G : s.n - 1;
   const int most = seen_by(a, s, last), least = seen_by(a, s, m0 / G);
-  nv_f16 O[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) O[i][r] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
-  const int tiles = (most + kKeys - 1) / kKeys, tk = threadIdx.x >> 2, g4 = threadIdx.x & 3;
+  const int tiles = (most + kKeys - 1) / kKeys;
+  const bool loads = threadIdx.x < 256;
+  const int tk = (threadIdx.x & 255) >> 2, g4 = threadIdx.x & 3;
   RawTile<DP> next;
   int page = tk < s.L ? page_of(a, s, tk) : 0;
-  if (tiles > 0) {
+  if (tiles > 0 && loads) {
     next.load(a, page, h, tk, tk < s.L, g4);
     page = kKeys + tk < s.L ? page_of(a, s, kKeys + tk) : 0;
     next.store(lds, lds + TILE, tk, g4);
@@ -132,57 +142,72 @@ __global__ __launch_bounds__(256) void k_attend_tiles(const AttendArgs a) {
     const uint8_t* K = lds + (j & 1) * 2 * TILE;
     const uint8_t* V = K + TILE;
     const int key0 = j * kKeys, nk = key0 + kKeys + tk;
-    if (j + 1 < tiles) {
+    if (j + 1 < tiles && loads) {
       next.load(a, page, h, nk, nk < s.L, g4);
       page = nk + kKeys < s.L ? page_of(a, s, nk + kKeys) : 0;
     }
-    nv_f16 S[2];
+    nv_f16 S[RB][2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) S[t][r] = 0.0f;
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int key = 32 * t + col, c = 2 * i + half;
+        for (int r = 0; r < 16; ++r) S[b][t][r] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        const int key = 32 * t + col, c = 2 * k + half;
         const nv_h8 A = *reinterpret_cast<const nv_h8*>(K + key * DP * 2 + ((c ^ (key & 7)) << 4));
-        S[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, Q[i], S[t], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) S[b][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, Q[b][k], S[b][t], 0, 0, 0);
       }
     }
-    float top = -INFINITY;
-    const bool edge = key0 + kKeys > least;
+    if (key0 + kKeys > least) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float x = S[t][r] * by;
-        if (edge) {
-          const int key = key0 + 32 * t + 8 * (r / 4) + 4 * half + r % 4;
-          x = key < limit ? x : -INFINITY;
-        }
-        S[t][r] = x;
-        top = fmaxf(top, x);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (key0 + 32 * t + 8 * (r / 4) + 4 * half + r % 4 >= limit[b]) S[b][t][r] = -INFINITY;
+    }
+    nv_h8 P[RB][2][2];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, S[b][t][r]);
+      top = half_max(top) * by[b];
+      if (__builtin_amdgcn_ballot_w64(top > m[b] + kSlack)) {
+        const float mn = fmaxf(m[b], top), alpha = exp2_fast(m[b] - (mn == -INFINITY ? 0.0f : mn));
+        m[b] = mn;
+        l[b] *= alpha;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) O[b][t][r] *= alpha;
       }
-    top = other_half_max(top);
-    const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = exp2_fast(m - base);
-    m = mn;
-    l *= alpha;
+      const float up = kWeightBits - (m[b] == -INFINITY ? 0.0f : m[b]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) O[i][r] *= alpha;
+        for (int q = 0; q < 2; ++q) {  // sixteen keys: 4 half + 0..3, and 8 more
+          nv_u4 w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = exp2_fast(__builtin_fmaf(S[b][t][8 * q + 2 * i], by[b], up));
+            const float y = exp2_fast(__builtin_fmaf(S[b][t][8 * q + 2 * i + 1], by[b], up));
+            l[b] += x + y;
+            w[i] = pack_f16(x, y);
+          }
+          P[b][t][q] = __builtin_bit_cast(nv_h8, w);
+        }
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {  // sixteen keys: 4 half + 0..3, and 8 more
-        nv_u4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = exp2_fast(S[t][8 * q + 2 * i] - base + kWeightBits), y = exp2_fast(S[t][8 * q + 2 * i + 1] - base + kWeightBits);
-          l += x + y;
-          w[i] = pack_f16(x, y);
-        }
-        const nv_h8 P = __builtin_bit_cast(nv_h8, w);
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           nv_h4 part[2];
@@ -190,43 +215,44 @@ __global__ __launch_bounds__(256) void k_attend_tiles(const AttendArgs a) {
           for (int g = 0; g < 2; ++g) {
             const int c16 = lane & 15, key = 32 * t + 16 * q + 8 * g + 4 * half + (c16 >> 2);
             const int c = 4 * i + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1);
-            typedef __attribute__((address_space(3))) short lds_s;
-            typedef short s4 __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s4 lds_s4;
-            const uint32_t off = (uint32_t)(uintptr_t)(lds_s*)(V + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (c16 & 1));
-            part[g] = __builtin_bit_cast(nv_h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(uintptr_t)off));
+            part[g] = read_turned(V + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (c16 & 1));
           }
-          O[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7), P, O[i], 0, 0, 0);
+          const nv_h8 A = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) O[b][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, P[b][t][q], O[b][i], 0, 0, 0);
         }
-      }
-    if (j + 1 < tiles) {
+    if (j + 1 < tiles && loads) {
       uint8_t* to = lds + ((j + 1) & 1) * 2 * TILE;
       next.store(to, to + TILE, tk, g4);
     }
     __syncthreads();
   }
-  l += __shfl_xor(l, 32, 64);
-  if (!real) return;
-  const float inv = l == 0.0f ? 0.0f : vdec / l;
-  const int64_t out = (int64_t)(s.q0 + mine) * a.q.heads + head;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int b = 0; b < RB; ++b) {
+    const float sum = l[b] + __shfl_xor(l[b], 32, 64);
+    const int row = m0 + 32 * (RB * wv + b) + col, i = row / G, head = h * G + row - i * G;
+    if (i >= s.n) continue;
+    const float inv = sum == 0.0f ? 0.0f : vdec / sum;
+    const int64_t out = (int64_t)(s.q0 + i) * a.q.heads + head;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 32 * i + 8 * r + 4 * half;
-      if (d >= D) continue;
-      nv_u2 w;
-      w.x = pack_bf16(O[i][4 * r] * inv, O[i][4 * r + 1] * inv);
-      w.y = pack_bf16(O[i][4 * r + 2] * inv, O[i][4 * r + 3] * inv);
-      *reinterpret_cast<nv_u2*>(a.out + out * D + d) = w;
-    }
-  if (half == 0) a.lse[out] = l == 0.0f ? -INFINITY : (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l)));
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 32 * t + 8 * r + 4 * half;
+        if (d >= D) continue;
+        nv_u2 w;
+        w.x = pack_bf16(O[b][t][4 * r] * inv, O[b][t][4 * r + 1] * inv);
+        w.y = pack_bf16(O[b][t][4 * r + 2] * inv, O[b][t][4 * r + 3] * inv);
+        *reinterpret_cast<nv_u2*>(a.out + out * D + d) = w;
+      }
+    if (half == 0) a.lse[out] = sum == 0.0f ? -INFINITY : log_sum(m[b], sum);
+  }
 }
 
 template <int DP>
 static int tiles_go(const AttendArgs& a, hipStream_t st) {
   const LayerLaunch p = plan_attend_tiles(a.T, a.B, a.q.heads, a.c.heads);
-  k_attend_tiles<DP><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
+  k_attend_tiles<DP, TILES_W, TILES_RB><<<(uint32_t)p.grid, 64 * TILES_W, 0, st>>>(a);
   return (int)hipGetLastError();
 }
 

@@ -7,11 +7,14 @@
 // taken times the power of two that brings its largest element to 2^13 and is
 // exact too, but for elements below 2^-24 of that one, which lose bits that the
 // sums in fp32 do not have.  The second-level scales are applied to the sums.
-// Weights exp(s - max) are rounded to fp16 times 2^14, so that they keep 11 bits
-// down to 2^-28 (a bf16 result has 8); their sum is taken before that rounding.
+// Weights exp(s - max) are rounded to fp16 times 2^11, the maximum being one that
+// may lie up to 2^4 below the row's, so that sums are rescaled seldom: they keep 11
+// bits down to 2^-25 (a bf16 result has 8), and below are off by 2^-36 of the
+// largest at most.  Their sum is taken before that rounding.
 #pragma once
 
 #include "nvfp4_cache.hpp"
+#include "nvfp4_experts.hpp"
 #include "nvfp4_plan.hpp"
 
 namespace nvfp4 {
@@ -20,10 +23,9 @@ typedef _Float16 nv_h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 nv_h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 nv_h8 __attribute__((ext_vector_type(8)));
 
-constexpr float kLog2e = 1.44269504088896340736f, kWeightBits = 14.0f;
+constexpr float kLog2e = 1.44269504088896340736f, kWeightBits = 11.0f, kSlack = 4.0f;
 constexpr double kLn2 = 0.693147180559945309417;
 
-NV_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 NV_DEV float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Eight codes times their block's scale (in both halves) -> fp16, exact.
@@ -72,7 +74,44 @@ NV_DEV uint32_t pack_f16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, nv_h2));
 }
 
-NV_DEV float other_half_max(float v) { return fmaxf(v, __shfl_xor(v, 32, 64)); }
+// Maximum (sum) over the lanes that are 32, or 16 and 32 apart, register to
+// register: a swap of two copies gives each lane its own and the other's.
+NV_DEV nv_f2 halves(float v) {
+  const nv_u32x2 r = __builtin_bit_cast(nv_u32x2, __builtin_amdgcn_permlane32_swap(f2bits(v), f2bits(v), false, false));
+  return (nv_f2){bits2f(r.x), bits2f(r.y)};
+}
+NV_DEV nv_f2 quarters(float v) {
+  const nv_u32x2 r = __builtin_bit_cast(nv_u32x2, __builtin_amdgcn_permlane16_swap(f2bits(v), f2bits(v), false, false));
+  return (nv_f2){bits2f(r.x), bits2f(r.y)};
+}
+NV_DEV float half_max(float v) {
+  const nv_f2 r = halves(v);
+  return fmaxf(r.x, r.y);
+}
+NV_DEV float quarter_max(float v) {
+  const nv_f2 r = quarters(v);
+  return half_max(fmaxf(r.x, r.y));
+}
+NV_DEV float quarter_sum(float v) {
+  const nv_f2 r = quarters(v);
+  const nv_f2 h = halves(r.x + r.y);
+  return h.x + h.y;
+}
+
+// What a score is taken times; never zero, so that hidden scores stay -infinity.
+NV_DEV float score_scale(float v) { return v < 0x1p-120f ? 0x1p-120f : v; }
+
+// log of the sum of exp from the running maximum and the sum of weights.
+NV_DEV float log_sum(float m, float l) { return (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l))); }
+
+// Of each sixteen lanes, lane 4 x + y names a quarter (four fp16) of row x; lane i
+// gets element i of the four rows.
+NV_DEV nv_h4 read_turned(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) const uint8_t lds_byte;
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  return __builtin_bit_cast(nv_h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(uintptr_t)(uint32_t)(uintptr_t)(lds_byte*)p));
+}
 
 // ------------------------------------------------------------- sequences
 
@@ -85,55 +124,68 @@ struct Sequence {
   int b, q0, n, L, first, over;  // first: units of the sequences before it
 };
 
-// One wave walks the sequences 64 at a time; Count gives a sequence's units.
+// One wave walks the sequences, kScan at a time, four of them a lane; Count gives a
+// sequence's units.  (64 at a time, one a lane: 256 sequences of up to 500 keys took
+// five rounds of loads and sums before the first key was read.)
+constexpr int kScan = 256;
 template <typename Count>
 struct SequenceScan {
+  static constexpr int PER = kScan / 64;
   const AttendArgs& a;
   const Count& count;
-  int lane, base, prev, before;       // sequences done, running end, units done
-  int q0, n, L, over, first, own;     // this lane's sequence of the current 64
+  int lane, base, prev, before;  // sequences done, running end, units done
+  int end[PER], len[PER], first[PER], begin, stop;  // this lane's: ends, lengths, units before each, first query, units up to the last
+  int next, last, longest;       // units and queries up to the current ones' end; the largest length so far
 
-  NV_DEV SequenceScan(const AttendArgs& a_, const Count& c_) : a(a_), count(c_), lane(threadIdx.x & 63) { restart(); }
+  NV_DEV SequenceScan(const AttendArgs& a_, const Count& c_) : a(a_), count(c_), lane(threadIdx.x & 63), base(0), prev(0), before(0), longest(0) { load(); }
   NV_DEV void restart() {
+    if (base == 0) return;
     base = prev = before = 0;
     load();
   }
-  NV_DEV void load() {
-    const int b = base + lane;
-    int end = a.T, len = 0;
-    if (b < a.B) {
-      end = a.ends ? a.ends[b] : b + 1;
-      end = end < 0 ? 0 : end > a.T ? a.T : end;
-      len = a.lens[b];
-    }
-    end = end > prev ? end : prev;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(end, off, 64);
-      end = lane >= off && o > end ? o : end;
-    }
-    const int up = __shfl_up(end, 1, 64);
-    q0 = lane ? up : prev;
-    n = b <= a.B ? end - q0 : 0;
+  NV_DEV int keys(int raw) const {
     const int64_t most = (int64_t)a.width << a.c.shift;
-    over = (int64_t)len > most ? 1 : 0;
-    L = len < 0 ? 0 : over ? (int)most : len;
-    own = n > 0 ? count(b < a.B, n, L) : 0;
-    int sum = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(sum, off, 64);
-      sum += lane >= off ? o : 0;
-    }
-    first = before + sum - own;
-    next = before + __shfl(sum, 63, 64);
-    last = __shfl(end, 63, 64);
+    return raw < 0 ? 0 : (int64_t)raw > most ? (int)most : raw;
   }
-  int next, last;
-  // To the next 64; false where there are none.
+  NV_DEV void load() {
+    const int b0 = base + PER * lane;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      end[i] = a.T;
+      len[i] = 0;
+      if (b0 + i < a.B) {
+        end[i] = a.ends ? a.ends[b0 + i] : b0 + i + 1;
+        len[i] = a.lens[b0 + i];
+      }
+    }
+    int top = prev;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      end[i] = end[i] < 0 ? 0 : end[i] > a.T ? a.T : end[i];
+      top = end[i] = end[i] > top ? end[i] : top;
+    }
+    top = running_max(top);
+    begin = __builtin_amdgcn_update_dpp(prev, top, 0x138, 0xF, 0xF, false);  // the lane before's; lane 0: prev
+    int at = begin, sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      end[i] = end[i] > begin ? end[i] : begin;
+      const int n = b0 + i <= a.B ? end[i] - at : 0, L = keys(len[i]);
+      longest = L > longest ? L : longest;
+      first[i] = sum;
+      sum += n > 0 ? count(b0 + i < a.B, n, L) : 0;
+      at = end[i];
+    }
+    stop = before + running_sum(sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) first[i] += stop - sum;
+    next = __builtin_amdgcn_readlane(stop, 63);
+    last = __builtin_amdgcn_readlane(top, 63);
+  }
+  // On; false where there are none.
   NV_DEV bool advance() {
-    if (base + 64 > a.B) return false;
-    base += 64;
+    if (base + kScan > a.B) return false;
+    base += kScan;
     prev = last;
     before = next;
     load();
@@ -141,20 +193,30 @@ struct SequenceScan {
   }
   NV_DEV int total() {
     while (advance()) {}
+    longest = __builtin_amdgcn_readlane(running_max(longest), 63);
     return next;
   }
-  // The sequence that has unit x, at or past the current 64; false: no sequence has.
+  // The sequence that has unit x, at or past the current ones; false: no sequence has.
   NV_DEV bool find(int x, Sequence& s) {
     while (x >= next)
       if (!advance()) return false;
-    const uint64_t hit = __builtin_amdgcn_ballot_w64(x >= first && x < first + own);
-    const int from = (int)__builtin_ctzll(hit);
-    s.b = base + from;
-    s.q0 = __builtin_amdgcn_readlane(q0, from);
-    s.n = __builtin_amdgcn_readlane(n, from);
-    s.L = __builtin_amdgcn_readlane(L, from);
-    s.over = __builtin_amdgcn_readlane(over, from);
-    s.first = __builtin_amdgcn_readlane(first, from);
+    const int from = (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(x >= first[0] && x < stop));
+    // a sequence without units starts where the next one does: the last that starts up to x has it
+    int i = 0, q0 = __builtin_amdgcn_readlane(begin, from), e = __builtin_amdgcn_readlane(end[0], from), raw = __builtin_amdgcn_readlane(len[0], from);
+    s.first = __builtin_amdgcn_readlane(first[0], from);
+#pragma unroll
+    for (int k = 1; k < PER; ++k) {
+      const int f = __builtin_amdgcn_readlane(first[k], from), ek = __builtin_amdgcn_readlane(end[k], from), rk = __builtin_amdgcn_readlane(len[k], from);
+      if (f <= x) {
+        q0 = __builtin_amdgcn_readlane(end[k - 1], from);
+        s.first = f, e = ek, raw = rk, i = k;
+      }
+    }
+    s.b = base + PER * from + i;
+    s.q0 = q0;
+    s.n = e - q0;
+    s.L = keys(raw);
+    s.over = raw > s.L ? 1 : 0;
     return true;
   }
 };
@@ -172,6 +234,36 @@ NV_DEV int page_of(const AttendArgs& a, const Sequence& s, int j) {
   return p >= 0 && p < a.c.pages && !s.over ? p : -1;
 }
 constexpr uint32_t kNanScales = 0x7F7F;
+
+// A sequence's pages for a wave that walks along the keys: 64 entries of its row of
+// the table in a register, the next 64 on their way, so that no load waits for a
+// page number.
+struct PageWindow {
+  const int* row;
+  int width, pages, shift, base, now, ahead;
+  // (A sequence without keys, as that of the queries past the last end, may have no row.)
+  NV_DEV PageWindow(const AttendArgs& a, const Sequence& s, int key)
+      : row(a.table + (int64_t)s.b * a.width), width(s.L > 0 ? a.width : 0), pages(s.over ? 0 : a.c.pages), shift(a.c.shift) {
+    base = key >> shift;
+    now = fetch(base);
+    ahead = fetch(base + 64);
+  }
+  NV_DEV int fetch(int at) const {
+    const int i = at + (int)(threadIdx.x & 63);
+    return i < width ? row[i] : -1;
+  }
+  // Page of key (at or past the last one asked for, below L), or -1.
+  NV_DEV int operator()(int key) {
+    const int i = key >> shift;
+    while (i >= base + 64) {
+      base += 64;
+      now = ahead;
+      ahead = fetch(base + 64);
+    }
+    const int p = __builtin_amdgcn_readlane(now, i - base);
+    return p >= 0 && p < pages ? p : -1;
+  }
+};
 
 NV_DEV uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 

@@ -307,8 +307,11 @@ inline LayerLaunch plan_read_cache(int64_t T, int64_t heads, int64_t D) {
 // Attention.  Rows: queries times the heads that share keys.  The split kernel takes sequences of up
 // to kAttendFew rows, and all where no sequence can have more; the tiled one the others.
 constexpr int kAttendFew = 32;
-constexpr int64_t kAttendPieces = 1024;  // workgroups of the split kernel at most
-constexpr int kAttendTile = 128;         // keys of a tile of its work
+// Workgroups of the split kernel at most: what runs at a time.  Of heads up to 128 the registers of
+// two waves on a SIMD (three: 64 sequences of up to 8192 keys 88 -> 105 us, codes spilled), of
+// larger ones of one (32 of head size 256: two 67 us, one 61).
+constexpr int64_t kAttendPieces = 512;  // workgroups of the split kernel at most
+constexpr int kAttendTile = 64;          // keys of a tile of its work
 constexpr int kAttendRows = 128;         // rows of a unit of the tiled kernel
 
 inline int attend_kernels(int64_t T, int64_t Hq, int64_t Hk, bool ends) { return ends && T * (Hq / Hk) > kAttendFew ? 3 : 1; }
@@ -318,19 +321,19 @@ inline int64_t attend_split_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk, 
   const int64_t units = B * few * Hk;
   return units * (keys > 0 ? ceil_div(keys, kAttendTile) : 1) + ceil_div(T * G, 16) * Hk;
 }
-inline int64_t attend_pieces(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
-  const int64_t n = attend_split_tiles(T, B, Hq, Hk, keys);
-  return n < kAttendPieces ? n : kAttendPieces;
+inline int64_t attend_pieces(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  const int64_t n = ceil_div(attend_split_tiles(T, B, Hq, Hk, keys), 4), most = D > 128 ? kAttendPieces / 2 : kAttendPieces;
+  return n < most ? n : most;
 }
-inline LayerLaunch plan_attend_split(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
-  return {PLAN_ATTEND_SPLIT, attend_pieces(T, B, Hq, Hk, keys), 1, 256};
+inline LayerLaunch plan_attend_split(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  return {PLAN_ATTEND_SPLIT, attend_pieces(T, B, Hq, Hk, D, keys), 1, 256};
 }
-inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t keys) {
+inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
   if (keys <= kAttendTile) return {0, 0, 0, 0};  // no unit has two tiles
-  return {PLAN_ATTEND_JOIN, attend_pieces(T, B, Hq, Hk, keys), 4, 256};
+  return {PLAN_ATTEND_JOIN, attend_pieces(T, B, Hq, Hk, D, keys), 4, 256};
 }
 inline size_t attend_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
-  return keys <= kAttendTile ? 0 : (size_t)(attend_pieces(T, B, Hq, Hk, keys) * 2 * (16 * D + 32) * 4);
+  return keys <= kAttendTile ? 0 : (size_t)(4 * attend_pieces(T, B, Hq, Hk, D, keys) * (2 * (16 * D + 32) * 4 + 32));
 }
 // Units of the tiled kernel at most: each sequence adds less than one to T * G / rows.
 inline LayerLaunch plan_attend_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk) {

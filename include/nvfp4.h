@@ -487,7 +487,7 @@ nvfp4_status nvfp4_read_cache(const nvfp4_cache* cache, const int32_t* slots, in
  * of a sequence longer than width * page_size, gets NaN.  width >= 1, scale >
  * 0.  Sums have a fixed order.  Further limits (NVFP4_E_RANGE): B <= 2^20, B * heads
  * <= 2^22, width * page_size <= 2^30, and B * max(2, ceil(G / 16)) * heads *
- * ceil(width * page_size / 128) + ceil(T * G / 16) * heads < 2^31, G = q->heads /
+ * ceil(width * page_size / 64) + ceil(T * G / 16) * heads < 2^31, G = q->heads /
  * heads.  workspace: at least
  * nvfp4_cache_attention_workspace_bytes (0: may be NULL), 16-byte aligned.
  */

@@ -87,10 +87,11 @@ def attention(q, keys, values, table, lens, ends, scale=None, causal=True):
         size = torch.einsum("thd,lhd->thl", q[t].abs(), k.abs()) * scale
         size = torch.where(torch.isfinite(s), size, 0.0).amax(-1)
         delta = (D + 16) * 2.0 ** -23 * size + 2.0 ** -20
-        # a weight: that, and its rounding to fp16 (2^-11; weights below 2^-28 of the largest less than 2^-38 of it); L terms
+        # a weight: that, and its rounding to fp16: 2^-11 of it, or half of fp16's smallest step 2^-24 where it is small; weights
+        # are 2^11 times exp(s - m) with m at most the row's maximum, so that step is at most 2^-35 of the largest weight; L terms
         # summed in fp32; the result's rounding to bf16
         spread = torch.einsum("thl,lhd->thd", p, v.abs())
-        small = L * 2.0 ** -38 * v.abs().amax(0)
+        small = L * 2.0 ** -36 * v.abs().amax(0)
         off[t] = out[t].abs() * 2.0 ** -8 + spread * (2.0 ** -11 + 2 * delta + (L + 64) * 2.0 ** -23).unsqueeze(-1) + small
         loff[t] = 2 * delta + (L + 64) * 2.0 ** -23 + torch.where(torch.isfinite(lse[t]), lse[t].abs(), 0.0) * 2.0 ** -22
     return out, lse, off, loff

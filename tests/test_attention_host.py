@@ -204,8 +204,8 @@ def test_launches_stay_in_the_limits():
             c = cache(heads=Hk, dim=D)
             G = Hq // Hk
             need = L.lib().nvfp4_cache_attention_workspace_bytes(T, Hq, ref(c), B, keys // 16)
-            assert (launches[1][1] > 0) == (need > 0) == (keys > 128)
-            assert launches[1][1] in (0, first[1]) and need in (0, first[1] * 2 * (16 * D + 32) * 4)
+            assert (launches[1][1] > 0) == (need > 0) == (keys > 64)
+            assert launches[1][1] in (0, first[1]) and need in (0, 4 * first[1] * (2 * (16 * D + 32) * 4 + 32))
             if launches[2][1]:  # units of any split of T queries over B sequences and those of none
                 assert entry == 5 and launches[2][1] >= (ceil(T * G, 128) + B) * Hk
             else:
