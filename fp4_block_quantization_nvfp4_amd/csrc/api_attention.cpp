@@ -223,7 +223,7 @@ nvfp4_status nvfp4_read_cache(const nvfp4_cache* cache, const int32_t* slots, in
 size_t nvfp4_cache_attention_workspace_bytes(int64_t T, int64_t q_heads, const nvfp4_cache* cache, int64_t B,
                                              int64_t width) {
   if (check_attention(T, q_heads, cache, B, width) != NVFP4_OK || T == 0 || q_heads == 0) return 0;
-  return nvfp4::attend_workspace_bytes(T, B, q_heads, cache->heads, cache->dim, width * cache->page_size);
+  return nvfp4::attend_workspace_bytes(T, B, q_heads, cache->heads, cache->dim, width * cache->page_size, true);
 }
 
 nvfp4_status nvfp4_cache_attention(const nvfp4_heads* q, int64_t T, const nvfp4_cache* cache, const int32_t* table,
@@ -238,7 +238,7 @@ nvfp4_status nvfp4_cache_attention(const nvfp4_heads* q, int64_t T, const nvfp4_
   if (T == 0 || q->heads == 0) return NVFP4_OK;
   if (nvfp4_status st = check_at(q, T, NVFP4_BF16)) return st;
   if (!out || !lse || (B != 0 && (!table || !lens))) return NVFP4_E_NULL;
-  const size_t need = nvfp4::attend_workspace_bytes(T, B, q->heads, cache->heads, cache->dim, width * cache->page_size);
+  const size_t need = nvfp4::attend_workspace_bytes(T, B, q->heads, cache->heads, cache->dim, width * cache->page_size, ends != nullptr);
   if (need && !workspace) return NVFP4_E_NULL;
   if (workspace_bytes < need) return NVFP4_E_ARG;
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(ends, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
@@ -257,7 +257,7 @@ nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int
   if (nvfp4_status st = check_tokens(T, D, entry < 5 ? nvfp4::kRopeMaxD : 256)) return st;
   if (Hq < 0 || Hk < 1 || B < 0 || keys < 16 || (entry >= 5 && (Hq % Hk != 0 || Hq == 0 || D % 32 != 0))) return NVFP4_E_SHAPE;
   if (Hq > kMaxHeads || Hk > kMaxHeads || !fits(Hq * D, T) || !fits(Hk * D, T) || B > kMaxB || keys > kMaxKeys || B * Hk > kMaxUnits) return NVFP4_E_RANGE;
-  nvfp4::LayerLaunch p[3] = {};
+  nvfp4::LayerLaunch p[4] = {};
   if (T != 0) {
     if (entry == 0) p[0] = nvfp4::plan_rope(T, Hq + Hk, D);
     if (entry == 1) p[0] = nvfp4::plan_rope_bwd(T), p[1] = nvfp4::plan_rope_sum(D);
@@ -268,10 +268,13 @@ nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int
       if (nvfp4::attend_split_tiles(T, B, Hq, Hk, keys) >= int64_t(1) << 31) return NVFP4_E_RANGE;
       p[0] = nvfp4::plan_attend_split(T, B, Hq, Hk, D, keys);
       p[1] = nvfp4::plan_attend_join(T, B, Hq, Hk, D, keys);
-      if (nvfp4::attend_kernels(T, Hq, Hk, entry == 5) & 2) p[2] = nvfp4::plan_attend_tiles(T, B, Hq, Hk);
+      if (nvfp4::attend_kernels(T, Hq, Hk, entry == 5) & 2) {
+        p[2] = nvfp4::plan_attend_tiles(T, B, Hq, Hk, D, keys);
+        p[3] = nvfp4::plan_attend_tiles_join(T, B, Hq, Hk, D, keys);
+      }
     }
   }
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     plan[4 * i] = p[i].kernel;
     plan[4 * i + 1] = p[i].grid;
     plan[4 * i + 2] = p[i].y;

@@ -20,10 +20,10 @@
 namespace nvfp4 {
 
 struct SplitCount {
-  int G, Hk, most, tile;
+  int G, Hk, most;
   // units of a sequence times their tiles of keys; a unit without keys counts as one
   NV_DEV int units(int n) const { return (int)(((int64_t)n * G + 15) / 16) * Hk; }
-  NV_DEV int tiles(int L) const { return L > 0 ? (L + tile - 1) / tile : 1; }
+  NV_DEV int tiles(int L) const { return L > 0 ? (L + kAttendTile - 1) / kAttendTile : 1; }
   NV_DEV int operator()(bool real, int n, int L) const { return real && (int64_t)n * G > most ? 0 : units(n) * tiles(L); }
 };
 
@@ -72,17 +72,6 @@ struct UnitRow {
 NV_DEV UnitRow unit_row(const Sequence& s, int G, int Hk, int unit, int r) {
   const int h = unit % Hk, m = unit / Hk * 16 + r, i = m / G;
   return {i < s.n ? s.q0 + i : -1, h * G + m - i * G};
-}
-
-// Four elements of a row, from its sums o, maximum and sum of weights.
-NV_DEV void write_row(const AttendArgs& a, const UnitRow& u, int d, nv_f4 o, float m, float l, float vdec) {
-  const float inv = l == 0.0f ? 0.0f : vdec / l;
-  const int64_t row = (int64_t)u.token * a.q.heads + u.head;
-  nv_u2 w;
-  w.x = pack_bf16(o[0] * inv, o[1] * inv);
-  w.y = pack_bf16(o[2] * inv, o[3] * inv);
-  *reinterpret_cast<nv_u2*>(a.out + row * a.c.dim + d) = w;
-  if (d == 0) a.lse[row] = l == 0.0f ? -INFINITY : log_sum(m, l);
 }
 
 template <int DP>
@@ -152,7 +141,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
   __shared__ float stat[2][4][16];
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
   const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
-  const SplitCount count{G, Hk, a.most, kAttendTile};
+  const SplitCount count{G, Hk, a.most};
   SequenceScan<SplitCount> scan(a, count);
   const int total = scan.total();
   const Pieces cut(count, total, scan.longest, 4 * gridDim.x);
@@ -226,13 +215,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
     const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
     const float by = score_scale(a.scale * kLog2e / factor * kdec);
     const int limit = mine.token < 0 ? 0 : seen_by(a, q, mine.token - q.q0);
-    const int least = seen_by(a, q, u / Hk * 16 / G);  // what all rows of the unit see
+    const int least = uniform(seen_by(a, q, u / Hk * 16 / G));  // what all rows of the unit see
     nv_f4 O[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) O[i] = (nv_f4){0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
     uint8_t* vs = lds[wv];
-    auto step = [&](const RawKeys<DP>(&K)[2], const RawKeys<DP>(&V)[2], int key0) {
+    auto step = [&](const RawKeys<DP>(&K)[2], const RawKeys<DP>(&V)[2], int key0, auto masked) {
       nv_f4 Sc[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -240,20 +229,21 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
 #pragma unroll
         for (int i = 0; i < NS; ++i) Sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(K[g].values(i), Q[i], Sc[g], 0, 0, 0);
       }
-      // values to shared memory, key by key; eight elements c of a key at c ^ key
+      // values to shared memory, key by key; chunk by chunk
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const int key = 16 * g + col, c = NS * grp + i;
-          *reinterpret_cast<nv_h8*>(vs + key * DP * 2 + ((c ^ (key & 7)) << 4)) = V[g].values(i);
+          *reinterpret_cast<nv_h8*>(vs + key * DP * 2 + ((c ^ chunk_at(key)) << 4)) = V[g].values(i);
         }
-      if (key0 + 32 > least) {
+      if constexpr (masked.value) {
+        const int hidden = limit - key0 - 4 * grp;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (key0 + 16 * g + 4 * grp + r >= limit) Sc[g][r] = -INFINITY;
+            if (16 * g + r >= hidden) Sc[g][r] = -INFINITY;
       }
       const float top = quarter_max(fmaxf(fmaxf(fmaxf(Sc[0][0], Sc[0][1]), fmaxf(Sc[0][2], Sc[0][3])),
                                           fmaxf(fmaxf(Sc[1][0], Sc[1][1]), fmaxf(Sc[1][2], Sc[1][3])))) * by;
@@ -287,7 +277,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int key = 16 * g + 4 * grp + (col >> 2), c = 2 * i + ((col & 3) >> 1);
-          part[g] = read_turned(vs + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (col & 1));
+          part[g] = read_turned(vs + key * DP * 2 + ((c ^ chunk_at(key)) << 4) + 8 * (col & 1));
         }
         const nv_h8 A = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
         O[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A, P, O[i], 0, 0, 0);
@@ -296,11 +286,17 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
       __builtin_amdgcn_wave_barrier();
     };
     // the next 32 keys are on their way while these are used
+    for (; key0 + 64 <= least && key0 + 64 <= keys; key0 += 64) {
+      load(K1, V1, key0 + 32);
+      step(K0, V0, key0, Masked<false>{});
+      load(K0, V0, key0 + 64);
+      step(K1, V1, key0 + 32, Masked<false>{});
+    }
     for (; key0 < keys; key0 += 64) {
       load(K1, V1, key0 + 32);
-      step(K0, V0, key0);
+      step(K0, V0, key0, Masked<true>{});
       load(K0, V0, key0 + 64);
-      if (key0 + 32 < keys) step(K1, V1, key0 + 32);
+      if (key0 + 32 < keys) step(K1, V1, key0 + 32, Masked<true>{});
     }
     l = quarter_sum(l);
     if (shared) {
@@ -333,7 +329,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
           for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
         }
         if (whole) {
-          write_row(a, row, d, o, mm, ll, vdec);
+          write_row(a, (int64_t)row.token * a.q.heads + row.head, d, o, mm, ll, vdec);
         } else {
           *reinterpret_cast<nv_f4*>(part + r * D + d) = o;
           if (d == 0) {
@@ -352,7 +348,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
       for (int i = 0; i < NT; ++i) {
         const int d = 16 * i + 4 * grp;
         if (d >= D) continue;
-        if (whole) write_row(a, mine, d, O[i], m, l, vdec);
+        if (whole) write_row(a, (int64_t)mine.token * a.q.heads + mine.head, d, O[i], m, l, vdec);
         else *reinterpret_cast<nv_f4*>(part + col * D + d) = O[i];
       }
       if (!whole && grp == 0) {
@@ -383,22 +379,27 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a, int pie
   const int lanes = D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32 : 64, groups = 64 / lanes * (shared ? 4 : 1);
   const int g = lane / lanes * (shared ? 4 : 1) + (shared ? wv : 0), d = lane % lanes * 4;
   const bool in = d < D;
-  for (int r = blockIdx.y; r < 16; r += 4) {
+  // few parts of many rows: the groups take rows of their own
+  const bool apart = !shared && j.parts <= 2 * FLY && unit_row(q, G, Hk, j.unit, 4).token >= 0;
+  const int first = apart ? 0 : g, step = apart ? 1 : groups;
+  for (int r0 = blockIdx.y; r0 < 16; r0 += apart ? 4 * groups : 4) {
+    if (unit_row(q, G, Hk, j.unit, r0).token < 0) break;
+    const int r = apart ? r0 + 4 * g : r0;
     const UnitRow row = unit_row(q, G, Hk, j.unit, r);
-    if (row.token < 0) break;
+    const bool mine = in && r < 16 && row.token >= 0;
     float m = -INFINITY, l = 0.0f;
     nv_f4 o = (nv_f4){0, 0, 0, 0};
-    for (int v0 = 0; v0 < j.parts; v0 += FLY * groups) {
+    for (int v0 = 0; v0 < j.parts; v0 += FLY * step) {
       float pm[FLY], pl[FLY];
       nv_f4 x[FLY];
 #pragma unroll
       for (int k = 0; k < FLY; ++k) {
-        const int v = v0 + k * groups + g;
+        const int v = v0 + k * step + first;
         const int p = v < j.head ? i + v : v < j.head + j.middle ? 4 * (i / 4 + 1 + v - j.head) : 4 * j.w1 + v - j.head - j.middle;
         pm[k] = -INFINITY;
         pl[k] = 0.0f;
         x[k] = (nv_f4){0, 0, 0, 0};
-        if (v < j.parts && in) {
+        if (v < j.parts && mine) {
           const float* part = a.part + (2 * (int64_t)p + (p == i ? 1 : 0)) * part_size(D);
           pm[k] = part[16 * D + r];
           pl[k] = part[16 * D + 16 + r];
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a, int pie
       m = mn;
     }
     // the groups' sums, in pairs, then the waves'
-    for (int off = lanes; off < 64; off <<= 1) {
+    for (int off = lanes; !apart && off < 64; off <<= 1) {
       const float om = __shfl_xor(m, off, 64), ol = __shfl_xor(l, off, 64), mn = fmaxf(m, om), base = mn == -INFINITY ? 0.0f : mn;
       const float f = exp2_fast(m - base), w = exp2_fast(om - base);
       l = l * f + ol * w;
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a, int pie
         for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(sums[w][lane][e], f, o[e]);
       }
     }
-    if (lane < lanes && in && (!shared || wv == 0)) write_row(a, row, d, o, m, l, vdec);
+    if (mine && (apart || lane < lanes) && (!shared || wv == 0)) write_row(a, (int64_t)row.token * a.q.heads + row.head, d, o, m, l, vdec);
   }
 }
 

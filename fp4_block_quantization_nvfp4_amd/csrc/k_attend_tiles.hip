@@ -3,11 +3,14 @@
 // in k_attend_split.hip.
 //
 // Bound by the matrix cores and the vector instructions beside them.  A unit is
-// 128 rows (queries, and heads that share keys) of one sequence and shared head,
-// 32 to a wave.  Its keys pass in tiles of 64, decoded once for the workgroup
-// into shared memory while the tile before is used; scores are formed transposed
-// (keys times queries), so a lane holds one query's scores, and its weights are
-// an operand of the second product as they lie.
+// 32 rows a wave (queries, and heads that share keys) of one sequence and shared
+// head.  Its keys pass in tiles of 64, decoded once for the workgroup into shared
+// memory while the tile before is used, and read from memory two tiles ahead;
+// scores are formed transposed (keys times queries), so a lane holds one query's
+// scores, and its weights are an operand of the second product as they lie.
+//
+// Where units are few, the keys of each are shared by `parts` workgroups, which
+// leave their sums in the workspace, and a second launch joins them in order.
 #include "nvfp4_attend.hpp"
 
 namespace nvfp4 {
@@ -19,247 +22,312 @@ struct TileCount {
   }
 };
 
-#ifndef TILES_W
-#define TILES_W 4
-#define TILES_RB 1
-#define TILES_OCC 2
-#endif
 constexpr int kKeys = 64;  // keys of a tile
 
-// A lane's part of a tile as loaded: RUN elements of key tid / 4, and the same of the value.
+// A lane's part of a tile of keys, or of values, as loaded: DP / 4 elements of one slot.
 template <int DP>
 struct RawTile {
-  static constexpr int NS = DP / 32;
-  uint32_t k[NS], v[NS];
-  uint32_t ks[DP == 256 ? 2 : 1], vs[DP == 256 ? 2 : 1];
-  // page: that of the lane's key, or -1; in: the key is one of the sequence's
-  NV_DEV void load(const AttendArgs& a, int page, int h, int key, bool in, int g4) {
-    const int D = a.c.dim;
+  static constexpr int NS = DP / 32, PIECES = DP == 256 ? 2 : 1;
+  uint32_t w[NS], s[PIECES];
+  // page: that of the slot, or -1 (scores are NaN); in: the key is one of the sequence's
+  NV_DEV void load(const CacheView& c, bool keys, int page, int h, int key, bool in, int g4) {
+    const int D = c.dim;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) k[i] = v[i] = 0;
+    for (int i = 0; i < NS; ++i) w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < (DP == 256 ? 2 : 1); ++i) ks[i] = vs[i] = 0;
-    if (!in) return;
-    if (page < 0) {  // no such page: scores are NaN
-#pragma unroll
-      for (int i = 0; i < (DP == 256 ? 2 : 1); ++i) ks[i] = kNanScales;
-      return;
-    }
-    const int64_t row = (((int64_t)page * a.c.heads + h) << a.c.shift) + (key & ((1 << a.c.shift) - 1));
-    const uint8_t *kc = a.c.k + row * (D / 2), *vc = a.c.v + row * (D / 2), *kb = a.c.ks + row * (D / 16), *vb = a.c.vs + row * (D / 16);
+    for (int i = 0; i < PIECES; ++i) s[i] = in && page < 0 && keys ? kNanScales : 0;
+    if (!in || page < 0) return;
+    const int64_t row = (((int64_t)page * c.heads + h) << c.shift) + (key & ((1 << c.shift) - 1));
+    const uint8_t *codes = (keys ? c.k : c.v) + row * (D / 2), *scales = (keys ? c.ks : c.vs) + row * (D / 16);
     if constexpr (DP == 64) {
       if (16 * g4 < D) {
-        const nv_u2 x = *reinterpret_cast<const nv_u2*>(kc + 8 * g4), y = *reinterpret_cast<const nv_u2*>(vc + 8 * g4);
-        k[0] = x.x, k[1] = x.y, v[0] = y.x, v[1] = y.y;
-        ks[0] = kb[g4], vs[0] = vb[g4];
+        const nv_u2 x = *reinterpret_cast<const nv_u2*>(codes + 8 * g4);
+        w[0] = x.x, w[1] = x.y;
+        s[0] = scales[g4];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NS / 4; ++i) {
+      for (int i = 0; i < PIECES; ++i) {
         const int d = 8 * NS * g4 + 32 * i;
         if (d < D) {
-          const nv_u4 x = *reinterpret_cast<const nv_u4*>(kc + d / 2), y = *reinterpret_cast<const nv_u4*>(vc + d / 2);
+          const nv_u4 x = *reinterpret_cast<const nv_u4*>(codes + d / 2);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) k[4 * i + j] = x[j], v[4 * i + j] = y[j];
-          ks[i] = *reinterpret_cast<const uint16_t*>(kb + d / 16), vs[i] = *reinterpret_cast<const uint16_t*>(vb + d / 16);
+          for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
+          s[i] = *reinterpret_cast<const uint16_t*>(scales + d / 16);
         }
       }
     }
   }
-  // Decoded to shared memory: eight elements c of a key at c ^ key.
-  NV_DEV void store(uint8_t* K, uint8_t* V, int key, int g4) const {
+  // Decoded to shared memory, chunk by chunk.
+  NV_DEV void store(uint8_t* to, int key, int g4) const {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const int c = NS * g4 + i, at = key * DP * 2 + ((c ^ (key & 7)) << 4);
-      const nv_h2 p = scale_pair(ks[i / 4], false), q = scale_pair(vs[i / 4], false);
-      *reinterpret_cast<nv_h8*>(K + at) = fp4_to_f16(k[i], both((i & 2) ? p.y : p.x));
-      *reinterpret_cast<nv_h8*>(V + at) = fp4_to_f16(v[i], both((i & 2) ? q.y : q.x));
+      const nv_h2 p = scale_pair(s[i / 4], false);
+      *reinterpret_cast<nv_h8*>(to + key * DP * 2 + (((NS * g4 + i) ^ chunk_at(key)) << 4)) = fp4_to_f16(w[i], both((i & 2) ? p.y : p.x));
     }
   }
 };
 
-// W waves, each with RB blocks of 32 rows.
-template <int DP, int W, int RB>
-__global__ __launch_bounds__(64 * W, TILES_OCC) void k_attend_tiles(const AttendArgs a) {
+// What the join needs of a unit; parts 0: nothing to join.
+struct TileHeader {
+  int parts, m0, h, q0, n, pad[3];
+};
+// The workspace: headers, then `parts` partial results for each unit, of rows x D
+// sums, their maxima and their sums of weights.
+NV_DEV TileHeader* tile_headers(const AttendArgs& a) { return reinterpret_cast<TileHeader*>(a.part); }
+NV_DEV float* tile_part(const AttendArgs& a, int units, int parts, int rows, int unit, int i) {
+  return a.part + 8 * (int64_t)units + ((int64_t)unit * parts + i) * rows * (a.c.dim + 2);
+}
+
+// W waves of 32 rows.  parts: workgroups that share a unit's keys at most.
+template <int DP, int W>
+__global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(const AttendArgs a, int units, int parts) {
   constexpr int NQ = DP / 16, NT = DP / 32;  // steps of 16 along d; tiles of 32 of it
   constexpr int TILE = kKeys * DP * 2;       // bytes of a tile's keys, or values
-  constexpr int ROWS = 32 * RB * W;
+  constexpr int ROWS = 32 * W;
   __shared__ __align__(16) uint8_t lds[4 * TILE];
   const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
   const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
+  const int split = blockIdx.x / units, unit = blockIdx.x - split * units;
   const TileCount count{G, Hk, a.most, ROWS};
   SequenceScan<TileCount> scan(a, count);
   Sequence s{};
-  if (!scan.find(blockIdx.x, s)) return;
+  // pieces are as long for all units, so that the longest sequence has `parts` of them
+  int per = 1 << 30;
+  if (parts > 1) {
+    scan.total();
+    const int longest = (scan.longest + kKeys - 1) / kKeys, even = (longest + parts - 1) / parts;
+    per = even > kAttendLeast ? even : kAttendLeast;
+    scan.restart();
+  }
+  if (!scan.find(unit, s)) {
+    if (parts > 1 && split == 0 && threadIdx.x == 0) tile_headers(a)[unit].parts = 0;
+    return;
+  }
   // the last rows first: with a causal mask they have the most keys
-  const int u = (int)blockIdx.x - s.first, h = u % Hk, units = (int)(((int64_t)s.n * G + ROWS - 1) / ROWS);
-  const int m0 = (units - 1 - u / Hk) * ROWS;
+  const int u = unit - s.first, h = u % Hk, blocks = (int)(((int64_t)s.n * G + ROWS - 1) / ROWS);
+  const int m0 = (blocks - 1 - u / Hk) * ROWS;
+  // keys that the unit's rows see, and those that all of them do
+  const int m1 = m0 + ROWS - 1, last = m1 / G < s.n ? m1 / G : s.n - 1;
+  const int most = uniform(seen_by(a, s, last)), least = uniform(seen_by(a, s, m0 / G));
+  const int all = (most + kKeys - 1) / kKeys;
+  const int first = split * per, tiles = all - first > per ? first + per : all;
+  const bool whole = all <= per;
+  if (parts > 1 && split == 0 && threadIdx.x == 0) tile_headers(a)[unit] = {whole ? 0 : (all + per - 1) / per, m0, h, s.q0, s.n, {0, 0, 0}};
+  if (split != 0 && first >= all) return;
+
+  const int tk = (threadIdx.x & 255) >> 2, g4 = threadIdx.x & 3;
+  // Of eight waves four load and decode: the others run ahead, and a SIMD's two are out of
+  // step, one at its products while the other is not (eight, one side each: 660 -> 710 us,
+  // two prompts of 8192).
+  const bool loads = W == 4 || wv < 4;
+  auto page_at = [&](int j) {
+    const int key = j * kKeys + tk;
+    return key < s.L ? page_of(a, s, key) : 0;
+  };
+  RawTile<DP> raw[2][2];
+  auto load = [&](RawTile<DP>* r, int j, int page) {
+    const int key = j * kKeys + tk;
+    r[0].load(a.c, true, page, h, key, key < s.L, g4);
+    r[1].load(a.c, false, page, h, key, key < s.L, g4);
+  };
+  auto store = [&](const RawTile<DP>* r, int buf) {
+    uint8_t* to = lds + buf * 2 * TILE;
+    r[0].store(to, tk, g4);
+    r[1].store(to + TILE, tk, g4);
+  };
+  int page = 0;
+  if (first < tiles && loads) {
+    load(raw[0], first, page_at(first));
+    load(raw[1], first + 1, page_at(first + 1));
+    page = page_at(first + 2);
+  }
+
   const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
-  nv_h8 Q[RB][NQ];
-  float by[RB], m[RB], l[RB];
-  int limit[RB];
-  nv_f16 O[RB][NT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int row = m0 + 32 * (RB * wv + b) + col, i = row / G, head = h * G + row - i * G;
-    nv_u4 raw[NQ];
+  const int row = m0 + 32 * wv + col, i = row / G, head = h * G + row - i * G;
+  nv_h8 Q[NQ];
+  float factor;
+  {
+    nv_u4 x[NQ];
     uint32_t big = 0;
 #pragma unroll
     for (int k = 0; k < NQ; ++k) {
       const int d = 16 * k + 8 * half;
-      raw[k] = (nv_u4){0, 0, 0, 0};
-      if (i < s.n && d < D) raw[k] = *reinterpret_cast<const nv_u4*>((const uint16_t*)a.q.at + (int64_t)(s.q0 + i) * a.q.token + head * a.q.head + d);
-      big = amax_bits(raw[k], big);
+      x[k] = (nv_u4){0, 0, 0, 0};
+      if (i < s.n && d < D) x[k] = *reinterpret_cast<const nv_u4*>((const uint16_t*)a.q.at + (int64_t)(s.q0 + i) * a.q.token + head * a.q.head + d);
+      big = amax_bits(x[k], big);
     }
     const uint32_t o = (uint32_t)__shfl_xor((int)big, 32, 64);
-    const float factor = query_factor(o > big ? o : big);
+    factor = query_factor(o > big ? o : big);
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) Q[b][k] = query_to_f16(raw[k], factor);
-    by[b] = score_scale(a.scale * kLog2e / factor * kdec);
-    limit[b] = i < s.n ? seen_by(a, s, i) : 0;
-    m[b] = -INFINITY;
-    l[b] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) O[b][t][r] = 0.0f;
+    for (int k = 0; k < NQ; ++k) Q[k] = query_to_f16(x[k], factor);
   }
-  // keys that the unit's rows see, and those that all of them do
-  const int m1 = m0 + ROWS - 1, last = m1 / G < s.n ? m1 / G : s.n - 1;
-  const int most = seen_by(a, s, last), least = seen_by(a, s, m0 / G);
-  const int tiles = (most + kKeys - 1) / kKeys;
-  const bool loads = threadIdx.x < 256;
-  const int tk = (threadIdx.x & 255) >> 2, g4 = threadIdx.x & 3;
-  RawTile<DP> next;
-  int page = tk < s.L ? page_of(a, s, tk) : 0;
-  if (tiles > 0 && loads) {
-    next.load(a, page, h, tk, tk < s.L, g4);
-    page = kKeys + tk < s.L ? page_of(a, s, kKeys + tk) : 0;
-    next.store(lds, lds + TILE, tk, g4);
-  }
+  const float by = score_scale(a.scale * kLog2e / factor * kdec);
+  const int limit = i < s.n ? seen_by(a, s, i) : 0;
+  nv_f16 O[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) O[t][r] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+  if (first < tiles && loads) store(raw[0], 0);
   __syncthreads();
-  for (int j = 0; j < tiles; ++j) {
-    const uint8_t* K = lds + (j & 1) * 2 * TILE;
+
+  // tile j from buffer buf; tile j + 2 into r, from where tile j was stored; then tile j + 1 from n
+  auto tile = [&](int j, int buf, RawTile<DP>* r, const RawTile<DP>* n) {
+    const uint8_t* K = lds + buf * 2 * TILE;
     const uint8_t* V = K + TILE;
-    const int key0 = j * kKeys, nk = key0 + kKeys + tk;
-    if (j + 1 < tiles && loads) {
-      next.load(a, page, h, nk, nk < s.L, g4);
-      page = nk + kKeys < s.L ? page_of(a, s, nk + kKeys) : 0;
+    const int key0 = j * kKeys;
+    if (j + 2 < tiles && loads) {
+      load(r, j + 2, page);
+      page = page_at(j + 3);
     }
-    nv_f16 S[RB][2];
+    nv_f16 S[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[b][t][r] = 0.0f;
+      for (int e = 0; e < 16; ++e) S[t][e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < NQ; ++k) {
         const int key = 32 * t + col, c = 2 * k + half;
-        const nv_h8 A = *reinterpret_cast<const nv_h8*>(K + key * DP * 2 + ((c ^ (key & 7)) << 4));
-#pragma unroll
-        for (int b = 0; b < RB; ++b) S[b][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, Q[b][k], S[b][t], 0, 0, 0);
+        const nv_h8 A = *reinterpret_cast<const nv_h8*>(K + key * DP * 2 + ((c ^ chunk_at(key)) << 4));
+        S[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, Q[k], S[t], 0, 0, 0);
       }
     }
     if (key0 + kKeys > least) {
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (key0 + 32 * t + 8 * (r / 4) + 4 * half + r % 4 >= limit[b]) S[b][t][r] = -INFINITY;
-    }
-    nv_h8 P[RB][2][2];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      float top = -INFINITY;
+      const int hidden = limit - key0 - 4 * half;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, S[b][t][r]);
-      top = half_max(top) * by[b];
-      if (__builtin_amdgcn_ballot_w64(top > m[b] + kSlack)) {
-        const float mn = fmaxf(m[b], top), alpha = exp2_fast(m[b] - (mn == -INFINITY ? 0.0f : mn));
-        m[b] = mn;
-        l[b] *= alpha;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) O[b][t][r] *= alpha;
-      }
-      const float up = kWeightBits - (m[b] == -INFINITY ? 0.0f : m[b]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {  // sixteen keys: 4 half + 0..3, and 8 more
-          nv_u4 w;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = exp2_fast(__builtin_fmaf(S[b][t][8 * q + 2 * i], by[b], up));
-            const float y = exp2_fast(__builtin_fmaf(S[b][t][8 * q + 2 * i + 1], by[b], up));
-            l[b] += x + y;
-            w[i] = pack_f16(x, y);
-          }
-          P[b][t][q] = __builtin_bit_cast(nv_h8, w);
-        }
+        for (int e = 0; e < 16; ++e)
+          if (32 * t + 8 * (e / 4) + e % 4 >= hidden) S[t][e] = -INFINITY;
     }
+    float top = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, S[t][e]);
+    top = half_max(top) * by;
+    if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+      const float mn = fmaxf(m, top), alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
+      m = mn;
+      l *= alpha;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) O[t][e] *= alpha;
+    }
+    const float up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // sixteen keys: 4 half + 0..3, and 8 more
+        nv_u4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e], by, up));
+          const float y = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e + 1], by, up));
+          l += x + y;
+          w[e] = pack_f16(x, y);
+        }
+        const nv_h8 P = __builtin_bit_cast(nv_h8, w);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
           nv_h4 part[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int c16 = lane & 15, key = 32 * t + 16 * q + 8 * g + 4 * half + (c16 >> 2);
-            const int c = 4 * i + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1);
-            part[g] = read_turned(V + key * DP * 2 + ((c ^ (key & 7)) << 4) + 8 * (c16 & 1));
+            const int c = 4 * k + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1);
+            part[g] = read_turned(V + key * DP * 2 + ((c ^ chunk_at(key)) << 4) + 8 * (c16 & 1));
           }
-          const nv_h8 A = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-          for (int b = 0; b < RB; ++b) O[b][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, P[b][t][q], O[b][i], 0, 0, 0);
+          O[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7), P, O[k], 0, 0, 0);
         }
-    if (j + 1 < tiles && loads) {
-      uint8_t* to = lds + ((j + 1) & 1) * 2 * TILE;
-      next.store(to, to + TILE, tk, g4);
-    }
+      }
+    if (j + 1 < tiles && loads) store(n, buf ^ 1);
     __syncthreads();
+  };
+  for (int j = first; j < tiles; j += 2) {
+    tile(j, 0, raw[0], raw[1]);
+    if (j + 1 < tiles) tile(j + 1, 1, raw[1], raw[0]);
   }
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const float sum = l[b] + __shfl_xor(l[b], 32, 64);
-    const int row = m0 + 32 * (RB * wv + b) + col, i = row / G, head = h * G + row - i * G;
-    if (i >= s.n) continue;
-    const float inv = sum == 0.0f ? 0.0f : vdec / sum;
-    const int64_t out = (int64_t)(s.q0 + i) * a.q.heads + head;
+  l += __shfl_xor(l, 32, 64);
+  if (i >= s.n) return;
+  if (!whole) {
+    float* part = tile_part(a, units, parts, ROWS, unit, split);
+    const int r0 = 32 * wv + col;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int d = 32 * t + 8 * r + 4 * half;
-        if (d >= D) continue;
-        nv_u2 w;
-        w.x = pack_bf16(O[b][t][4 * r] * inv, O[b][t][4 * r + 1] * inv);
-        w.y = pack_bf16(O[b][t][4 * r + 2] * inv, O[b][t][4 * r + 3] * inv);
-        *reinterpret_cast<nv_u2*>(a.out + out * D + d) = w;
+        if (d < D) *reinterpret_cast<nv_f4*>(part + r0 * D + d) = (nv_f4){O[t][4 * r], O[t][4 * r + 1], O[t][4 * r + 2], O[t][4 * r + 3]};
       }
-    if (half == 0) a.lse[out] = sum == 0.0f ? -INFINITY : log_sum(m[b], sum);
+    if (half == 0) {
+      part[ROWS * D + r0] = m;
+      part[ROWS * (D + 1) + r0] = l;
+    }
+    return;
+  }
+  const int64_t out = (int64_t)(s.q0 + i) * a.q.heads + head;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = 32 * t + 8 * r + 4 * half;
+      if (d < D) write_row(a, out, d, (nv_f4){O[t][4 * r], O[t][4 * r + 1], O[t][4 * r + 2], O[t][4 * r + 3]}, m, l, vdec);
+    }
+}
+
+// Workgroup (unit, y) joins rows 16 y .. 16 y + 15: D / 4 lanes take four sums each.
+template <int ROWS>
+__global__ __launch_bounds__(256) void k_attend_tiles_join(const AttendArgs a, int units, int parts) {
+  const TileHeader t = tile_headers(a)[blockIdx.x];
+  if (t.parts == 0) return;
+  const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
+  const float vdec = a.c.va ? a.c.va[t.h] / 2688.0f : 1.0f;
+  for (int e = threadIdx.x; e < 4 * D; e += 256) {
+    const int r = 16 * blockIdx.y + e / (D / 4), d = e % (D / 4) * 4;
+    const int row = t.m0 + r, i = row / G, head = t.h * G + row - i * G;
+    if (i >= t.n) break;
+    float m = -INFINITY, l = 0.0f;
+    nv_f4 o = (nv_f4){0, 0, 0, 0};
+    constexpr int FLY = 4;
+    for (int p0 = 0; p0 < t.parts; p0 += FLY) {
+      float pm[FLY], pl[FLY];
+      nv_f4 x[FLY];
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        const float* part = tile_part(a, units, parts, ROWS, blockIdx.x, p0 + k < t.parts ? p0 + k : t.parts - 1);
+        pm[k] = part[ROWS * D + r];
+        pl[k] = part[ROWS * (D + 1) + r];
+        x[k] = *reinterpret_cast<const nv_f4*>(part + r * D + d);
+      }
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        if (p0 + k >= t.parts) break;
+        const float mn = fmaxf(m, pm[k]), base = mn == -INFINITY ? 0.0f : mn, f = exp2_fast(m - base), w = exp2_fast(pm[k] - base);
+        l = __builtin_fmaf(pl[k], w, l * f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(x[k][j], w, o[j] * f);
+        m = mn;
+      }
+    }
+    write_row(a, (int64_t)(t.q0 + i) * a.q.heads + head, d, o, m, l, vdec);
   }
 }
 
-template <int DP>
-static int tiles_go(const AttendArgs& a, hipStream_t st) {
-  const LayerLaunch p = plan_attend_tiles(a.T, a.B, a.q.heads, a.c.heads);
-  k_attend_tiles<DP, TILES_W, TILES_RB><<<(uint32_t)p.grid, 64 * TILES_W, 0, st>>>(a);
+template <int DP, int W>
+static int tiles_go(const AttendArgs& a, const TilesPlan& p, hipStream_t st) {
+  k_attend_tiles<DP, W><<<(uint32_t)(p.units * p.parts), 64 * W, 0, st>>>(a, (int)p.units, p.parts);
+  if (p.parts > 1) k_attend_tiles_join<32 * W><<<dim3((uint32_t)p.units, 2 * W), 256, 0, st>>>(a, (int)p.units, p.parts);
   return (int)hipGetLastError();
 }
 
 int launch_attend_tiles(const AttendArgs& a, hipStream_t st) {
-  if (a.c.dim <= 64) return tiles_go<64>(a, st);
-  if (a.c.dim <= 128) return tiles_go<128>(a, st);
-  return tiles_go<256>(a, st);
+  const TilesPlan p = tiles_plan(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
+  if (a.c.dim <= 64) return p.waves == 8 ? tiles_go<64, 8>(a, p, st) : tiles_go<64, 4>(a, p, st);
+  if (a.c.dim <= 128) return p.waves == 8 ? tiles_go<128, 8>(a, p, st) : tiles_go<128, 4>(a, p, st);
+  return tiles_go<256, 4>(a, p, st);
 }
 
 }  // namespace nvfp4

@@ -98,11 +98,23 @@ NV_DEV float quarter_sum(float v) {
   return h.x + h.y;
 }
 
+// Whether a step's scores are masked, known when compiled (a branch in the loop became
+// selections in every step).
+template <bool B>
+struct Masked {
+  static constexpr bool value = B;
+};
+
 // What a score is taken times; never zero, so that hidden scores stay -infinity.
 NV_DEV float score_scale(float v) { return v < 0x1p-120f ? 0x1p-120f : v; }
 
 // log of the sum of exp from the running maximum and the sum of weights.
 NV_DEV float log_sum(float m, float l) { return (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l))); }
+
+// Decoded keys and values in shared memory: chunk c (eight elements) of key j lies
+// at c ^ chunk_at(j): neither eight keys' same chunk (rows as an operand) nor two
+// chunks of four keys in a row (columns, turned) meet in a bank.
+NV_DEV int chunk_at(int key) { return (key & 3) << 1 | ((key >> 2) & 1); }
 
 // Of each sixteen lanes, lane 4 x + y names a quarter (four fp16) of row x; lane i
 // gets element i of the four rows.
@@ -265,6 +277,14 @@ struct PageWindow {
   }
 };
 
-NV_DEV uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
+// Four elements of row `row` of the outputs, from its sums o, maximum and sum of weights.
+NV_DEV void write_row(const AttendArgs& a, int64_t row, int d, nv_f4 o, float m, float l, float vdec) {
+  const float inv = l == 0.0f ? 0.0f : vdec / l;
+  nv_u2 w;
+  w.x = pack_bf16(o[0] * inv, o[1] * inv);
+  w.y = pack_bf16(o[2] * inv, o[3] * inv);
+  *reinterpret_cast<nv_u2*>(a.out + row * a.c.dim + d) = w;
+  if (d == 0) a.lse[row] = l == 0.0f ? -INFINITY : log_sum(m, l);
+}
 
 }  // namespace nvfp4

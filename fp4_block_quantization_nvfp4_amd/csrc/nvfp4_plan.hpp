@@ -274,6 +274,7 @@ enum AttentionKernel {
   PLAN_ATTEND_SPLIT = 4,
   PLAN_ATTEND_JOIN = 5,
   PLAN_ATTEND_TILES = 6,
+  PLAN_ATTEND_TILES_JOIN = 7,
 };
 
 // Norm and rotation: LN lanes to a row, sixteen elements each, 64 / LN rows a
@@ -305,14 +306,15 @@ inline LayerLaunch plan_read_cache(int64_t T, int64_t heads, int64_t D) {
 }
 
 // Attention.  Rows: queries times the heads that share keys.  The split kernel takes sequences of up
-// to kAttendFew rows, and all where no sequence can have more; the tiled one the others.
-constexpr int kAttendFew = 32;
+// to kAttendFew rows, which would not fill a unit of the tiled one, and all where no sequence can
+// have more.  Measured, us, split (tiled), 32 heads, 8 of keys, D = 128: 32 sequences of 48 rows and up to
+// 4096 keys 60 (90), of 96 rows 85 (98), 8 of 128 rows and up to 2048 keys 38 (32).
+constexpr int kAttendFew = 128;
 // Workgroups of the split kernel at most: what runs at a time.  Of heads up to 128 the registers of
 // two waves on a SIMD (three: 64 sequences of up to 8192 keys 88 -> 105 us, codes spilled), of
 // larger ones of one (32 of head size 256: two 67 us, one 61).
-constexpr int64_t kAttendPieces = 512;  // workgroups of the split kernel at most
-constexpr int kAttendTile = 64;          // keys of a tile of its work
-constexpr int kAttendRows = 128;         // rows of a unit of the tiled kernel
+constexpr int64_t kAttendPieces = 512;
+constexpr int kAttendTile = 64;  // keys of a tile of its work
 
 inline int attend_kernels(int64_t T, int64_t Hq, int64_t Hk, bool ends) { return ends && T * (Hq / Hk) > kAttendFew ? 3 : 1; }
 // Tiles of the split kernel at most: with units of sixteen rows, of keys that the table's rows name.
@@ -332,12 +334,44 @@ inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk
   if (keys <= kAttendTile) return {0, 0, 0, 0};  // no unit has two tiles
   return {PLAN_ATTEND_JOIN, attend_pieces(T, B, Hq, Hk, D, keys), 4, 256};
 }
-inline size_t attend_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
-  return keys <= kAttendTile ? 0 : (size_t)(4 * attend_pieces(T, B, Hq, Hk, D, keys) * (2 * (16 * D + 32) * 4 + 32));
+// Tiled kernel.  Units of 32 rows a wave at most: each sequence adds less than one to T * G / rows.
+// Eight waves share the decoding of a tile among twice the rows of four, where there are
+// enough units and heads over 64 (two prompts of 8192, 32 heads of 128: 705 -> 655 us; 4 of 4096, 16 heads
+// of 64: 120 -> 139).
+// parts: workgroups that share a unit's keys, in pieces of kAttendLeast tiles of 64 or more, where
+// units alone would not fill the chip's 512 places twice (512 queries behind 32768 keys: 870 us
+// whole, 350 in parts; pieces of four tiles instead of eight, which a piece's start and sums
+// cost more than: 43 -> 50 us, 7 sequences of up to 301 queries and 1999 keys).
+constexpr int kAttendLeast = 8;
+struct TilesPlan {
+  int waves, parts;
+  int64_t units;
+};
+inline TilesPlan tiles_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  const int64_t rows = T * (Hq / Hk);
+  const int waves = D > 64 && D <= 128 && ceil_div(rows, 256) * Hk >= 256 ? 8 : 4;
+  const int64_t units = (ceil_div(rows, 32 * waves) + B) * Hk;
+  int64_t parts = 1024 / units, most = ceil_div(keys, 64 * kAttendLeast);
+  if (parts > most) parts = most;
+  return {waves, (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts), units};
 }
-// Units of the tiled kernel at most: each sequence adds less than one to T * G / rows.
-inline LayerLaunch plan_attend_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk) {
-  return {PLAN_ATTEND_TILES, (ceil_div(T * (Hq / Hk), kAttendRows) + B) * Hk, 1, 256};
+inline LayerLaunch plan_attend_tiles(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
+  return {PLAN_ATTEND_TILES, p.units * p.parts, 1, 64 * p.waves};
+}
+inline LayerLaunch plan_attend_tiles_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
+  if (p.parts == 1) return {0, 0, 0, 0};
+  return {PLAN_ATTEND_TILES_JOIN, p.units, 2 * p.waves, 256};
+}
+// Both kernels' workspaces, one after the other's: they run one after the other.
+inline size_t attend_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys, bool ends) {
+  size_t split = keys <= kAttendTile ? 0 : (size_t)(4 * attend_pieces(T, B, Hq, Hk, D, keys) * (2 * (16 * D + 32) * 4 + 32)), tiles = 0;
+  if (attend_kernels(T, Hq, Hk, ends) & 2) {
+    const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
+    if (p.parts > 1) tiles = (size_t)(p.units * (32 + (int64_t)p.parts * 32 * p.waves * (D + 2) * 4));
+  }
+  return split > tiles ? split : tiles;
 }
 
 }  // namespace nvfp4

@@ -486,7 +486,7 @@ nvfp4_status nvfp4_read_cache(const nvfp4_cache* cache, const int32_t* slots, in
  * least 0.  A query that sees a key whose page is not in the cache, and every one
  * of a sequence longer than width * page_size, gets NaN.  width >= 1, scale >
  * 0.  Sums have a fixed order.  Further limits (NVFP4_E_RANGE): B <= 2^20, B * heads
- * <= 2^22, width * page_size <= 2^30, and B * max(2, ceil(G / 16)) * heads *
+ * <= 2^22, width * page_size <= 2^30, and B * max(8, ceil(G / 16)) * heads *
  * ceil(width * page_size / 64) + ceil(T * G / 16) * heads < 2^31, G = q->heads /
  * heads.  workspace: at least
  * nvfp4_cache_attention_workspace_bytes (0: may be NULL), 16-byte aligned.
@@ -563,8 +563,8 @@ nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t 
  *   entry    0 norm_rope, 1 its backward, 2 norm_rope_write, 3 write_cache, 4
  *            read_cache, 5 cache_attention with ends, 6 without.  Hq, Hk: heads of
  *            queries and of keys; keys: width * page_size.
- *   plan     HOST pointer to twelve int64: {kernel id, workgroups along x, along
- *            y, lanes per workgroup} of up to three launches (zeros: none).
+ *   plan     HOST pointer to sixteen int64: {kernel id, workgroups along x, along
+ *            y, lanes per workgroup} of up to four launches (zeros: none).
  */
 nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
                                            int64_t keys, int64_t* plan);

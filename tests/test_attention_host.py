@@ -154,13 +154,13 @@ def test_cpu_tensors_are_refused():
 
 # ----------------------------------------------------------------- launches
 
-ROPE_K, ROPE_BWD, ROPE_SUM, READ, SPLIT, JOIN, TILES = range(7)
+ROPE_K, ROPE_BWD, ROPE_SUM, READ, SPLIT, JOIN, TILES, TILES_JOIN = range(8)
 
 
 def plan(entry, T, Hq=4, Hk=2, D=64, B=1, keys=16):
-    out = (ctypes.c_int64 * 12)()
+    out = (ctypes.c_int64 * 16)()
     st = L.lib().nvfp4_selftest_attention_plan(entry, T, Hq, Hk, D, B, keys, out)
-    return st, [list(out[4 * i:4 * i + 4]) for i in range(3)]
+    return st, [list(out[4 * i:4 * i + 4]) for i in range(4)]
 
 
 def ceil(a, b):
@@ -201,16 +201,22 @@ def test_launches_stay_in_the_limits():
         if entry == 4:
             assert first[1] * 256 >= T * Hk * (D // 16) and first[2] == 2
         if entry >= 5:
-            c = cache(heads=Hk, dim=D)
-            G = Hq // Hk
+            split, join, tiles, tiles_join = launches
+            c, G = cache(heads=Hk, dim=D), Hq // Hk
             need = L.lib().nvfp4_cache_attention_workspace_bytes(T, Hq, ref(c), B, keys // 16)
-            assert (launches[1][1] > 0) == (need > 0) == (keys > 64)
-            assert launches[1][1] in (0, first[1]) and need in (0, 4 * first[1] * (2 * (16 * D + 32) * 4 + 32))
-            if launches[2][1]:  # units of any split of T queries over B sequences and those of none
-                assert entry == 5 and launches[2][1] >= (ceil(T * G, 128) + B) * Hk
+            assert (join[1] > 0) == (keys > 64) and join[1] in (0, split[1])
+            assert need >= join[1] * 4 * (2 * (16 * D + 32) * 4 + 32)
+            if tiles[1]:  # units of any split of T queries over B sequences and those of none, each in as many parts
+                rows = tiles[3] // 2
+                units = (ceil(T * G, rows) + B) * Hk
+                assert entry == 5 and rows in (128, 256) and tiles[1] % units == 0
+                parts = tiles[1] // units
+                assert 1 <= parts <= 16 and (tiles_join[1] == units and tiles_join[2] * 16 == rows if parts > 1 else tiles_join[1] == 0)
+                assert parts == 1 or need >= units * (32 + parts * rows * (D + 2) * 4)
+                assert parts == 1 or units * parts <= 1024
             else:
-                assert entry == 6 or T * G <= 32
-    assert set(got) == set(range(7)) and min(got.values()) > 20
+                assert entry == 6 or T * G <= 128
+    assert set(got) == set(range(8)) and min(got.values()) > 20
 
 
 def test_plan_refusals():

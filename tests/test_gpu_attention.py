@@ -401,6 +401,16 @@ def test_long_sequences_are_split(D):
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("D,n,L", [(96, [300, 129], [300, 700]), (128, [513], [513]), (64, [300], [900]), (256, [140, 190], [140, 900])])
+def test_many_heads(D, n, L):
+    """Enough units for workgroups of eight waves, which heads over 64 take."""
+    g = gen(D)
+    table, pages = tables(g, L, 64)
+    c = filled(g, pages, 64, 128 if D < 256 else 16, D)
+    poison(c, table, L)
+    check_attention(randn(g, sum(n), 128 if D < 256 else 16, D).cuda(), c, table, L, torch.cumsum(torch.tensor(n), 0).tolist(), True)
+
+
 def test_many_sequences():
     """More than a wave's 64 at a time, each with a few keys."""
     g = gen(9)
