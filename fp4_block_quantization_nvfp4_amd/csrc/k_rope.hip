@@ -28,29 +28,36 @@ struct SinCos {
   double s, c;
 };
 
+// A constant in a scalar, made where it is used: kept in vector registers over the
+// loop, those of the series cost 40 of them.
+NV_DEV double scalar(double v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
 NV_DEV SinCos sincos64(double a) {
-  const double n = __builtin_rint(a * 0x1.45f306dc9c883p-1);  // 2 / pi
-  double r = __builtin_fma(-n, 0x1.921fb54442d18p+0, a);       // pi / 2, the first 53 bits: the product's own bits are kept
-  r = __builtin_fma(-n, 0x1.1a62633145c07p-54, r);              // and the next 53
+  const double n = __builtin_rint(a * scalar(0x1.45f306dc9c883p-1));  // 2 / pi
+  double r = __builtin_fma(-n, scalar(0x1.921fb54442d18p+0), a);       // pi / 2, the first 53 bits: the product's own bits are kept
+  r = __builtin_fma(-n, scalar(0x1.1a62633145c07p-54), r);              // and the next 53
   const double q = r * r;
   // Taylor's series on |r| <= pi / 4: the first term left out is below 5e-17 (sine), 3e-18 (cosine)
-  double s = 1.0 / 355687428096000.0;
-  s = __builtin_fma(s, q, -1.0 / 1307674368000.0);
-  s = __builtin_fma(s, q, 1.0 / 6227020800.0);
-  s = __builtin_fma(s, q, -1.0 / 39916800.0);
-  s = __builtin_fma(s, q, 1.0 / 362880.0);
-  s = __builtin_fma(s, q, -1.0 / 5040.0);
-  s = __builtin_fma(s, q, 1.0 / 120.0);
-  s = __builtin_fma(s, q, -1.0 / 6.0);
+  double s = scalar(1.0 / 355687428096000.0);
+  s = __builtin_fma(s, q, scalar(-1.0 / 1307674368000.0));
+  s = __builtin_fma(s, q, scalar(1.0 / 6227020800.0));
+  s = __builtin_fma(s, q, scalar(-1.0 / 39916800.0));
+  s = __builtin_fma(s, q, scalar(1.0 / 362880.0));
+  s = __builtin_fma(s, q, scalar(-1.0 / 5040.0));
+  s = __builtin_fma(s, q, scalar(1.0 / 120.0));
+  s = __builtin_fma(s, q, scalar(-1.0 / 6.0));
   s = __builtin_fma(s * q, r, r);
-  double c = 1.0 / 20922789888000.0;
-  c = __builtin_fma(c, q, -1.0 / 87178291200.0);
-  c = __builtin_fma(c, q, 1.0 / 479001600.0);
-  c = __builtin_fma(c, q, -1.0 / 3628800.0);
-  c = __builtin_fma(c, q, 1.0 / 40320.0);
-  c = __builtin_fma(c, q, -1.0 / 720.0);
-  c = __builtin_fma(c, q, 1.0 / 24.0);
-  c = __builtin_fma(c, q, -0.5);
+  double c = scalar(1.0 / 20922789888000.0);
+  c = __builtin_fma(c, q, scalar(-1.0 / 87178291200.0));
+  c = __builtin_fma(c, q, scalar(1.0 / 479001600.0));
+  c = __builtin_fma(c, q, scalar(-1.0 / 3628800.0));
+  c = __builtin_fma(c, q, scalar(1.0 / 40320.0));
+  c = __builtin_fma(c, q, scalar(-1.0 / 720.0));
+  c = __builtin_fma(c, q, scalar(1.0 / 24.0));
+  c = __builtin_fma(c, q, scalar(-0.5));
   c = __builtin_fma(c, q, 1.0);
   const int quarter = (int)(n - 4.0 * __builtin_floor(n * 0.25));  // 0..3
   const double x = quarter & 1 ? c : s, y = quarter & 1 ? s : c;
@@ -74,14 +81,6 @@ NV_DEV V row_sum(V v) {
   return v;
 }
 
-NV_DEV void load8(const uint16_t* p, float x[8]) {
-  const nv_u4 w = *reinterpret_cast<const nv_u4*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bits2f(w[i] << 16);
-    x[2 * i + 1] = bits2f(w[i] & 0xFFFF0000u);
-  }
-}
 NV_DEV void load8(const float* p, float x[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -100,6 +99,37 @@ NV_DEV void store8(float* p, const float x[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) reinterpret_cast<nv_f4*>(p)[i] = (nv_f4){x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
 }
+
+// Two runs of eight elements of a row as loaded, on their way while others are used.
+template <typename T>
+struct RawRuns {
+  static constexpr int N = sizeof(T) / 2;  // 16-byte words of a run
+  nv_u4 w[2 * N];
+  NV_DEV void load(bool has, const T* row, int e0, int e1) {
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) w[i] = (nv_u4){0, 0, 0, 0};
+    if (has) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        w[i] = reinterpret_cast<const nv_u4*>(row + e0)[i];
+        w[N + i] = reinterpret_cast<const nv_u4*>(row + e1)[i];
+      }
+    }
+  }
+  NV_DEV void values(float x[16]) const {
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (N == 1) {
+          x[8 * i + 2 * j] = bits2f(w[i][j] << 16);
+          x[8 * i + 2 * j + 1] = bits2f(w[i][j] & 0xFFFF0000u);
+        } else {
+          x[4 * i + j] = bits2f(w[i][j]);
+        }
+      }
+  }
+};
 
 // The value that T holds for 64-bit v: rounded to fp32, and from there to bf16 as
 // torch converts them.  (A value within 2^-24 of the middle between two bf16 may
@@ -160,8 +190,18 @@ NV_DEV void angles(const RopeArgs& a, int t, int lane, bool turn, SinCos* lds, V
   __builtin_amdgcn_wave_barrier();
 }
 
+// A lane group's row of a token: of which kind, of which head, where its runs lie.
+struct Row {
+  bool is_q, is_v, has;
+  int h, e0, e1;
+};
+
+// The next row is on its way while one is used (16384 tokens to the cache, 8 heads of
+// 128: 29 -> 25 us; 8192 with norm and rotation: 60 -> 50).  Of 16-bit rows that go to
+// the outputs, registers for four waves on a SIMD (8192 tokens, 40 heads of 128: 36.5 ->
+// 34.3 us; 32-bit ones then spill: 21 -> 26 at 20 heads of 64).
 template <typename T, int LN, bool INTER, bool CACHE>
-__global__ __launch_bounds__(256) void k_norm_rope(const RopeArgs a, int chunks, int per) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_rope(const RopeArgs a, int chunks, int per) {
   constexpr int RW = 64 / LN;
   __shared__ SinCos lds[4][8 * LN];
   const int lane = threadIdx.x & 63, p = lane % LN;
@@ -172,22 +212,30 @@ __global__ __launch_bounds__(256) void k_norm_rope(const RopeArgs a, int chunks,
     const int first = (int)(u - t * chunks) * per * RW;
     const int slot = CACHE ? a.slots[t] : 0;
     const bool kept = !CACHE || slot_ok(a.c, slot);
+    const int stop = first + per * RW < rows ? first + per * RW : rows;
+    auto row_of = [&](int r0) {
+      Row o;
+      const int row = r0 + lane / LN;
+      o.is_q = row < Hq, o.is_v = CACHE && row >= Hq + Hk, o.has = row < stop && at.in && (o.is_q || kept);
+      o.h = o.is_q ? row : o.is_v ? row - Hq - Hk : row - Hq;
+      o.e0 = o.is_v ? 16 * p : at.e0, o.e1 = o.is_v ? 16 * p + 8 : at.e1;
+      return o;
+    };
+    auto fetch = [&](const Row& o, RawRuns<T>& raw) {
+      const HeadsView& view = o.is_q ? a.q : o.is_v ? a.v : a.k;
+      raw.load(o.has, (const T*)view.at + t * view.token + o.h * view.head, o.e0, o.e1);
+    };
+    RawRuns<T> next;
+    fetch(row_of(first), next);
     double c[8], s[8];
     if (a.R) angles<LN>(a, (int)t, lane, at.turn, lds[threadIdx.x >> 6], c, s);
-    for (int r0 = first; r0 < rows && r0 < first + per * RW; r0 += RW) {
-      const int row = r0 + lane / LN;
-      const bool is_q = row < Hq, is_v = CACHE && row >= Hq + Hk, has = row < rows && at.in && (is_q || kept);
-      const int h = is_q ? row : is_v ? row - Hq - Hk : row - Hq;
-      const HeadsView& view = is_q ? a.q : is_v ? a.v : a.k;
-      const int e0 = is_v ? 16 * p : at.e0, e1 = is_v ? 16 * p + 8 : at.e1;
+    for (int r0 = first; r0 < stop; r0 += RW) {
+      const Row row = row_of(r0);
+      const bool is_q = row.is_q, is_v = row.is_v, has = row.has;
+      const int h = row.h, e0 = row.e0, e1 = row.e1, heads = is_q ? Hq : Hk;
       float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-      if (has) {
-        const T* src = (const T*)view.at + t * view.token + h * view.head;
-        load8(src + e0, x);
-        load8(src + e1, x + 8);
-      }
+      next.values(x);
+      if (r0 + RW < stop) fetch(row_of(r0 + RW), next);
       const float* w = is_q ? a.qw : a.kw;
       float o[16];
       if (w != nullptr || a.R) {  // otherwise the rows are taken as they are
@@ -215,7 +263,7 @@ __global__ __launch_bounds__(256) void k_norm_rope(const RopeArgs a, int chunks,
         for (int i = 0; i < 16; ++i) o[i] = x[i];
       }
       if (has && (is_q || !CACHE)) {
-        T* dst = (T*)(is_q ? a.q_out : a.k_out) + (t * view.heads + h) * a.D;
+        T* dst = (T*)(is_q ? a.q_out : a.k_out) + (t * heads + h) * a.D;
         store8(dst + e0, o);
         store8(dst + e1, o + 8);
       }
@@ -268,22 +316,21 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(const RopeArgs a, const H
       const HeadsView &dz = kind ? dk : dq, &view = kind ? a.k : a.q;
       const float* w = kind ? a.kw : a.qw;
       T* dst = (T*)(kind ? a.k_out : a.q_out);
+      auto fetch = [&](int h0, RawRuns<T>& g, RawRuns<T>& y) {
+        const int h = h0 + lane / LN;
+        const bool has = h < view.heads && at.in;
+        g.load(has, (const T*)dz.at + t * dz.token + h * dz.head, at.e0, at.e1);
+        y.load(has && w, (const T*)view.at + t * view.token + h * view.head, at.e0, at.e1);
+      };
+      RawRuns<T> gn, yn;
+      fetch(0, gn, yn);
       for (int h0 = 0; h0 < view.heads; h0 += RW) {
         const int h = h0 + lane / LN;
         const bool has = h < view.heads && at.in;
         float d[16], x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[i] = x[i] = 0.0f;
-        if (has) {
-          const T* src = (const T*)dz.at + t * dz.token + h * dz.head;
-          load8(src + at.e0, d);
-          load8(src + at.e1, d + 8);
-          if (w) {
-            const T* row = (const T*)view.at + t * view.token + h * view.head;
-            load8(row + at.e0, x);
-            load8(row + at.e1, x + 8);
-          }
-        }
+        gn.values(d);
+        yn.values(x);
+        if (h0 + RW < view.heads) fetch(h0 + RW, gn, yn);
         if (a.R && at.turn) rotate<INTER>(d, c, s, true);
         if (w) {
           float f[16];
