@@ -245,9 +245,9 @@ nvfp4_status nvfp4_cache_attention(const nvfp4_heads* q, int64_t T, const nvfp4_
       !aligned(workspace, 16))
     return NVFP4_E_ALIGN;
   const int which = nvfp4::attend_kernels(T, q->heads, cache->heads, ends != nullptr);
-  const nvfp4::AttendArgs a = {view(q), view(cache), table, lens, ends, (uint16_t*)out, lse, (float*)workspace, scale,
+  const nvfp4::AttendArgs a = {view(q), view(cache), table, lens, ends, (uint16_t*)out, lse, nullptr, nullptr, scale,
                                (int)T, (int)B, (int)width, causal != 0, which == 3 ? nvfp4::kAttendFew : INT_MAX};
-  return hip_status(nvfp4::launch_attend(a, which, stream));
+  return hip_status(nvfp4::launch_attend(a, which, workspace, stream));
 }
 
 nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
@@ -267,11 +267,9 @@ nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int
     if (entry >= 5) {
       if (nvfp4::attend_split_tiles(T, B, Hq, Hk, keys) >= int64_t(1) << 31) return NVFP4_E_RANGE;
       p[0] = nvfp4::plan_attend_split(T, B, Hq, Hk, D, keys);
-      p[1] = nvfp4::plan_attend_join(T, B, Hq, Hk, D, keys);
-      if (nvfp4::attend_kernels(T, Hq, Hk, entry == 5) & 2) {
-        p[2] = nvfp4::plan_attend_tiles(T, B, Hq, Hk, D, keys);
-        p[3] = nvfp4::plan_attend_tiles_join(T, B, Hq, Hk, D, keys);
-      }
+      const int which = nvfp4::attend_kernels(T, Hq, Hk, entry == 5);
+      if (which & 2) p[1] = nvfp4::plan_attend_tiles(T, B, Hq, Hk, D, keys);
+      p[2] = nvfp4::plan_attend_join(T, B, Hq, Hk, D, keys, which);
     }
   }
   for (int i = 0; i < 4; ++i) {

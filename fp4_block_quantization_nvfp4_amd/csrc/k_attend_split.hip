@@ -29,14 +29,6 @@ struct SplitCount {
 
 NV_DEV int min_of(int64_t a, int b) { return a < b ? (int)a : b; }
 
-// What the join needs of a unit whose first part is this piece's; parts 0: no unit.
-// The parts: `head` pieces from here on, then one of each of `middle` workgroups,
-// then the others from the first piece of workgroup w1 on.  (The join scanned the
-// sequences itself before: 10 to 27 us.)
-struct JoinHeader {
-  int parts, head, middle, w1, unit, q0, n, shared;
-};
-
 // The pieces: the waves take as many tiles each, and a unit lies in at most
 // kMostParts pieces (the join takes them one after the other).
 constexpr int kMostParts = 512;
@@ -58,21 +50,6 @@ struct Pieces {
     return {head + middle + tail, head, middle, w1, unit, q.q0, q.n, one ? 1 : 0};
   }
 };
-
-// A partial result: sixteen rows of D sums, then their maxima, then their sums of weights.
-NV_DEV int64_t part_size(int D) { return 16 * (int64_t)D + 32; }
-// The workspace: two partial results for each piece (of a unit that began before it,
-// and of one that it begins), then the headers.
-NV_DEV JoinHeader* headers(const AttendArgs& a, int D, int pieces) { return reinterpret_cast<JoinHeader*>(a.part + 2 * (int64_t)pieces * part_size(D)); }
-
-// Sixteen rows of unit `unit` of sequence s: row r is query r / G, head r % G of the unit's shared head.
-struct UnitRow {
-  int token, head;  // token -1: no such row
-};
-NV_DEV UnitRow unit_row(const Sequence& s, int G, int Hk, int unit, int r) {
-  const int h = unit % Hk, m = unit / Hk * 16 + r, i = m / G;
-  return {i < s.n ? s.q0 + i : -1, h * G + m - i * G};
-}
 
 template <int DP>
 struct SplitShape {
@@ -360,114 +337,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
   }
 }
 
-// A wave joins rows y, y + 4, .. (y: grid y) of the unit that begins in its piece
-// and goes on in the next ones; of a unit that workgroups share, all four waves of
-// its first do.  D / 4 lanes take four sums each, groups of them every so many'th
-// part, four parts in flight at a time.
-__global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a, int pieces) {
-  constexpr int FLY = 4;
-  __shared__ nv_f4 sums[4][64];
-  __shared__ float stat[2][4];
-  const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk, lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
-  const JoinHeader* all = headers(a, D, pieces) + 4 * blockIdx.x;
-  const bool shared = all[0].shared != 0;
-  const JoinHeader j = all[shared ? 0 : wv];
-  if (j.parts == 0) return;
-  const int i = 4 * blockIdx.x + (shared ? 0 : wv);
-  const Sequence q{0, j.q0, j.n, 0, 0, 0};
-  const float vdec = a.c.va ? a.c.va[j.unit % Hk] / 2688.0f : 1.0f;
-  const int lanes = D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32 : 64, groups = 64 / lanes * (shared ? 4 : 1);
-  const int g = lane / lanes * (shared ? 4 : 1) + (shared ? wv : 0), d = lane % lanes * 4;
-  const bool in = d < D;
-  // few parts of many rows: the groups take rows of their own
-  const bool apart = !shared && j.parts <= 2 * FLY && unit_row(q, G, Hk, j.unit, 4).token >= 0;
-  const int first = apart ? 0 : g, step = apart ? 1 : groups;
-  for (int r0 = blockIdx.y; r0 < 16; r0 += apart ? 4 * groups : 4) {
-    if (unit_row(q, G, Hk, j.unit, r0).token < 0) break;
-    const int r = apart ? r0 + 4 * g : r0;
-    const UnitRow row = unit_row(q, G, Hk, j.unit, r);
-    const bool mine = in && r < 16 && row.token >= 0;
-    float m = -INFINITY, l = 0.0f;
-    nv_f4 o = (nv_f4){0, 0, 0, 0};
-    for (int v0 = 0; v0 < j.parts; v0 += FLY * step) {
-      float pm[FLY], pl[FLY];
-      nv_f4 x[FLY];
-#pragma unroll
-      for (int k = 0; k < FLY; ++k) {
-        const int v = v0 + k * step + first;
-        const int p = v < j.head ? i + v : v < j.head + j.middle ? 4 * (i / 4 + 1 + v - j.head) : 4 * j.w1 + v - j.head - j.middle;
-        pm[k] = -INFINITY;
-        pl[k] = 0.0f;
-        x[k] = (nv_f4){0, 0, 0, 0};
-        if (v < j.parts && mine) {
-          const float* part = a.part + (2 * (int64_t)p + (p == i ? 1 : 0)) * part_size(D);
-          pm[k] = part[16 * D + r];
-          pl[k] = part[16 * D + 16 + r];
-          x[k] = *reinterpret_cast<const nv_f4*>(part + r * D + d);
-        }
-      }
-      float mn = m;
-#pragma unroll
-      for (int k = 0; k < FLY; ++k) mn = fmaxf(mn, pm[k]);
-      const float base = mn == -INFINITY ? 0.0f : mn, f = exp2_fast(m - base);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= f;
-#pragma unroll
-      for (int k = 0; k < FLY; ++k) {
-        const float w = exp2_fast(pm[k] - base);
-        l = __builtin_fmaf(pl[k], w, l);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(x[k][e], w, o[e]);
-      }
-      m = mn;
-    }
-    // the groups' sums, in pairs, then the waves'
-    for (int off = lanes; !apart && off < 64; off <<= 1) {
-      const float om = __shfl_xor(m, off, 64), ol = __shfl_xor(l, off, 64), mn = fmaxf(m, om), base = mn == -INFINITY ? 0.0f : mn;
-      const float f = exp2_fast(m - base), w = exp2_fast(om - base);
-      l = l * f + ol * w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * f + __shfl_xor(o[e], off, 64) * w;
-      m = mn;
-    }
-    if (shared) {
-      __syncthreads();
-      sums[wv][lane] = o;
-      if (lane == 0) {
-        stat[0][wv] = m;
-        stat[1][wv] = l;
-      }
-      __syncthreads();
-      m = fmaxf(fmaxf(stat[0][0], stat[0][1]), fmaxf(stat[0][2], stat[0][3]));
-      l = 0.0f;
-      o = (nv_f4){0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = exp2_fast(stat[0][w] - (m == -INFINITY ? 0.0f : m));
-        l = __builtin_fmaf(stat[1][w], f, l);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(sums[w][lane][e], f, o[e]);
-      }
-    }
-    if (mine && (apart || lane < lanes) && (!shared || wv == 0)) write_row(a, (int64_t)row.token * a.q.heads + row.head, d, o, m, l, vdec);
-  }
-}
-
-int launch_attend_tiles(const AttendArgs& a, hipStream_t st);
-
-int launch_attend(const AttendArgs& a, int which, void* stream) {
-  hipStream_t st = (hipStream_t)stream;
-  if (which & 1) {
-    const LayerLaunch p = plan_attend_split(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
-    if (a.c.dim <= 64) k_attend_split<64><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
-    else if (a.c.dim <= 128) k_attend_split<128><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
-    else k_attend_split<256><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
-    const LayerLaunch j = plan_attend_join(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
-    if (j.grid) k_attend_join<<<dim3((uint32_t)j.grid, (uint32_t)j.y), j.block, 0, st>>>(a, 4 * (int)p.grid);
-  }
-  if (which & 2) return launch_attend_tiles(a, st);
-  return (int)hipGetLastError();
+void launch_attend_split(const AttendArgs& a, hipStream_t st) {
+  const LayerLaunch p = plan_attend_split(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
+  if (a.c.dim <= 64) k_attend_split<64><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
+  else if (a.c.dim <= 128) k_attend_split<128><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
+  else k_attend_split<256><<<(uint32_t)p.grid, p.block, 0, st>>>(a);
 }
 
 }  // namespace nvfp4

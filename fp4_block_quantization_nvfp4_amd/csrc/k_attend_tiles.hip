@@ -68,17 +68,6 @@ struct RawTile {
   }
 };
 
-// What the join needs of a unit; parts 0: nothing to join.
-struct TileHeader {
-  int parts, m0, h, q0, n, pad[3];
-};
-// The workspace: headers, then `parts` partial results for each unit, of rows x D
-// sums, their maxima and their sums of weights.
-NV_DEV TileHeader* tile_headers(const AttendArgs& a) { return reinterpret_cast<TileHeader*>(a.part); }
-NV_DEV float* tile_part(const AttendArgs& a, int units, int parts, int rows, int unit, int i) {
-  return a.part + 8 * (int64_t)units + ((int64_t)unit * parts + i) * rows * (a.c.dim + 2);
-}
-
 // W waves of 32 rows.  parts: workgroups that share a unit's keys at most.
 template <int DP, int W>
 __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(const AttendArgs a, int units, int parts) {
@@ -182,18 +171,22 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
       load(r, j + 2, page);
       page = page_at(j + 3);
     }
+    // The two halves of the tile in turn: a product waits for the one before it only
+    // every second time (two prompts of 8192: 660 us one half after the other, 652 so; heads of
+    // 256: 501 and 478).
     nv_f16 S[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 16; ++e) S[t][e] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) {
+    for (int k = 0; k < NQ; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
         const int key = 32 * t + col, c = 2 * k + half;
         const nv_h8 A = *reinterpret_cast<const nv_h8*>(K + key * DP * 2 + ((c ^ chunk_at(key)) << 4));
         S[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A, Q[k], S[t], 0, 0, 0);
       }
-    }
     if (key0 + kKeys > least) {
       const int hidden = limit - key0 - 4 * half;
 #pragma unroll
@@ -278,56 +271,13 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
     }
 }
 
-// Workgroup (unit, y) joins rows 16 y .. 16 y + 15: D / 4 lanes take four sums each.
-template <int ROWS>
-__global__ __launch_bounds__(256) void k_attend_tiles_join(const AttendArgs a, int units, int parts) {
-  const TileHeader t = tile_headers(a)[blockIdx.x];
-  if (t.parts == 0) return;
-  const int D = a.c.dim, Hk = a.c.heads, G = a.q.heads / Hk;
-  const float vdec = a.c.va ? a.c.va[t.h] / 2688.0f : 1.0f;
-  for (int e = threadIdx.x; e < 4 * D; e += 256) {
-    const int r = 16 * blockIdx.y + e / (D / 4), d = e % (D / 4) * 4;
-    const int row = t.m0 + r, i = row / G, head = t.h * G + row - i * G;
-    if (i >= t.n) break;
-    float m = -INFINITY, l = 0.0f;
-    nv_f4 o = (nv_f4){0, 0, 0, 0};
-    constexpr int FLY = 4;
-    for (int p0 = 0; p0 < t.parts; p0 += FLY) {
-      float pm[FLY], pl[FLY];
-      nv_f4 x[FLY];
-#pragma unroll
-      for (int k = 0; k < FLY; ++k) {
-        const float* part = tile_part(a, units, parts, ROWS, blockIdx.x, p0 + k < t.parts ? p0 + k : t.parts - 1);
-        pm[k] = part[ROWS * D + r];
-        pl[k] = part[ROWS * (D + 1) + r];
-        x[k] = *reinterpret_cast<const nv_f4*>(part + r * D + d);
-      }
-#pragma unroll
-      for (int k = 0; k < FLY; ++k) {
-        if (p0 + k >= t.parts) break;
-        const float mn = fmaxf(m, pm[k]), base = mn == -INFINITY ? 0.0f : mn, f = exp2_fast(m - base), w = exp2_fast(pm[k] - base);
-        l = __builtin_fmaf(pl[k], w, l * f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(x[k][j], w, o[j] * f);
-        m = mn;
-      }
-    }
-    write_row(a, (int64_t)(t.q0 + i) * a.q.heads + head, d, o, m, l, vdec);
-  }
-}
-
-template <int DP, int W>
-static int tiles_go(const AttendArgs& a, const TilesPlan& p, hipStream_t st) {
-  k_attend_tiles<DP, W><<<(uint32_t)(p.units * p.parts), 64 * W, 0, st>>>(a, (int)p.units, p.parts);
-  if (p.parts > 1) k_attend_tiles_join<32 * W><<<dim3((uint32_t)p.units, 2 * W), 256, 0, st>>>(a, (int)p.units, p.parts);
-  return (int)hipGetLastError();
-}
-
-int launch_attend_tiles(const AttendArgs& a, hipStream_t st) {
-  const TilesPlan p = tiles_plan(a.T, a.B, a.q.heads, a.c.heads, a.c.dim, (int64_t)a.width << a.c.shift);
-  if (a.c.dim <= 64) return p.waves == 8 ? tiles_go<64, 8>(a, p, st) : tiles_go<64, 4>(a, p, st);
-  if (a.c.dim <= 128) return p.waves == 8 ? tiles_go<128, 8>(a, p, st) : tiles_go<128, 4>(a, p, st);
-  return tiles_go<256, 4>(a, p, st);
+void launch_attend_tiles(const AttendArgs& a, const TilesPlan& p, hipStream_t st) {
+  const uint32_t grid = (uint32_t)(p.units * p.parts);
+  const int units = (int)p.units;
+  if (a.c.dim > 128) k_attend_tiles<256, 4><<<grid, 256, 0, st>>>(a, units, p.parts);
+  else if (a.c.dim > 64 && p.waves == 8) k_attend_tiles<128, 8><<<grid, 512, 0, st>>>(a, units, p.parts);
+  else if (a.c.dim > 64) k_attend_tiles<128, 4><<<grid, 256, 0, st>>>(a, units, p.parts);
+  else k_attend_tiles<64, 4><<<grid, 256, 0, st>>>(a, units, p.parts);
 }
 
 }  // namespace nvfp4

@@ -277,6 +277,42 @@ struct PageWindow {
   }
 };
 
+// ------------------------------------------------------------- what is joined
+
+// What the join needs of a unit whose first part is this piece's; parts 0: no unit.
+// The parts: `head` pieces from here on, then one of each of `middle` workgroups,
+// then the others from the first piece of workgroup w1 on.  (The join scanned the
+// sequences itself before: 10 to 27 us.)
+struct JoinHeader {
+  int parts, head, middle, w1, unit, q0, n, shared;
+};
+
+// A partial result: sixteen rows of D sums, then their maxima, then their sums of weights.
+NV_DEV int64_t part_size(int D) { return 16 * (int64_t)D + 32; }
+// The workspace: two partial results for each piece (of a unit that began before it,
+// and of one that it begins), then the headers.
+NV_DEV JoinHeader* headers(const AttendArgs& a, int D, int pieces) { return reinterpret_cast<JoinHeader*>(a.part + 2 * (int64_t)pieces * part_size(D)); }
+
+// Sixteen rows of unit `unit` of sequence s: row r is query r / G, head r % G of the unit's shared head.
+struct UnitRow {
+  int token, head;  // token -1: no such row
+};
+NV_DEV UnitRow unit_row(const Sequence& s, int G, int Hk, int unit, int r) {
+  const int h = unit % Hk, m = unit / Hk * 16 + r, i = m / G;
+  return {i < s.n ? s.q0 + i : -1, h * G + m - i * G};
+}
+
+// What the join needs of a unit; parts 0: nothing to join.
+struct TileHeader {
+  int parts, m0, h, q0, n, pad[3];
+};
+// The workspace: headers, then `parts` partial results for each unit, of rows x D
+// sums, their maxima and their sums of weights.
+NV_DEV TileHeader* tile_headers(const AttendArgs& a) { return reinterpret_cast<TileHeader*>(a.tiles); }
+NV_DEV float* tile_part(const AttendArgs& a, int units, int parts, int rows, int unit, int i) {
+  return a.tiles + 8 * (int64_t)units + ((int64_t)unit * parts + i) * rows * (a.c.dim + 2);
+}
+
 // Four elements of row `row` of the outputs, from its sums o, maximum and sum of weights.
 NV_DEV void write_row(const AttendArgs& a, int64_t row, int d, nv_f4 o, float m, float l, float vdec) {
   const float inv = l == 0.0f ? 0.0f : vdec / l;

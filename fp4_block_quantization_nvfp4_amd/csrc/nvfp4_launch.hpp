@@ -142,12 +142,13 @@ struct AttendArgs {
   const int* ends;         // [B] cumulative queries, or NULL: one each
   uint16_t* out;           // [T, heads, dim] bf16
   float* lse;              // [T, heads]
-  float* part;             // workspace of the split kernel
+  float *part, *tiles;     // workspaces of the split kernel and of the tiled one
   float scale;
   int T, B, width, causal;
   int most;                // rows (queries times heads that share keys) of a sequence that the split kernel takes
 };
-int launch_attend(const AttendArgs& a, int which, void* stream);  // which: 1 the split kernel, 2 the tiled one, 3 both
+// which: attend_kernels().  Sets `part` and `tiles` from the workspace.
+int launch_attend(AttendArgs a, int which, void* workspace, void* stream);
 
 // Test support: exhaustive conversion scans (k_selftest.hip).
 int launch_selftest_scan(int kind, uint32_t param, uint64_t first, uint64_t count, int chunk_log2,

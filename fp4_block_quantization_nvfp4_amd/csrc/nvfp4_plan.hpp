@@ -272,9 +272,8 @@ enum AttentionKernel {
   PLAN_ROPE_SUM = 2,
   PLAN_READ_CACHE = 3,
   PLAN_ATTEND_SPLIT = 4,
-  PLAN_ATTEND_JOIN = 5,
-  PLAN_ATTEND_TILES = 6,
-  PLAN_ATTEND_TILES_JOIN = 7,
+  PLAN_ATTEND_TILES = 5,
+  PLAN_ATTEND_JOIN = 6,
 };
 
 // Norm and rotation: LN lanes to a row, sixteen elements each, 64 / LN rows a
@@ -330,9 +329,9 @@ inline int64_t attend_pieces(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64
 inline LayerLaunch plan_attend_split(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
   return {PLAN_ATTEND_SPLIT, attend_pieces(T, B, Hq, Hk, D, keys), 1, 256};
 }
-inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
-  if (keys <= kAttendTile) return {0, 0, 0, 0};  // no unit has two tiles
-  return {PLAN_ATTEND_JOIN, attend_pieces(T, B, Hq, Hk, D, keys), 4, 256};
+// What its pieces leave: none where no unit has two tiles.
+inline size_t attend_split_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+  return keys <= kAttendTile ? 0 : (size_t)(4 * attend_pieces(T, B, Hq, Hk, D, keys) * (2 * (16 * D + 32) * 4 + 32));
 }
 // Tiled kernel.  Units of 32 rows a wave at most: each sequence adds less than one to T * G / rows.
 // Eight waves share the decoding of a tile among twice the rows of four, where there are
@@ -359,19 +358,21 @@ inline LayerLaunch plan_attend_tiles(int64_t T, int64_t B, int64_t Hq, int64_t H
   const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
   return {PLAN_ATTEND_TILES, p.units * p.parts, 1, 64 * p.waves};
 }
-inline LayerLaunch plan_attend_tiles_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
+// Joins both kernels' parts: four workgroups to one of the split kernel, one to sixteen rows
+// of a shared unit of the tiled one.
+inline LayerLaunch plan_attend_join(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys, int which) {
+  if (keys <= kAttendTile) return {0, 0, 0, 0};  // no unit has two tiles
   const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
-  if (p.parts == 1) return {0, 0, 0, 0};
-  return {PLAN_ATTEND_TILES_JOIN, p.units, 2 * p.waves, 256};
+  return {PLAN_ATTEND_JOIN, 4 * attend_pieces(T, B, Hq, Hk, D, keys) + (which & 2 && p.parts > 1 ? p.units * 2 * p.waves : 0), 1, 256};
 }
-// Both kernels' workspaces, one after the other's: they run one after the other.
+// The split kernel's workspace, then the tiled one's: one launch joins both.
 inline size_t attend_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys, bool ends) {
-  size_t split = keys <= kAttendTile ? 0 : (size_t)(4 * attend_pieces(T, B, Hq, Hk, D, keys) * (2 * (16 * D + 32) * 4 + 32)), tiles = 0;
+  size_t n = attend_split_bytes(T, B, Hq, Hk, D, keys);
   if (attend_kernels(T, Hq, Hk, ends) & 2) {
     const TilesPlan p = tiles_plan(T, B, Hq, Hk, D, keys);
-    if (p.parts > 1) tiles = (size_t)(p.units * (32 + (int64_t)p.parts * 32 * p.waves * (D + 2) * 4));
+    if (p.parts > 1) n += (size_t)(p.units * (32 + (int64_t)p.parts * 32 * p.waves * (D + 2) * 4));
   }
-  return split > tiles ? split : tiles;
+  return n;
 }
 
 }  // namespace nvfp4

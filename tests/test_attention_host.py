@@ -154,7 +154,7 @@ def test_cpu_tensors_are_refused():
 
 # ----------------------------------------------------------------- launches
 
-ROPE_K, ROPE_BWD, ROPE_SUM, READ, SPLIT, JOIN, TILES, TILES_JOIN = range(8)
+ROPE_K, ROPE_BWD, ROPE_SUM, READ, SPLIT, TILES, JOIN = range(7)
 
 
 def plan(entry, T, Hq=4, Hk=2, D=64, B=1, keys=16):
@@ -201,22 +201,26 @@ def test_launches_stay_in_the_limits():
         if entry == 4:
             assert first[1] * 256 >= T * Hk * (D // 16) and first[2] == 2
         if entry >= 5:
-            split, join, tiles, tiles_join = launches
+            split, tiles, join, _ = launches
             c, G = cache(heads=Hk, dim=D), Hq // Hk
             need = L.lib().nvfp4_cache_attention_workspace_bytes(T, Hq, ref(c), B, keys // 16)
-            assert (join[1] > 0) == (keys > 64) and join[1] in (0, split[1])
-            assert need >= join[1] * 4 * (2 * (16 * D + 32) * 4 + 32)
+            assert (join[1] > 0) == (keys > 64)
+            least = (keys > 64) * split[1] * 4 * (2 * (16 * D + 32) * 4 + 32)
+            assert need >= least and least % 16 == 0
+            joined = 4 * split[1]
             if tiles[1]:  # units of any split of T queries over B sequences and those of none, each in as many parts
                 rows = tiles[3] // 2
                 units = (ceil(T * G, rows) + B) * Hk
                 assert entry == 5 and rows in (128, 256) and tiles[1] % units == 0
                 parts = tiles[1] // units
-                assert 1 <= parts <= 16 and (tiles_join[1] == units and tiles_join[2] * 16 == rows if parts > 1 else tiles_join[1] == 0)
-                assert parts == 1 or need >= units * (32 + parts * rows * (D + 2) * 4)
-                assert parts == 1 or units * parts <= 1024
+                assert 1 <= parts <= 16
+                if parts > 1:
+                    assert need >= least + units * (32 + parts * rows * (D + 2) * 4) and units * parts <= 1024 and keys > 64
+                    joined += units * rows // 16
             else:
                 assert entry == 6 or T * G <= 128
-    assert set(got) == set(range(8)) and min(got.values()) > 20
+            assert join[1] == (joined if keys > 64 else 0)
+    assert set(got) == set(range(7)) and min(got.values()) > 20
 
 
 def test_plan_refusals():

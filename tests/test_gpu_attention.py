@@ -4,6 +4,7 @@
 masks that leave rows empty, garbage in slots that no query may see, bad pages,
 other streams, captured and replayed steps.  Tolerances count the roundings that
 the definitions allow; each is derived where it is used."""
+import ctypes
 import math
 
 import numpy as np
@@ -12,6 +13,7 @@ import torch
 
 import fp4_block_quantization_nvfp4_amd as nv
 import oracle
+from fp4_block_quantization_nvfp4_amd import _lib as L
 from tests import attention_ref as A
 from tests import layer_ref as R
 from tests.gpu_util import need_gpu
@@ -564,6 +566,26 @@ def test_empty_calls():
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
     out, lse = nv.cache_attention(torch.ones(3, 4, 64, dtype=BF, device="cuda"), c, torch.zeros(0, 1, dtype=torch.int32, device="cuda"), i, i)
     assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_workspace_of_no_bytes():
+    """Where none is needed, one that is there is left as it was."""
+    g = gen(31)
+    table, pages = tables(g, [40, 64, 0], 16, extra=0)
+    c, q = filled(g, pages, 16, 2, 64), randn(g, 40, 4, 64).cuda()
+    table = table[:, :4].contiguous().cuda()
+    lens, ends = torch.tensor([40, 64, 0], dtype=torch.int32).cuda(), torch.tensor([38, 39, 40], dtype=torch.int32).cuda()
+    want = nv.cache_attention(q, c, table, lens, ends)
+    P = lambda t: None if t is None else t.data_ptr()
+    heads = L.Heads(P(q), 4, q.stride(0), q.stride(1))
+    view = L.Cache(P(c.k), P(c.k_scale), P(c.v), P(c.v_scale), P(c.k_amax), P(c.v_amax), c.k.shape[0], 16, 2, 64)
+    assert L.lib().nvfp4_cache_attention_workspace_bytes(40, 4, ctypes.byref(view), 3, 4) == 0
+    space = torch.full((1 << 24,), 7, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(40, 4, device="cuda")
+    st = L.lib().nvfp4_cache_attention(ctypes.byref(heads), 40, ctypes.byref(view), P(table), 3, 4, P(lens), P(ends), 0.125, 1, P(out), P(lse), P(space), 0, torch.cuda.current_stream().cuda_stream)
+    assert st == L.OK
+    torch.cuda.synchronize()
+    assert (space == 7).all() and torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 # ------------------------------------------------------- a run of them together
