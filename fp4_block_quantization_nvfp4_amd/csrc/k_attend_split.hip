@@ -20,7 +20,7 @@
 // 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 79 us and 7 for the join, 4.3
 // TB/s of the 5.1 that a large copy reaches; two of up to 131072 keys 47 and 8.  What is
 // left is the start (scan of the sequences, page numbers, first keys: 4 us, one after the
-// other) and the two launches; the vector pipes are busy a third of the time, decoding
+// other) and the two launches; the vector pipes are busy half of the time, decoding
 // and softmax.  Two or four blocks of sixteen rows a unit, decoded for once, were slower:
 // 24 queries a sequence 81 -> 93 us, 16 sequences of up to 64 queries 35 -> 43, the chain
 // from scores to weights being longer than what it saves.
