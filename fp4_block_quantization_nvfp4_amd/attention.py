@@ -127,7 +127,9 @@ def cache_attention(q, cache, table, lens, ends=None, *, scale=None, causal=True
     keys; key j lies in page table[b, j // page_size] (int32 [B, pages at most]).
     causal: the sequence's last queries and keys are the same tokens, so query i of
     n sees the keys j <= lens[b] - n + i; otherwise all (an encoder's states).
-    Queries without keys and those past the last end get 0 and -inf.  scale > 0,
-    D ** -0.5 by default."""
+    Queries without keys and those past the last end get 0 and -inf; NaN those that
+    see a key of a page that is not in the cache or with a NaN among its scales or its
+    value's, and all of a sequence with more keys than its row of the table names.
+    scale > 0, D ** -0.5 by default."""
     return _n.cache_attention(q, cache.k, cache.k_scale, cache.v, cache.v_scale, cache.k_amax, cache.v_amax, table, lens, ends,
                               scale, causal)

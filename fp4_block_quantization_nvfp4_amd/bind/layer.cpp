@@ -399,7 +399,7 @@ struct Pages {
       t[i] = x;
     }
     const int64_t P = t[0].size(0), H = t[0].size(1), S = t[0].size(2), half = t[0].size(3);
-    REFUSE_IF(half % 8 != 0 || half == 0, "cache.k must be [pages, heads, page_size, dim / 2] with dim % 16 == 0");
+    REFUSE_IF(half % 8 != 0 || half == 0 || H == 0, "cache.k must be [pages, heads, page_size, dim / 2] with heads >= 1 and dim % 16 == 0");
     for (int i = 1; i < 4; ++i)
       REFUSE_IF(t[i].device() != t[0].device() || t[i].sizes() != at::IntArrayRef({P, H, S, i == 2 ? half : half / 8}), kNames[i],
                 " must be ", at::IntArrayRef({P, H, S, i == 2 ? half : half / 8}), " on the same device");

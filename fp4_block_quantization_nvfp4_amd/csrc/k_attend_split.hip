@@ -207,7 +207,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
     for (int i = 0; i < NT; ++i) O[i] = (nv_f4){0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
     uint8_t* vs = lds[wv];
-    auto step = [&](const RawKeys<DP>(&K)[2], const RawKeys<DP>(&V)[2], int key0, auto masked) {
+    auto step = [&](RawKeys<DP>(&K)[2], RawKeys<DP>(&V)[2], int key0, auto masked) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < RawKeys<DP>::PIECES; ++i) nan_to_key(K[g].s[i], V[g].s[i]);
       nv_f4 Sc[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {

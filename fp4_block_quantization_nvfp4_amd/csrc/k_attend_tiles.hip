@@ -123,8 +123,10 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
     r[0].load(a.c, true, page, h, key, key < s.L, g4);
     r[1].load(a.c, false, page, h, key, key < s.L, g4);
   };
-  auto store = [&](const RawTile<DP>* r, int buf) {
+  auto store = [&](RawTile<DP>* r, int buf) {
     uint8_t* to = lds + buf * 2 * TILE;
+#pragma unroll
+    for (int i = 0; i < RawTile<DP>::PIECES; ++i) nan_to_key(r[0].s[i], r[1].s[i]);
     r[0].store(to, tk, g4);
     r[1].store(to + TILE, tk, g4);
   };
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
   __syncthreads();
 
   // tile j from buffer buf; tile j + 2 into r, from where tile j was stored; then tile j + 1 from n
-  auto tile = [&](int j, int buf, RawTile<DP>* r, const RawTile<DP>* n) {
+  auto tile = [&](int j, int buf, RawTile<DP>* r, RawTile<DP>* n) {
     const uint8_t* K = lds + buf * 2 * TILE;
     const uint8_t* V = K + TILE;
     const int key0 = j * kKeys;

@@ -246,6 +246,13 @@ NV_DEV int page_of(const AttendArgs& a, const Sequence& s, int j) {
   return p >= 0 && p < a.c.pages && !s.over ? p : -1;
 }
 constexpr uint32_t kNanScales = 0x7F7F;
+// Scales of a key's and of its value's blocks, up to two bytes each: a NaN of the value's goes
+// to the key's, so that a query that does not see the key (weight 0) has none of it.
+NV_DEV void nan_to_key(uint32_t& k, uint32_t& v) {
+  const bool nan = (((v & 0x7F7Fu) + 0x0101u) & 0x8080u) != 0;
+  k = nan ? kNanScales : k;
+  v = nan ? 0 : v;
+}
 
 // A sequence's pages for a wave that walks along the keys: 64 entries of its row of
 // the table in a register, the next 64 on their way, so that no load waits for a

@@ -455,6 +455,24 @@ def test_rows_that_are_not_finite():
         assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[1, 2]) and torch.isnan(out[3, 0].float()).any()
 
 
+@pytest.mark.parametrize("n,L,D", [(5, 40, 64), (40, 150, 128), (100, 200, 256), (300, 400, 96), (300, 300, 64), (150, 700, 160)])
+@pytest.mark.parametrize("what", ["k_scale", "v_scale"])
+def test_nan_in_keys_that_are_hidden(n, L, D, what):
+    """A NaN scale of a key or a value reaches the queries that see it, and no other."""
+    g = gen(50 + D)
+    table, pages = tables(g, [L], 16)
+    c = filled(g, pages, 16, 2, D)
+    q, lens, ends = randn(g, n, 4, D).cuda(), torch.tensor([L], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda()
+    want = nv.cache_attention(q, c, table.cuda(), lens, ends)
+    j = L - n // 2  # queries from here on see it
+    getattr(c, what)[table[0, j // 16], 1, j % 16, D // 16 - 1] = 0x7F if n % 2 else 0xFF
+    out, lse = nv.cache_attention(q, c, table.cuda(), lens, ends)
+    first = j - (L - n)
+    assert torch.equal(out[:first], want[0][:first]) and torch.equal(lse[:first], want[1][:first])
+    assert torch.equal(out[:, :2], want[0][:, :2]) and torch.equal(lse[:, :2], want[1][:, :2])
+    assert torch.isnan(out[first:, 2:]).all() and torch.isnan(lse[first:, 2:]).all()
+
+
 def test_bad_pages_and_lengths():
     """Pages that are not in the cache, and lengths past the table's rows, give NaN where a query sees them; ends in any order stay in range."""
     g = gen(13)
@@ -536,6 +554,9 @@ def test_refusals():
     value("out_dtype", lambda: nv.read_cache(c, i, out_dtype=torch.float16))
     value("cache.v_scale", lambda: nv.read_cache(nv.PagedCache(c.k, c.k_scale, c.v, c.v_scale[:1]), i))
     value("k_amax", lambda: nv.read_cache(nv.PagedCache(c.k, c.k_scale, c.v, c.v_scale, k_amax=torch.ones(1).cuda()), i))
+    none = nv.PagedCache.empty(3, 16, 0, 64)
+    value("heads >= 1", lambda: nv.cache_attention(q, none, table, i))
+    value("heads >= 1", lambda: nv.write_cache(none, q[:, :0], q[:, :0], i))
     status = lambda call: _refused(nv.NVFP4Error, "status", call)
     status(lambda: nv.cache_attention(q, c, table, i, scale=-1.0))
     status(lambda: nv.norm_rope(q, k, i, nv.rotary_frequencies(66)[0]))
