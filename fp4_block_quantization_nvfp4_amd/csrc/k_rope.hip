@@ -300,11 +300,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_
 
 // A wave has tokens in turn and keeps its sums of dw in registers over all of them; a
 // workgroup's four meet in shared memory, and a second kernel adds the workgroups' in order.
-// 8192 tokens, 40 heads of 128, bf16: 59 us (69 from idle), 252 MB at 4.3 TB/s, and 4.7 for
-// the second.  Bound by memory, with two waves on a SIMD for what each keeps (registers
-// for three: spilled and slower).
+// 8192 tokens, 40 heads of 128, bf16: 50.8 us with the second kernel's 4.7, 252 MB at 5.4
+// TB/s.  Bound by memory; three waves on a SIMD (two, 32-bit rows), each with its next rows on
+// their way, also over the end of a token, are all of the grid.
 template <typename T, int LN, bool INTER>
-__global__ __launch_bounds__(256) void k_norm_rope_bwd(const RopeArgs a, const HeadsView dq, const HeadsView dk, float* __restrict__ partial) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_norm_rope_bwd(const RopeArgs a, const HeadsView dq, const HeadsView dk, float* __restrict__ partial) {
   constexpr int RW = 64 / LN;
   __shared__ SinCos lds[4][8 * LN];
   __shared__ float sums[4][16 * LN];
@@ -313,29 +313,34 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(const RopeArgs a, const H
   float dw[2][16];
 #pragma unroll
   for (int i = 0; i < 32; ++i) dw[i / 16][i % 16] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wv; t < a.T; t += (int64_t)gridDim.x * 4) {
+  // the next rows are on their way while these are used, across kinds and tokens
+  RawRuns<T> gn, yn;
+  auto fetch = [&](bool keys, int64_t t, int h0) {
+    const HeadsView &dz = keys ? dk : dq, &view = keys ? a.k : a.q;
+    const int h = h0 + lane / LN;
+    const bool has = h < view.heads && at.in;
+    gn.load(has, (const T*)dz.at + t * dz.token + h * dz.head, at.e0, at.e1);
+    yn.load(has && (keys ? a.kw : a.qw), (const T*)view.at + t * view.token + h * view.head, at.e0, at.e1);
+  };
+  const int64_t t0 = (int64_t)blockIdx.x * 4 + wv, step = (int64_t)gridDim.x * 4;
+  if (t0 < a.T) fetch(a.q.heads == 0, t0, 0);
+  for (int64_t t = t0; t < a.T; t += step) {
     float c[8], s[8];
     if (a.R) angles<LN>(a, (int)t, lane, at.turn, lds[wv], c, s);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      const HeadsView &dz = kind ? dk : dq, &view = kind ? a.k : a.q;
+      const HeadsView& view = kind ? a.k : a.q;
       const float* w = kind ? a.kw : a.qw;
       T* dst = (T*)(kind ? a.k_out : a.q_out);
-      auto fetch = [&](int h0, RawRuns<T>& g, RawRuns<T>& y) {
-        const int h = h0 + lane / LN;
-        const bool has = h < view.heads && at.in;
-        g.load(has, (const T*)dz.at + t * dz.token + h * dz.head, at.e0, at.e1);
-        y.load(has && w, (const T*)view.at + t * view.token + h * view.head, at.e0, at.e1);
-      };
-      RawRuns<T> gn, yn;
-      fetch(0, gn, yn);
       for (int h0 = 0; h0 < view.heads; h0 += RW) {
         const int h = h0 + lane / LN;
         const bool has = h < view.heads && at.in;
         float d[16], x[16];
         gn.values(d);
         yn.values(x);
-        if (h0 + RW < view.heads) fetch(h0 + RW, gn, yn);
+        const bool more = h0 + RW < view.heads, keys = more ? kind : kind == 0 && a.k.heads || a.q.heads == 0;
+        const int64_t then = more || (kind == 0 && a.k.heads) ? t : t + step;
+        if (then < a.T) fetch(keys, then, more ? h0 + RW : 0);
         if (a.R && at.turn) rotate<INTER>(d, c, s, true);
         if (w) {
           float f[16];
@@ -448,11 +453,11 @@ int launch_norm_rope(const RopeArgs& a, void* stream) {
   return (int)hipGetLastError();
 }
 
-size_t rope_bwd_workspace_bytes(int64_t T, int64_t D) { return (size_t)(rope_bwd_groups(T) * 2 * D * 4); }
+size_t rope_bwd_workspace_bytes(int64_t T, int64_t D) { return (size_t)(rope_bwd_groups(T, true) * 2 * D * 4); }
 
 template <typename T, int LN, bool INTER>
 static void rope_bwd_go(const RopeArgs& a, const HeadsView& dq, const HeadsView& dk, float* partial, hipStream_t st) {
-  const LayerLaunch p = plan_rope_bwd(a.T);
+  const LayerLaunch p = plan_rope_bwd(a.T, a.in_bf16);
   k_norm_rope_bwd<T, LN, INTER><<<(uint32_t)p.grid, p.block, 0, st>>>(a, dq, dk, partial);
 }
 
@@ -466,7 +471,7 @@ int launch_norm_rope_bwd(const RopeArgs& a, const HeadsView& dq, const HeadsView
     NV_ROPE(NV_GO)
 #undef NV_GO
   }
-  if (dw) return launch_sum_rows(partial, (int)rope_bwd_groups(a.T), 2 * (int64_t)a.D, dw, stream);
+  if (dw) return launch_sum_rows(partial, (int)rope_bwd_groups(a.T, a.in_bf16), 2 * (int64_t)a.D, dw, stream);
   return (int)hipGetLastError();
 }
 
