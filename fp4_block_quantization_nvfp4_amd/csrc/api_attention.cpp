@@ -259,10 +259,10 @@ nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int
   if (Hq > kMaxHeads || Hk > kMaxHeads || !fits(Hq * D, T) || !fits(Hk * D, T) || B > kMaxB || keys > kMaxKeys || B * Hk > kMaxUnits) return NVFP4_E_RANGE;
   nvfp4::LayerLaunch p[4] = {};
   if (T != 0) {
-    if (entry == 0) p[0] = nvfp4::plan_rope(T, Hq + Hk, D);
+    if (entry == 0) p[0] = nvfp4::plan_rope(T, Hq + Hk, D, true, false);
     if (entry == 1) p[0] = nvfp4::plan_rope_bwd(T, true), p[1] = nvfp4::plan_rope_sum(D);
-    if (entry == 2) p[0] = nvfp4::plan_rope(T, Hq + 2 * Hk, D);
-    if (entry == 3) p[0] = nvfp4::plan_rope(T, 2 * Hk, D);
+    if (entry == 2) p[0] = nvfp4::plan_rope(T, Hq + 2 * Hk, D, true, true);
+    if (entry == 3) p[0] = nvfp4::plan_rope(T, 2 * Hk, D, true, true);
     if (entry == 4) p[0] = nvfp4::plan_read_cache(T, Hk, D);
     if (entry >= 5) {
       if (nvfp4::attend_split_tiles(T, B, Hq, Hk, keys) >= int64_t(1) << 31) return NVFP4_E_RANGE;

@@ -197,7 +197,8 @@ struct Row {
 };
 
 // The next row is on its way while one is used (16384 tokens to the cache, 8 heads of
-// 128: 29 -> 25 us; 8192 with norm and rotation: 60 -> 50).  Of 16-bit rows that go to
+// 128: 29 -> 25 us, 22 with a grid of what runs at a time; 8192 with norm and rotation: 60 ->
+// 50, 47).  (Over the end of a token too, as the gradient has it: 170 registers, 27 and 59 us.)  Of 16-bit rows that go to
 // the outputs, registers for four waves on a SIMD (8192 tokens, 40 heads of 128: 36.5 ->
 // 34.3 us; 32-bit ones then spill: 21 -> 26 at 20 heads of 64).
 template <typename T, int LN, bool INTER, bool CACHE>
@@ -427,7 +428,7 @@ __global__ __launch_bounds__(256) void k_read_cache(const CacheView c, const int
 template <typename T, int LN, bool INTER>
 static void rope_go(const RopeArgs& a, hipStream_t st) {
   const int rows = a.q.heads + a.k.heads + (a.slots ? a.k.heads : 0);
-  const LayerLaunch p = plan_rope(a.T, rows, a.D);
+  const LayerLaunch p = plan_rope(a.T, rows, a.D, a.in_bf16, a.slots != nullptr);
   const int64_t chunks = rope_chunks(a.T, rows, a.D), per = ceil_div(rope_passes(rows, a.D), chunks);
   if (a.slots) k_norm_rope<T, LN, INTER, true><<<(uint32_t)p.grid, p.block, 0, st>>>(a, (int)chunks, (int)per);
   else k_norm_rope<T, LN, INTER, false><<<(uint32_t)p.grid, p.block, 0, st>>>(a, (int)chunks, (int)per);

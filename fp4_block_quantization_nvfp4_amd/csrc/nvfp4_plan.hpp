@@ -290,9 +290,17 @@ inline int64_t rope_chunks(int64_t T, int64_t rows, int64_t D) {
   const int64_t p = rope_passes(rows, D), c = T > 0 ? ceil_div(4096, T) : 1;
   return c < 1 ? 1 : c < p ? c : p;
 }
-inline LayerLaunch plan_rope(int64_t T, int64_t rows, int64_t D) {
-  const int64_t g = ceil_div(T * rope_chunks(T, rows, D), 4);
-  return {PLAN_ROPE, g < kNormMaxGrid ? g : kNormMaxGrid, 1, 256};  // further tokens in a loop
+#ifndef RG
+#define RG kNormMaxGrid
+#endif
+// Workgroups: what runs at a time by registers, three waves on a SIMD, of 32-bit rows to the cache
+// two; rows of 16 bits to the outputs, four and little work each, all at once.  Measured, us, all at
+// once (so): 16384 tokens of 8 heads to the cache 24.4 (22.1), 8192 of 40 heads with norm and rotation
+// 49.0 (47.0), of 20 in fp32 39.9 (37.8), fp32 to the outputs 20.8 (19.5); bf16 34.5 (1024 groups 35.2).
+inline int64_t rope_groups(bool bf16, bool cache) { return cache ? (bf16 ? 768 : 512) : bf16 ? kNormMaxGrid : 768; }
+inline LayerLaunch plan_rope(int64_t T, int64_t rows, int64_t D, bool bf16, bool cache) {
+  const int64_t g = ceil_div(T * rope_chunks(T, rows, D), 4), most = rope_groups(bf16, cache);
+  return {PLAN_ROPE, g < most ? g : most, 1, 256};  // further tokens in a loop
 }
 // The gradient's workgroups: what runs at a time, three waves on a SIMD of 16-bit rows, two of
 // 32-bit ones, so that none waits for a place (8192 tokens, 40 heads of 128 in bf16: 1024 groups
