@@ -301,8 +301,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_
 
 // A wave has tokens in turn and keeps its sums of dw in registers over all of them; a
 // workgroup's four meet in shared memory, and a second kernel adds the workgroups' in order.
-// 8192 tokens, 40 heads of 128, bf16: 50.8 us with the second kernel's 4.7, 252 MB at 5.4
-// TB/s.  Bound by memory; three waves on a SIMD (two, 32-bit rows), each with its next rows on
+// 8192 tokens, 40 heads of 128, bf16: 51 to 54 us with the second kernel's 4.7, 252 MB at
+// 5.1 to 5.4 TB/s.  Bound by memory; three waves on a SIMD (two, 32-bit rows), each with its next rows on
 // their way, also over the end of a token, are all of the grid.
 template <typename T, int LN, bool INTER>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_norm_rope_bwd(const RopeArgs a, const HeadsView dq, const HeadsView dk, float* __restrict__ partial) {
