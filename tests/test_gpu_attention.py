@@ -155,10 +155,44 @@ def test_norm_rope_many_tokens():
     first = nv.norm_rope_backward(dq.cuda(), dk.cuda(), qc, kc, p.cuda(), f.cuda(), **how)
     gx, gw, terms, wterms = A.norm_rope_gradient(dq, q, w, p, f)
     R.assert_near(first[0], gx, gx.abs() * 2.0 ** -8 + 32 * R.U24 * terms.amax(-1, keepdim=True), "dq")
-    # a lane adds up at most T * H / (1024 workgroups) terms and the partial sums are joined in a tree and 16 more: far below T / 4
+    # a lane adds up at most T * H / (768 workgroups) terms and the partial sums are joined in a tree and 16 more: far below T / 4
     R.assert_near(first[2], gw, (T // 4) * R.U24 * wterms, "dq weight")
     again = nv.norm_rope_backward(dq.cuda(), dk.cuda(), qc, kc, p.cuda(), f.cuda(), **how)
     assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hk,D", [(2, 0, 64), (0, 3, 48), (9, 2, 128), (17, 1, 64), (2, 5, 256)])
+def test_many_tokens_a_wave(Hq, Hk, D, dtype):
+    """Tokens past the grid, with sides that have no heads or a ragged last pass: rows are those of calls on parts of the tokens,
+    and so is what is written; the weights' gradients are the parts' sums."""
+    g = gen(60 + D)
+    T, page = 8200, 64
+    q, k = rows(g, T, Hq, Hk, D, dtype)
+    both, dz = torch.cat((q, k), 1).cuda(), randn(g, T, Hq + Hk, D, dtype=dtype).cuda()
+    p, f = torch.randint(0, 1 << 17, (T,), generator=g, dtype=torch.int32).cuda(), nv.rotary_frequencies(D - D % 32)[0]
+    for qw, kw in ((torch.rand(D, generator=g).cuda(), torch.rand(D, generator=g).cuda()), (None, torch.rand(D, generator=g).cuda()), (None, None)):
+        how = dict(q_weight=qw, k_weight=kw)
+        cut = lambda at: (dz[at, :Hq], dz[at, Hq:], both[at, :Hq], both[at, Hq:], p[at], f)
+        parts = [slice(a, min(a + 1000, T)) for a in range(0, T, 1000)]
+        whole, some = nv.norm_rope_backward(*cut(slice(0, T)), **how), [nv.norm_rope_backward(*cut(at), **how) for at in parts]
+        for i in range(2):
+            assert torch.equal(whole[i], torch.cat([x[i] for x in some]))
+        for i, heads in ((2, Hq), (3, Hk)):
+            if whole[i] is not None:
+                want = torch.stack([x[i].double() for x in some]).sum(0)
+                # each sum's order: T * heads terms, of which a lane has a few hundred at most and trees the others
+                size = torch.stack([x[i].double().abs() for x in some]).sum(0) + (T * max(heads, 1)) ** 0.5 * 64
+                assert ((whole[i].double() - want).abs() <= 512 * R.U24 * size).all()
+    if Hk == 0:
+        return
+    slots = torch.randperm(T + 100, generator=g)[:T].int().cuda()
+    slots[5::7] = -1
+    a, b = (nv.PagedCache.empty((T + 163) // page, page, Hk, D) for _ in range(2))
+    cut = lambda at: (both[at, :Hq], both[at, Hq:], dz[at, Hq:], p[at], f)
+    out = nv.norm_rope_write(*cut(slice(0, T)), a, slots, k_weight=torch.ones(D).cuda())
+    got = torch.cat([nv.norm_rope_write(*cut(at), b, slots[at], k_weight=torch.ones(D).cuda()) for at in parts])
+    assert torch.equal(out, got) and all(torch.equal(getattr(a, n), getattr(b, n)) for n in ("k", "k_scale", "v", "v_scale"))
 
 
 # ------------------------------------------------------------------- cache
