@@ -233,10 +233,11 @@ struct SequenceScan {
   }
 };
 
-// Keys that query i of the sequence sees.
+// Keys that query i of the sequence sees.  Of one that is `over` all do all that the row
+// names (sixteen at least, and all NaN): counted back from the clamped L the first queries would see none, and get 0.
 NV_DEV int seen_by(const AttendArgs& a, const Sequence& s, int i) {
   const int m = s.L - s.n + i + 1;
-  return !a.causal ? s.L : m < 0 ? 0 : m;
+  return !a.causal || s.over ? s.L : m < 0 ? 0 : m;
 }
 
 // Page that holds key j of a sequence (j < L), or -1 where the table names none.
