@@ -289,6 +289,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
       if (key0 + 32 < keys) step(K1, V1, key0 + 32, Masked<true>{});
     }
     l = quarter_sum(l);
+    m = left_max(m, l, limit);
     if (shared) {
       float* mysum = reinterpret_cast<float*>(lds[wv]);
 #pragma unroll

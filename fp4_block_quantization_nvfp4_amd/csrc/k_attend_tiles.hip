@@ -249,6 +249,7 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
     if (j + 1 < tiles) tile(j + 1, 1, raw[1], raw[0]);
   }
   l += __shfl_xor(l, 32, 64);
+  m = left_max(m, l, limit);
   if (i >= s.n) return;
   if (!whole) {
     float* part = tile_part(a, units, parts, ROWS, unit, split);

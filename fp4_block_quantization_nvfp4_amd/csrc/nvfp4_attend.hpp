@@ -13,6 +13,8 @@
 // largest at most.  Their sum is taken before that rounding.
 #pragma once
 
+#include <float.h>
+
 #include "nvfp4_cache.hpp"
 #include "nvfp4_experts.hpp"
 #include "nvfp4_plan.hpp"
@@ -321,14 +323,20 @@ NV_DEV float* tile_part(const AttendArgs& a, int units, int parts, int rows, int
   return a.tiles + 8 * (int64_t)units + ((int64_t)unit * parts + i) * rows * (a.c.dim + 2);
 }
 
-// Four elements of row `row` of the outputs, from its sums o, maximum and sum of weights.
+// The maximum that a row leaves.  Without weights it stays -infinity where the row sees no
+// key, and is the lowest finite number where it does: those scores are all -infinity, or lie
+// in other parts, next to which this one counts nothing.
+NV_DEV float left_max(float m, float l, int seen) { return l == 0.0f && seen > 0 ? -FLT_MAX : m; }
+
+// Four elements of row `row` of the outputs, from its sums o, maximum and sum of weights.  No
+// weights: 0 and -infinity for a row without keys, NaN where all its scores are -infinity.
 NV_DEV void write_row(const AttendArgs& a, int64_t row, int d, nv_f4 o, float m, float l, float vdec) {
-  const float inv = l == 0.0f ? 0.0f : vdec / l;
+  const float inv = l != 0.0f ? vdec / l : m == -INFINITY ? 0.0f : __builtin_nanf("");
   nv_u2 w;
   w.x = pack_bf16(o[0] * inv, o[1] * inv);
   w.y = pack_bf16(o[2] * inv, o[3] * inv);
   *reinterpret_cast<nv_u2*>(a.out + row * a.c.dim + d) = w;
-  if (d == 0) a.lse[row] = l == 0.0f ? -INFINITY : log_sum(m, l);
+  if (d == 0) a.lse[row] = l != 0.0f ? log_sum(m, l) : m == -INFINITY ? m : inv;
 }
 
 }  // namespace nvfp4

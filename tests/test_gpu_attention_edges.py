@@ -1,5 +1,5 @@
 """Attention on an NVFP4 cache on the GPU, where a result could pass for another one:
-sequences longer than their row of the table."""
+sequences longer than their row of the table, scores that are not finite."""
 import pytest
 import torch
 
@@ -55,3 +55,37 @@ def test_longer_than_the_row_among_many():
     out, lse = nv.cache_attention(q, c, table.cuda(), ints(640, 641), ints(n, 2 * n))
     assert torch.isnan(out[n:]).all() and torch.isnan(lse[n:]).all()
     assert (out[:60] == 0).all() and (lse[:60] == -INF).all() and torch.isfinite(out[60:n]).all() and torch.isfinite(lse[60:n]).all()
+
+
+# ------------------------------------------------- scores that are not finite
+
+
+def one_sign(page, pages, Hk, D):
+    """Keys that are all positive."""
+    g = gen(41)
+    c = filled(g, pages, page, Hk, D)
+    c.k.copy_(torch.tensor([0x12, 0x34, 0x56, 0x71], dtype=torch.uint8)[torch.randint(0, 4, c.k.shape, generator=g)])
+    return c
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,L", [(1, 1), (3, 40), (20, 300), (5, 3000), (80, 80), (80, 30), (300, 900), (130, 5000)])
+def test_scores_that_are_all_minus_infinity(D, n, L):
+    """-inf for every key that a query sees: exp(-inf + inf) is NaN, and 0 is only for queries that see none."""
+    c = one_sign(64, -(-L // 64) + 1, 2, D)
+    table = torch.arange(-(-L // 64), dtype=torch.int32).view(1, -1).cuda()
+    q = randn(gen(n), n, 4, D)
+    want, wl = nv.cache_attention(q.cuda(), c, table, ints(L), ints(n))
+    first = max(n - L, 0)  # the queries before see no key
+    row = (first + n) // 2
+    q[row, 1, 3] = -INF
+    out, lse = nv.cache_attention(q.cuda(), c, table, ints(L), ints(n))
+    assert torch.isnan(out[row, 1]).all() and torch.isnan(lse[row, 1])
+    assert (out[:first] == 0).all() and (lse[:first] == -INF).all()
+    keep = torch.ones(n, 4, dtype=torch.bool)
+    keep[row, 1] = False
+    assert torch.equal(out[keep.cuda()], want[keep.cuda()]) and torch.equal(lse[keep.cuda()], wl[keep.cuda()])
+    if first:
+        q[0, 2, 5] = -INF  # sees no key
+        out, lse = nv.cache_attention(q.cuda(), c, table, ints(L), ints(n))
+        assert (out[:first] == 0).all() and (lse[:first] == -INF).all()
