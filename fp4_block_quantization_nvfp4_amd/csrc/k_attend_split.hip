@@ -194,12 +194,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
       const uint32_t p = (uint32_t)__shfl_xor((int)big, 32, 64);
       big = p > big ? p : big;
     }
-    const float factor = query_factor(big);
+    const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
+    const float factor = query_factor(big), full = a.scale * kLog2e / factor * kdec, by = score_scale(full);
     nv_h8 Q[NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) Q[i] = query_to_f16(raw[i], factor);
-    const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
-    const float by = score_scale(a.scale * kLog2e / factor * kdec);
+    for (int i = 0; i < NS; ++i) Q[i] = query_to_f16(raw[i], query_scale(factor, full));
     const int limit = mine.token < 0 ? 0 : seen_by(a, q, mine.token - q.q0);
     const int least = uniform(seen_by(a, q, u / Hk * 16 / G));  // what all rows of the unit see
     nv_f4 O[NT];

@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
   const float kdec = a.c.ka ? a.c.ka[h] / 2688.0f : 1.0f, vdec = a.c.va ? a.c.va[h] / 2688.0f : 1.0f;
   const int row = m0 + 32 * wv + col, i = row / G, head = h * G + row - i * G;
   nv_h8 Q[NQ];
-  float factor;
+  float by;
   {
     nv_u4 x[NQ];
     uint32_t big = 0;
@@ -152,11 +152,11 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
       big = amax_bits(x[k], big);
     }
     const uint32_t o = (uint32_t)__shfl_xor((int)big, 32, 64);
-    factor = query_factor(o > big ? o : big);
+    const float factor = query_factor(o > big ? o : big), full = a.scale * kLog2e / factor * kdec;
+    by = score_scale(full);
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) Q[k] = query_to_f16(x[k], factor);
+    for (int k = 0; k < NQ; ++k) Q[k] = query_to_f16(x[k], query_scale(factor, full));
   }
-  const float by = score_scale(a.scale * kLog2e / factor * kdec);
   const int limit = i < s.n ? seen_by(a, s, i) : 0;
   nv_f16 O[NT];
 #pragma unroll

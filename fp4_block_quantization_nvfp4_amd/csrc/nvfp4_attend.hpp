@@ -107,8 +107,11 @@ struct Masked {
   static constexpr bool value = B;
 };
 
-// What a score is taken times; never zero, so that hidden scores stay -infinity.
-NV_DEV float score_scale(float v) { return v < 0x1p-120f ? 0x1p-120f : v; }
+// What a score is taken times; never zero or NaN, so that hidden scores stay -infinity.  Where it
+// would be NaN (the second-level scale is) the query is taken times that instead of its
+// power of two: NaN are then the scores of the keys that are seen, and no others.
+NV_DEV float score_scale(float v) { return v >= 0x1p-120f ? v : 0x1p-120f; }
+NV_DEV float query_scale(float factor, float by) { return by == by ? factor : by; }
 
 // log of the sum of exp from the running maximum and the sum of weights.
 NV_DEV float log_sum(float m, float l) { return (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l))); }

@@ -9,7 +9,7 @@ from tests.test_gpu_attention import filled, gen, randn, tables
 
 pytestmark = pytest.mark.gpu
 
-INF = float("inf")
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(autouse=True)
@@ -89,3 +89,20 @@ def test_scores_that_are_all_minus_infinity(D, n, L):
         q[0, 2, 5] = -INF  # sees no key
         out, lse = nv.cache_attention(q.cuda(), c, table, ints(L), ints(n))
         assert (out[:first] == 0).all() and (lse[:first] == -INF).all()
+
+
+@pytest.mark.parametrize("what", ["k_amax", "v_amax"])
+@pytest.mark.parametrize("n,L,D", [(20, 7, 64), (40, 33, 128), (90, 50, 128), (200, 180, 256), (700, 600, 64)])
+def test_amax_that_is_nan(n, L, D, what):
+    """A NaN second-level scale reaches the queries of its head that see a key, and no other."""
+    g = gen(42)
+    c = filled(g, -(-L // 64), 64, 2, D)
+    table = torch.arange(-(-L // 64), dtype=torch.int32).view(1, -1).cuda()
+    q = randn(g, n, 4, D).cuda()
+    want, wl = nv.cache_attention(q, c, table, ints(L), ints(n))
+    getattr(c, what)[1] = NAN
+    out, lse = nv.cache_attention(q, c, table, ints(L), ints(n))
+    first = n - L
+    assert torch.equal(out[:, :2], want[:, :2]) and torch.equal(lse[:, :2], wl[:, :2])
+    assert (out[:first] == 0).all() and (lse[:first] == -INF).all()
+    assert torch.isnan(out[first:, 2:]).all() and (what == "v_amax" or torch.isnan(lse[first:, 2:]).all())
