@@ -205,6 +205,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
 #pragma unroll
     for (int i = 0; i < NT; ++i) O[i] = (nv_f4){0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
+    bool far = false;  // a row's scores are large
     uint8_t* vs = lds[wv];
     auto step = [&](RawKeys<DP>(&K)[2], RawKeys<DP>(&V)[2], int key0, auto masked) {
 #pragma unroll
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
       }
       const float top = quarter_max(fmaxf(fmaxf(fmaxf(Sc[0][0], Sc[0][1]), fmaxf(Sc[0][2], Sc[0][3])),
                                           fmaxf(fmaxf(Sc[1][0], Sc[1][1]), fmaxf(Sc[1][2], Sc[1][3])))) * by;
-      if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+      if (__builtin_amdgcn_ballot_w64(top - m > kSlack)) {
         const float mn = fmaxf(m, top), alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
         m = mn;
         l *= alpha;
@@ -244,14 +245,22 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_split(const A
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) O[i][r] *= alpha;
+        far = __builtin_amdgcn_ballot_w64(far_up(m)) != 0;
       }
-      const float up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+      float f = by, up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+      if (far) {
+        const FarScores less(m, f, up);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Sc[g][r] = less(Sc[g][r]);
+      }
       float w[8];
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          w[4 * g + r] = exp2_fast(__builtin_fmaf(Sc[g][r], by, up));
+          w[4 * g + r] = exp2_fast(__builtin_fmaf(Sc[g][r], f, up));
           l += w[4 * g + r];
         }
       nv_u4 pw;

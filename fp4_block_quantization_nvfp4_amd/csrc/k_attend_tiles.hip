@@ -164,6 +164,7 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
 #pragma unroll
     for (int r = 0; r < 16; ++r) O[t][r] = 0.0f;
   float m = -INFINITY, l = 0.0f;
+  bool far = false;  // a row's scores are large
   if (first < tiles && loads) store(raw[0], 0);
   __syncthreads();
 
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, S[t][e]);
     top = half_max(top) * by;
-    if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+    if (__builtin_amdgcn_ballot_w64(top - m > kSlack)) {
       const float mn = fmaxf(m, top), alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
       m = mn;
       l *= alpha;
@@ -214,8 +215,16 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) O[t][e] *= alpha;
+      far = __builtin_amdgcn_ballot_w64(far_up(m)) != 0;
     }
-    const float up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+    float f = by, up = kWeightBits - (m == -INFINITY ? 0.0f : m);
+    if (far) {
+      const FarScores less(m, f, up);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[t][e] = less(S[t][e]);
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -223,8 +232,8 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void k_attend_tiles(cons
         nv_u4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e], by, up));
-          const float y = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e + 1], by, up));
+          const float x = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e], f, up));
+          const float y = exp2_fast(__builtin_fmaf(S[t][8 * q + 2 * e + 1], f, up));
           l += x + y;
           w[e] = pack_f16(x, y);
         }

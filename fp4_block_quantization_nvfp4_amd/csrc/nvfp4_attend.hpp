@@ -113,6 +113,21 @@ struct Masked {
 NV_DEV float score_scale(float v) { return v >= 0x1p-120f ? v : 0x1p-120f; }
 NV_DEV float query_scale(float factor, float by) { return by == by ? factor : by; }
 
+// A weight is 2^(score * by - m + 11), one multiply-add whose product is not rounded, while m
+// is.  From 2^23 on the two part by half and more, and far up by more than fp16 holds.  Rows with
+// such a maximum take rounded scores, and the difference from m by itself, which is exact near m:
+// scores become fl(score * by) - m for them, and stay for the other rows of the wave.
+NV_DEV bool far_up(float m) { return __builtin_fabsf(m) >= 0x1p23f && __builtin_fabsf(m) < INFINITY; }
+struct FarScores {
+  float mul, sub;
+  NV_DEV FarScores(float m, float& by, float& up) : mul(1.0f), sub(0.0f) {
+    if (!far_up(m)) return;
+    mul = by, sub = m;
+    by = 1.0f, up = kWeightBits;
+  }
+  NV_DEV float operator()(float score) const { return score * mul - sub; }
+};
+
 // log of the sum of exp from the running maximum and the sum of weights.
 NV_DEV float log_sum(float m, float l) { return (float)(kLn2 * ((double)m - kWeightBits + (double)__builtin_amdgcn_logf(l))); }
 

@@ -1,11 +1,13 @@
 """Attention on an NVFP4 cache on the GPU, where a result could pass for another one:
-sequences longer than their row of the table, scores that are not finite."""
+sequences longer than their row of the table, scores that are not finite or very large."""
 import pytest
 import torch
 
 import fp4_block_quantization_nvfp4_amd as nv
+from tests import attention_ref as A
+from tests import layer_ref as R
 from tests.gpu_util import need_gpu
-from tests.test_gpu_attention import filled, gen, randn, tables
+from tests.test_gpu_attention import check_attention, filled, gen, randn, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +108,24 @@ def test_amax_that_is_nan(n, L, D, what):
     assert torch.equal(out[:, :2], want[:, :2]) and torch.equal(lse[:, :2], wl[:, :2])
     assert (out[:first] == 0).all() and (lse[:first] == -INF).all()
     assert torch.isnan(out[first:, 2:]).all() and (what == "v_amax" or torch.isnan(lse[first:, 2:]).all())
+
+
+@pytest.mark.parametrize("by", [1e4, 1e6, 1e8, 1e12, 1e20, 1e30])
+@pytest.mark.parametrize("n,L,D", [(1, 2000, 64), (3, 500, 128), (70, 2000, 128), (150, 700, 64), (90, 300, 256), (16, 40000, 128)])
+def test_very_large_scores(n, L, D, by):
+    """Scores far past 2^24, finite: all the weight is on the largest one (or on those within the rounding of a score)."""
+    g = gen(43)
+    table, pages = tables(g, [L], 64)
+    c = filled(g, pages, 64, 1, D, amax=False)
+    check_attention(randn(g, n, 4, D, by=by).cuda(), c, table, [L], [n], True, what=f"by {by}")
+    # keys of twos, but one of threes: far ahead of the others
+    c.k.fill_(0x44), c.k_scale.fill_(0x38)
+    q = torch.full((n, 4, D), by).bfloat16()
+    j = L // 3
+    c.k[table[0, j // 64], 0, j % 64] = 0x55
+    out, lse = nv.cache_attention(q.cuda(), c, table.cuda(), ints(L), ints(n), causal=False)
+    value = A.cache_values(c.v, c.v_scale)[table[0, j // 64].item(), 0, j % 64]
+    score = R.f64(q)[0, 0, 0] * 3 * D * D ** -0.5
+    # the weight of all the others is 0; the result's rounding, and the weight's own: 2^-11
+    R.assert_near(out, value.expand(n, 4, D), value.abs().expand(n, 4, D) * (2.0 ** -8 + 2.0 ** -11) + 1e-30, "the largest")
+    R.assert_near(lse, score.expand(n, 4), score.expand(n, 4) * 2.0 ** -20, "its score")
