@@ -38,15 +38,11 @@ struct SplitCount {
 
 NV_DEV int min_of(int64_t a, int b) { return a < b ? (int)a : b; }
 
-// The pieces: the waves take as many tiles each, and a unit lies in at most
-// kMostParts pieces (the join takes them one after the other).
-constexpr int kMostParts = 512;
+// The pieces: the waves take as many tiles each (attend_piece_tiles).
 struct Pieces {
   int total, per;
-  NV_DEV Pieces(const SplitCount& count, int total_, int longest, int pieces) : total(total_) {
-    const int even = (total + pieces - 1) / pieces, most = (count.tiles(longest) + kMostParts - 1) / kMostParts;
-    per = even > most ? even : most;
-  }
+  NV_DEV Pieces(const SplitCount& count, int total_, int longest, int pieces)
+      : total(total_), per(attend_piece_tiles(total_, count.tiles(longest), pieces)) {}
   NV_DEV int start(int piece) const { return min_of((int64_t)per * piece, total); }
   // Whether the four pieces of workgroup w lie in the unit of tiles begin .. end - 1.
   NV_DEV bool shared(int w, int begin, int end) const { return start(4 * w) >= begin && start(4 * w + 4) <= end; }

@@ -338,6 +338,14 @@ inline int64_t attend_pieces(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64
   const int64_t n = ceil_div(attend_split_tiles(T, B, Hq, Hk, keys), 4), most = D > 128 ? kAttendPieces / 2 : kAttendPieces;
   return n < most ? n : most;
 }
+// Tiles of a piece, one of `pieces`: of `total` tiles as many each, and so many that a unit of
+// `longest` tiles lies in at most kMostParts pieces (the join takes them one after the other).
+// Unsigned: total may come near 2^31, and total + pieces pass it.
+constexpr int kMostParts = 512;
+constexpr int attend_piece_tiles(uint32_t total, uint32_t longest, uint32_t pieces) {
+  const uint32_t even = (total + pieces - 1) / pieces, most = (longest + kMostParts - 1) / kMostParts;
+  return (int)(even > most ? even : most);
+}
 inline LayerLaunch plan_attend_split(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t keys) {
   return {PLAN_ATTEND_SPLIT, attend_pieces(T, B, Hq, Hk, D, keys), 1, 256};
 }
