@@ -290,9 +290,6 @@ inline int64_t rope_chunks(int64_t T, int64_t rows, int64_t D) {
   const int64_t p = rope_passes(rows, D), c = T > 0 ? ceil_div(4096, T) : 1;
   return c < 1 ? 1 : c < p ? c : p;
 }
-#ifndef RG
-#define RG kNormMaxGrid
-#endif
 // Workgroups: what runs at a time by registers, three waves on a SIMD, of 32-bit rows to the cache
 // two; rows of 16 bits to the outputs, four and little work each, all at once.  Measured, us, all at
 // once (so): 16384 tokens of 8 heads to the cache 24.4 (22.1), 8192 of 40 heads with norm and rotation
