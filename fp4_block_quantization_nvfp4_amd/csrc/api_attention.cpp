@@ -252,17 +252,19 @@ nvfp4_status nvfp4_cache_attention(const nvfp4_heads* q, int64_t T, const nvfp4_
 
 nvfp4_status nvfp4_selftest_attention_plan(int entry, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
                                            int64_t keys, int64_t* plan) {
-  if (entry < 0 || entry > 6) return NVFP4_E_ARG;
+  const bool bf16 = entry < 16;  // 16 and up: of 32-bit rows
+  if (entry < 0 || (bf16 ? entry > 6 : entry > 19)) return NVFP4_E_ARG;
+  entry &= 15;
   if (!plan) return NVFP4_E_NULL;
   if (nvfp4_status st = check_tokens(T, D, entry < 5 ? nvfp4::kRopeMaxD : 256)) return st;
   if (Hq < 0 || Hk < 1 || B < 0 || keys < 16 || (entry >= 5 && (Hq % Hk != 0 || Hq == 0 || D % 32 != 0))) return NVFP4_E_SHAPE;
   if (Hq > kMaxHeads || Hk > kMaxHeads || !fits(Hq * D, T) || !fits(Hk * D, T) || B > kMaxB || keys > kMaxKeys || B * Hk > kMaxUnits) return NVFP4_E_RANGE;
   nvfp4::LayerLaunch p[4] = {};
   if (T != 0) {
-    if (entry == 0) p[0] = nvfp4::plan_rope(T, Hq + Hk, D, true, false);
-    if (entry == 1) p[0] = nvfp4::plan_rope_bwd(T, true), p[1] = nvfp4::plan_rope_sum(D);
-    if (entry == 2) p[0] = nvfp4::plan_rope(T, Hq + 2 * Hk, D, true, true);
-    if (entry == 3) p[0] = nvfp4::plan_rope(T, 2 * Hk, D, true, true);
+    if (entry == 0) p[0] = nvfp4::plan_rope(T, Hq + Hk, D, bf16, false);
+    if (entry == 1) p[0] = nvfp4::plan_rope_bwd(T, bf16), p[1] = nvfp4::plan_rope_sum(D);
+    if (entry == 2) p[0] = nvfp4::plan_rope(T, Hq + 2 * Hk, D, bf16, true);
+    if (entry == 3) p[0] = nvfp4::plan_rope(T, 2 * Hk, D, bf16, true);
     if (entry == 4) p[0] = nvfp4::plan_read_cache(T, Hk, D);
     if (entry >= 5) {
       if (nvfp4::attend_split_tiles(T, B, Hq, Hk, keys) >= int64_t(1) << 31) return NVFP4_E_RANGE;

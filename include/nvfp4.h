@@ -562,8 +562,9 @@ nvfp4_status nvfp4_selftest_layer_plan(int entry, int64_t T, int64_t E, int64_t 
 /*
  * nvfp4_selftest_attention_plan - the same for the operators on a cache.
  *   entry    0 norm_rope, 1 its backward, 2 norm_rope_write, 3 write_cache, 4
- *            read_cache, 5 cache_attention with ends, 6 without.  Hq, Hk: heads of
- *            queries and of keys; keys: width * page_size.
+ *            read_cache, 5 cache_attention with ends, 6 without; of rows in
+ *            bf16, 16 + 0 .. 3 in fp32.  Hq, Hk: heads of queries and of keys;
+ *            keys: width * page_size.
  *   plan     HOST pointer to sixteen int64: {kernel id, workgroups along x, along
  *            y, lanes per workgroup} of up to four launches (zeros: none).
  */
