@@ -31,18 +31,19 @@ def rotary_frequencies(dim, *, base=10000.0, factor=1.0, scaling="none", origina
     "linear"  f_i / factor;
     "base"    base * factor^(dim / (dim - 2)): the slowest pair turns factor times
               slower, the fastest as before;
-    "parts"   pairs that turn more than 32 times in original_length stay, those that
-              turn less than once are divided by factor, a ramp between; the
-              multiplier is 0.1 ln(factor) + 1.
+    "parts"   the YaRN method: pairs that turn more than 32 times in original_length
+              stay, those that turn less than once are divided by factor, a ramp
+              between, from the pair below the one that turns 32 times to the pair
+              above the one that turns once; the multiplier is 0.1 ln(factor) + 1.
     """
     if dim < 0 or dim % 2:
         raise ValueError("dim must be even")
-    if not (base > 0 and factor >= 1):
-        raise ValueError("base > 0 and factor >= 1 are required")
+    if not (0 < base < math.inf and 1 <= factor < math.inf):
+        raise ValueError("base > 0 and factor >= 1, both finite, are required")
     if scaling not in ("none", "linear", "base", "parts"):
         raise ValueError("scaling must be 'none', 'linear', 'base' or 'parts'")
-    if scaling == "parts" and not original_length:
-        raise ValueError("scaling 'parts' needs original_length")
+    if scaling == "parts" and not (base > 1 and original_length and 0 < original_length < math.inf):
+        raise ValueError("scaling 'parts' needs original_length > 0 and base > 1")
     if scaling == "base" and dim > 2:
         base = base * factor ** (dim / (dim - 2))
     f = [base ** (-2 * i / dim) for i in range(dim // 2)]
