@@ -1,5 +1,6 @@
 """Attention on an NVFP4 cache on the GPU, where a result could pass for another one:
-sequences longer than their row of the table, scores that are not finite or very large."""
+sequences longer than their row of the table, scores that are not finite or very large, many
+sequences at a time, one in as many pieces as there may be."""
 import pytest
 import torch
 
@@ -129,3 +130,35 @@ def test_very_large_scores(n, L, D, by):
     # the weight of all the others is 0; the result's rounding, and the weight's own: 2^-11
     R.assert_near(out, value.expand(n, 4, D), value.abs().expand(n, 4, D) * (2.0 ** -8 + 2.0 ** -11) + 1e-30, "the largest")
     R.assert_near(lse, score.expand(n, 4), score.expand(n, 4) * 2.0 ** -20, "its score")
+
+
+# ------------------------------------------------- many sequences, many pieces
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_sequences_of_many_rows(D, causal):
+    """More sequences than are scanned at a time (256), some of more rows than the split kernel takes on both sides of that
+    border and at it, a few of them long enough for their keys to be shared by workgroups; some without queries or keys."""
+    g = gen(44)
+    B = 310
+    n = torch.randint(0, 4, (B,), generator=g)
+    lens = torch.randint(0, 90, (B,), generator=g)
+    for b in (0, 3, 100, 254, 255, 256, 257, 300, 309):
+        n[b] = 66 + b % 7
+        lens[b] = 1900 if b in (3, 255, 256, 309) else 75 + b % 50
+    n[20:30], lens[40:45] = 0, 0
+    table, pages = tables(g, lens.tolist(), 32)
+    c = filled(g, pages, 32, 1, D)
+    ends = torch.cumsum(n, 0)
+    check_attention(randn(g, int(ends[-1]) + 5, 2, D).cuda(), c, table, lens.tolist(), ends.tolist(), causal)
+
+
+@pytest.mark.parametrize("lens", [[70000], [70000, 3], [1, 0, 40000, 129, 33000]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_unit_in_as_many_pieces_as_there_may_be(lens, D):
+    """One head of keys, so long that pieces of an even cut would be more than the 512 that a unit may lie in."""
+    g = gen(45)
+    table, pages = tables(g, lens, 256)
+    c = filled(g, pages, 256, 1, D)
+    check_attention(randn(g, len(lens), 4, D).cuda(), c, table, lens, None, True)
