@@ -131,6 +131,7 @@ def cache_attention(q, cache, table, lens, ends=None, *, scale=None, causal=True
     Queries without keys and those past the last end get 0 and -inf; NaN those that
     see a key of a page that is not in the cache or with a NaN among its scales or its
     value's, and all of a sequence with more keys than its row of the table names.
-    scale > 0, D ** -0.5 by default."""
+    scale > 0, D ** -0.5 by default.  The same call gives the same bits; the last ones
+    may change with the other sequences and the table's width."""
     return _n.cache_attention(q, cache.k, cache.k_scale, cache.v, cache.v_scale, cache.k_amax, cache.v_amax, table, lens, ends,
                               scale, causal)

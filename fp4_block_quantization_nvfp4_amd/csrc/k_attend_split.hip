@@ -17,7 +17,7 @@
 // memory (turned by the load).  Waves wait for each other only at the end, where all
 // four of a workgroup lie in one unit: their sums meet in shared memory.
 //
-// 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 79 us and 7 for the join, 4.3
+// 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 80 us and 7 for the join, 4.3
 // TB/s of the 5.1 that a large copy reaches; two of up to 131072 keys 47 and 8.  What is
 // left is the start (scan of the sequences, page numbers, first keys: 4 us, one after the
 // other) and the two launches; the vector pipes are busy half of the time, decoding

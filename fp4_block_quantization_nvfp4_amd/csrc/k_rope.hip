@@ -40,7 +40,7 @@ NV_DEV SinCos sincos64(double a) {
   double r = __builtin_fma(-n, scalar(0x1.921fb54442d18p+0), a);       // pi / 2, the first 53 bits: the product's own bits are kept
   r = __builtin_fma(-n, scalar(0x1.1a62633145c07p-54), r);              // and the next 53
   const double q = r * r;
-  // Taylor's series on |r| <= pi / 4: the first term left out is below 5e-17 (sine), 3e-18 (cosine)
+  // Taylor's series on |r| <= pi / 4: the first term left out is below 1e-19 (sine, r^19 / 19!), 3e-18 (cosine, r^18 / 18!)
   double s = scalar(1.0 / 355687428096000.0);
   s = __builtin_fma(s, q, scalar(-1.0 / 1307674368000.0));
   s = __builtin_fma(s, q, scalar(1.0 / 6227020800.0));
@@ -196,11 +196,12 @@ struct Row {
   int h, e0, e1;
 };
 
-// The next row is on its way while one is used (16384 tokens to the cache, 8 heads of
-// 128: 29 -> 25 us, 22 with a grid of what runs at a time; 8192 with norm and rotation: 60 ->
-// 50, 47).  (Over the end of a token too, as the gradient has it: 170 registers, 27 and 59 us.)  Of 16-bit rows that go to
-// the outputs, registers for four waves on a SIMD (8192 tokens, 40 heads of 128: 36.5 ->
-// 34.3 us; 32-bit ones then spill: 21 -> 26 at 20 heads of 64).
+// The next row is on its way while one is used, within a token.  Measured, us, without and with
+// it: 16384 tokens of 8 heads of 128 to the cache 29 and 25, 8192 of 40 heads with norm and
+// rotation 60 and 50; the grid of what runs at a time (rope_groups) takes these to 23 and 49.
+// Over the end of a token too, as the gradient has it, costs 170 registers: 27 and 59.
+// 16-bit rows that go to the outputs have registers for four waves on a SIMD: 8192 tokens of 40
+// heads of 128 36.5 -> 34.3.  32-bit rows spill with so few: 20 heads of 64 21 -> 26.
 template <typename T, int LN, bool INTER, bool CACHE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_rope(const RopeArgs a, int chunks, int per) {
   constexpr int RW = 64 / LN;
@@ -301,8 +302,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !CACHE ? 4 : 2) void k_norm_
 
 // A wave has tokens in turn and keeps its sums of dw in registers over all of them; a
 // workgroup's four meet in shared memory, and a second kernel adds the workgroups' in order.
-// 8192 tokens, 40 heads of 128, bf16: 51 to 54 us with the second kernel's 4.7, 252 MB at
-// 5.1 to 5.4 TB/s.  Bound by memory; three waves on a SIMD (two, 32-bit rows), each with its next rows on
+// 8192 tokens, 40 heads of 128, bf16: called by itself over and over, 51 to 54 us with the second
+// kernel's 4.7, 252 MB at 4.7 to 4.9 TB/s, a part of them still in the last cache; behind the forward
+// pass 57 + 5.  Bound by memory; three waves on a SIMD (two, 32-bit rows), each with its next rows on
 // their way, also over the end of a token, are all of the grid.
 template <typename T, int LN, bool INTER>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_norm_rope_bwd(const RopeArgs a, const HeadsView dq, const HeadsView dk, float* __restrict__ partial) {

@@ -355,9 +355,10 @@ inline size_t attend_split_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, i
 // enough units and heads over 64 (two prompts of 8192, 32 heads of 128: 705 -> 655 us; 4 of 4096, 16 heads
 // of 64: 120 -> 139).
 // parts: workgroups that share a unit's keys, in pieces of kAttendLeast tiles of 64 or more, where
-// units alone would not fill the chip's 512 places twice (512 queries behind 32768 keys: 870 us
-// whole, 350 in parts; pieces of four tiles instead of eight, which a piece's start and sums
-// cost more than: 43 -> 50 us, 7 sequences of up to 301 queries and 1999 keys).
+// units alone would not make 1024 workgroups: twice what runs at a time with four waves (two on a
+// CU, three of heads up to 64, one of heads over 128), four times with eight (one on a CU).  512 queries behind 32768
+// keys: 870 us whole, 350 in parts; pieces of four tiles instead of eight, which a piece's start and
+// sums cost more than: 43 -> 50 us, 7 sequences of up to 301 queries and 1999 keys.
 constexpr int kAttendLeast = 8;
 struct TilesPlan {
   int waves, parts;

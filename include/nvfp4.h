@@ -486,7 +486,9 @@ nvfp4_status nvfp4_read_cache(const nvfp4_cache* cache, const int32_t* slots, in
  * least 0.  A query that sees a key whose page is not in the cache, or one with a
  * NaN among its scales or its value's, and every one of a sequence longer than width *
  * page_size, gets NaN in its whole row and lse; one that does not see it has none of
- * it.  width >= 1, scale > 0.  Sums have a fixed order.  Further limits (NVFP4_E_RANGE): B <= 2^20, B * heads
+ * it.  width >= 1, scale > 0.  Sums have a fixed order: the same call gives the same bits.  Where keys are cut
+ * goes by T, B, width * page_size and all lengths, so a sequence's last bits may change with what
+ * comes beside it or with a wider table.  Further limits (NVFP4_E_RANGE): B <= 2^20, B * heads
  * <= 2^22, width * page_size <= 2^30, and B * max(8, ceil(G / 16)) * heads *
  * ceil(width * page_size / 64) + ceil(T * G / 16) * heads < 2^31, G = q->heads /
  * heads.  workspace: at least
