@@ -3,7 +3,7 @@
 // in k_attend_split.hip.
 //
 // Bound by what a wave does between the matrix instructions, which are at work 44% of
-// the time (two prompts of 3201 and 8192 tokens, 32 heads on 8 of 128: 657 to 669 us, 950 to 965
+// the time (two prompts of 3201 and 8192 tokens, 32 heads on 8 of 128: 657 to 669 us, 945 to 965
 // TFLOP/s of the 1300 that a large bf16 product reaches), and by shared memory, which they read for a
 // third of it.  A unit is
 // 32 rows a wave (queries, and heads that share keys) of one sequence and shared
