@@ -10,10 +10,10 @@
 // Weights exp(s - max) are rounded to fp16 times 2^11, the maximum being one that
 // may lie up to 2^4 below the row's, so that sums are rescaled seldom: they keep 11
 // bits down to 2^-25 (a bf16 result has 8), and below are off by 2^-36 of the
-// largest at most.  Their sum is taken before that rounding.  It adds 0.3 to 0.7% to the
-// result's error, 1.64e-3 instead of 1.63e-3 of its size, which is bf16's own rounding.
-// Weights in two fp16, the second of what the first leaves, add nothing; the products that
-// takes cost two prompts of 8192 tokens 657 -> 876 us, decoding 87.5 -> 91.5, two long sequences
+// largest at most.  Their sum is taken before that rounding, which adds 0.3 to 0.7% to the
+// result's error: 1.64e-3 of its size for one sequence, 1.63e-3 of which is bf16's own rounding.
+// Weights in two fp16, the second holding what the first leaves, add nothing, but their products
+// cost two prompts of 8192 tokens 657 -> 876 us, decoding 87.5 -> 91.5, two long sequences
 // 54.5 -> 58.6, an encoder's states 34.8 -> 36.2.
 #pragma once
 
