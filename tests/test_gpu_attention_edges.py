@@ -1,6 +1,6 @@
 """Attention on an NVFP4 cache on the GPU, where a result could pass for another one:
 sequences longer than their row of the table, scores that are not finite or very large, many
-sequences at a time, one in as many pieces as there may be."""
+sequences at a time, one in as many pieces as there may be, no pages and the largest."""
 import pytest
 import torch
 
@@ -162,3 +162,41 @@ def test_a_unit_in_as_many_pieces_as_there_may_be(lens, D):
     table, pages = tables(g, lens, 256)
     c = filled(g, pages, 256, 1, D)
     check_attention(randn(g, len(lens), 4, D).cuda(), c, table, lens, None, True)
+
+
+# ------------------------------------------------- the smallest and the largest
+
+
+def test_a_cache_without_pages():
+    """Nothing is written, zeros are read, and sequences have no keys, or NaN for keys of pages that are not there."""
+    c = nv.PagedCache.empty(0, 16, 2, 64)
+    x = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    nv.write_cache(c, x, x, ints(0, 1, -1, 1 << 20))
+    for t in nv.read_cache(c, ints(0, 5, -1)):
+        assert t.shape == (3, 2, 64) and (t == 0).all()
+    table = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    out, lse = nv.cache_attention(x, c, table, ints(0, 3, 0, 32))
+    assert (out[::2] == 0).all() and (lse[::2] == -INF).all() and torch.isnan(out[1::2]).all() and torch.isnan(lse[1::2]).all()
+    many = torch.ones(90, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = nv.cache_attention(many, c, table[:2], ints(0, 30), ints(40, 90), causal=False)
+    assert (out[:40] == 0).all() and (lse[:40] == -INF).all() and torch.isnan(out[40:]).all() and torch.isnan(lse[40:]).all()
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_the_largest_pages(n):
+    """65536 slots a page, a sequence that goes on in a second one."""
+    g = gen(46)
+    lens = [65536 + 200, 65535]
+    table, pages = tables(g, lens, 65536)
+    c = filled(g, pages, 65536, 2, 32)
+    ends = None if n == 1 else [n, 2 * n]
+    check_attention(randn(g, 2 * n, 4, 32).cuda(), c, table, lens, ends, True)
+
+
+def test_many_heads_of_keys():
+    g = gen(47)
+    lens = [5, 0, 33, 70]
+    table, pages = tables(g, lens, 16)
+    c = filled(g, pages, 16, 1000, 32)
+    check_attention(randn(g, 4, 1000, 32).cuda(), c, table, lens, None, True)
+    check_attention(randn(g, 140, 1000, 32).cuda(), c, table, lens, [1, 60, 100, 139], True)
